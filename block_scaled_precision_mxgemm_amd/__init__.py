@@ -20,6 +20,14 @@ _BINDING_NAMES = (
     "mxgemm_epilogue",
     "fp16gemm_run",
     "mxgemm_run_dequant_fp16",
+    "int8gemm_quantize",
+    "int8gemm_run",
+    "int8gemm_run_grouped",
+    "expert_route",
+    "expert_route_backward",
+    "expert_plan",
+    "expert_combine",
+    "expert_combine_backward",
     "mxgemm_mfma_ceiling",
     "mxgemm_device_supported",
     "MXGemmError",
@@ -46,6 +54,9 @@ _BINDING_NAMES = (
     "ACT_NONE",
     "ACT_GELU",
     "CEIL_FP16",
+    "SCORE_SOFTMAX",
+    "SCORE_SIGMOID",
+    "INT8_MAX_K",
     "library_path",
 )
 

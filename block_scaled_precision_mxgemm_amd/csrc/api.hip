@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include "../../include/mxgemm.h"
+#include "mxg_int8.h"
 #include "mxg_internal.h"
 
 namespace {
@@ -104,8 +105,43 @@ int run_mx(const void* A, const uint8_t* SA, const void* B, const uint8_t* SB, c
   return to_status(mxg::launch_mx_tiled(A, SA, B, SB, e, M, N, K, fmt, st));
 }
 
+bool type_ok(int t) { return t == MXG_OUT_F32 || t == MXG_OUT_BF16 || t == MXG_OUT_F16; }
+
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+// start of a row of elements that the kernels may also read one by one
+bool aligned_elem(const void* p, int type) { return ((uintptr_t)p & (type == MXG_OUT_F32 ? 3u : 1u)) == 0; }
+
+// int8 products: validated arguments of the dense and the expert form
+int run_int8(const mxg::I8Args& a, const float* bias, int act, int out_type, hipStream_t st) {
+  if (!a.A || !a.SA || !a.B || !a.SB || !a.e.C) return MXG_EINVAL;
+  if (a.N < 1 || a.K < 16 || (a.K % 16) != 0 || a.K > MXG_INT8_MAX_K) return MXG_EINVAL;
+  if (!aligned16(a.A) || !aligned16(a.B) || !aligned16(a.e.C) || !aligned16(a.SB)) return MXG_EALIGN;
+  if (!aligned4(a.SA) || !aligned4(a.offsets) || !aligned4(a.index)) return MXG_EALIGN;
+  int s = validate_epi(bias, act, out_type);
+  if (s != MXG_OK) return s;
+  s = check_device();
+  if (s != MXG_OK) return s;
+  return to_status(mxg::launch_int8(a, st));
+}
+
+int validate_route(const void* logits, int in_type, int64_t T, int64_t E, int k, int score) {
+  if (!logits || !type_ok(in_type) || !dim_ok(T)) return MXG_EINVAL;
+  if (E < 1 || E > MXG_MAX_EXPERTS || k < 1 || k > MXG_MAX_CHOICES || k > E) return MXG_EINVAL;
+  if (score != MXG_SCORE_SOFTMAX && score != MXG_SCORE_SIGMOID) return MXG_EINVAL;
+  return aligned_elem(logits, in_type) ? MXG_OK : MXG_EALIGN;
+}
+
+int validate_combine(const mxg::CombineArgs& a, int y_type, int out_type) {
+  if (!a.Y || !a.position || !a.weights || !a.out || !type_ok(y_type) || !type_ok(out_type)) return MXG_EINVAL;
+  if (!dim_ok(a.N) || !dim_ok(a.T) || a.k < 1 || a.k > MXG_MAX_CHOICES) return MXG_EINVAL;
+  if (a.rows < 1 || a.rows > MXG_MAX_SLOTS) return MXG_EINVAL;
+  if (!aligned16(a.Y) || !aligned16(a.out) || !aligned4(a.position) || !aligned4(a.weights)) return MXG_EALIGN;
+  return MXG_OK;
+}
+
 static_assert(MXG_OUT_F32 == mxg::kOutF32 && MXG_OUT_BF16 == mxg::kOutBF16 && MXG_OUT_F16 == mxg::kOutF16,
               "output type ids");
+static_assert(MXG_SCORE_SOFTMAX == mxg::kScoreSoftmax && MXG_SCORE_SIGMOID == mxg::kScoreSigmoid, "score ids");
 static_assert(MXG_ACT_NONE == mxg::kActNone && MXG_ACT_GELU == mxg::kActGelu, "activation ids");
 static_assert(MXG_ELEM_E4M3 == mxg::kFmtFp8 && MXG_ELEM_E5M2 == mxg::kFmtBf8 && MXG_ELEM_E2M1 == mxg::kFmtFp4,
               "element ids are the MFMA format ids");
@@ -206,6 +242,108 @@ int mxgemm_run_dequant_fp16(const void* A, const uint8_t* scaleA, const void* B,
   s = check_device();
   if (s != MXG_OK) return s;
   return to_status(mxg::launch_deq_tiled(A, scaleA, B, scaleB, C, M, N, K, (hipStream_t)stream));
+}
+
+int int8gemm_quantize(const void* X, int in_type, int64_t rows, int64_t K, int8_t* Q, float* S, void* stream) {
+  if (!X || !Q || !S || !type_ok(in_type)) return MXG_EINVAL;
+  if (!dim_ok(rows) || !dim_ok(K) || (K % 16) != 0) return MXG_EINVAL;
+  if (!aligned16(X) || !aligned16(Q) || !aligned4(S)) return MXG_EALIGN;
+  const int d = check_device();
+  if (d != MXG_OK) return d;
+  return to_status(mxg::launch_quantize_int8(X, in_type, rows, K, Q, S, (hipStream_t)stream));
+}
+
+int int8gemm_run(const int8_t* A, const float* scaleA, const int8_t* B, const float* scaleB, void* C, int64_t M,
+                 int64_t N, int64_t K, const float* bias, int act, int out_type, void* stream) {
+  if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return MXG_EINVAL;
+  return run_int8(mxg::I8Args{A, scaleA, M, B, scaleB, mxg::Epi{C, bias, out_type, act}, M, (int)N, (int)K, 1, nullptr,
+                              nullptr, 1},
+                  bias, act, out_type, (hipStream_t)stream);
+}
+
+int int8gemm_run_grouped(const int8_t* A, const float* scaleA, int64_t rowsA, const int8_t* B, const float* scaleB,
+                         void* C, int64_t rows, int64_t N, int64_t K, int64_t E, const int32_t* offsets,
+                         const int32_t* index, int index_div, const float* bias, int act, int out_type,
+                         void* stream) {
+  if (!offsets || rows < 1 || rows > MXG_MAX_SLOTS || rowsA < 1 || rowsA > MXG_MAX_SLOTS) return MXG_EINVAL;
+  if (!dim_ok(N) || !dim_ok(K) || E < 1 || E > MXG_MAX_EXPERTS || index_div < 1) return MXG_EINVAL;
+  if (index == nullptr && rowsA < rows) return MXG_EINVAL;
+  return run_int8(mxg::I8Args{A, scaleA, rowsA, B, scaleB, mxg::Epi{C, bias, out_type, act}, rows, (int)N, (int)K,
+                              (int)E, offsets, index, index_div},
+                  bias, act, out_type, (hipStream_t)stream);
+}
+
+int expert_route(const void* logits, int in_type, int64_t T, int64_t E, int k, int score, const float* bias, int groups,
+                 int top_groups, int group_top, int renormalize, float scale, int32_t* ids, float* weights,
+                 void* stream) {
+  int s = validate_route(logits, in_type, T, E, k, score);
+  if (s != MXG_OK) return s;
+  if (!ids || !weights || (renormalize != 0 && renormalize != 1)) return MXG_EINVAL;
+  if (groups < 1 || groups > MXG_MAX_GROUPS || E % groups != 0 || top_groups < 1 || top_groups > groups)
+    return MXG_EINVAL;
+  if (group_top != 1 && group_top != 2) return MXG_EINVAL;
+  if (E / groups * top_groups < k) return MXG_EINVAL;
+  if (!aligned4(bias) || !aligned4(ids) || !aligned4(weights)) return MXG_EALIGN;
+  s = check_device();
+  if (s != MXG_OK) return s;
+  return to_status(mxg::launch_route(mxg::RouteArgs{logits, bias, T, (int)E, k, score, groups, top_groups, group_top,
+                                                    renormalize, scale, ids, weights},
+                                     in_type, (hipStream_t)stream));
+}
+
+int expert_route_backward(const void* logits, int in_type, int64_t T, int64_t E, const int32_t* ids,
+                          const float* d_weights, int k, int score, int renormalize, float scale, void* d_logits,
+                          void* stream) {
+  int s = validate_route(logits, in_type, T, E, k, score);
+  if (s != MXG_OK) return s;
+  if (!ids || !d_weights || !d_logits || (renormalize != 0 && renormalize != 1)) return MXG_EINVAL;
+  if (!aligned4(ids) || !aligned4(d_weights) || !aligned_elem(d_logits, in_type)) return MXG_EALIGN;
+  s = check_device();
+  if (s != MXG_OK) return s;
+  return to_status(mxg::launch_route_backward(mxg::RouteArgs{logits, nullptr, T, (int)E, k, score, 1, 1, 1,
+                                                             renormalize, scale, const_cast<int32_t*>(ids), nullptr},
+                                              in_type, d_weights, d_logits, (hipStream_t)stream));
+}
+
+int64_t expert_plan_workspace(int64_t T, int k, int64_t E) {
+  if (!dim_ok(T) || k < 1 || k > MXG_MAX_CHOICES || E < 1 || E > MXG_MAX_EXPERTS) return -1;
+  return mxg::plan_workspace(T * k, (int)E);
+}
+
+int expert_plan(const int32_t* ids, int64_t T, int k, int64_t E, int32_t* offsets, int32_t* order, int32_t* position,
+                void* workspace, void* stream) {
+  if (!ids || !offsets || !order || !position) return MXG_EINVAL;
+  const int64_t need = expert_plan_workspace(T, k, E);
+  if (need < 0 || (need > 0 && !workspace)) return MXG_EINVAL;
+  if (!aligned4(ids) || !aligned4(offsets) || !aligned4(order) || !aligned4(position) || !aligned4(workspace))
+    return MXG_EALIGN;
+  const int d = check_device();
+  if (d != MXG_OK) return d;
+  return to_status(
+      mxg::launch_plan(ids, T * k, (int)E, offsets, order, position, workspace, (hipStream_t)stream));
+}
+
+int expert_combine(const void* Y, int y_type, int64_t rows, int64_t N, const int32_t* position, const float* weights,
+                   int64_t T, int k, void* out, int out_type, void* stream) {
+  const mxg::CombineArgs a{Y, rows, N, position, weights, T, k, out};
+  const int s = validate_combine(a, y_type, out_type);
+  if (s != MXG_OK) return s;
+  const int d = check_device();
+  if (d != MXG_OK) return d;
+  return to_status(mxg::launch_combine(a, y_type, out_type, (hipStream_t)stream));
+}
+
+int expert_combine_backward(const void* dOut, int out_type, const void* Y, int y_type, int64_t rows, int64_t N,
+                            const int32_t* position, const float* weights, int64_t T, int k, void* dY, float* dW,
+                            void* stream) {
+  const mxg::CombineArgs a{Y, rows, N, position, weights, T, k, const_cast<void*>(dOut)};
+  const int s = validate_combine(a, y_type, out_type);
+  if (s != MXG_OK) return s;
+  if (!dY || !dW) return MXG_EINVAL;
+  if (!aligned16(dY) || !aligned4(dW)) return MXG_EALIGN;
+  const int d = check_device();
+  if (d != MXG_OK) return d;
+  return to_status(mxg::launch_combine_backward(a, y_type, out_type, dY, dW, (hipStream_t)stream));
 }
 
 }  // extern "C"

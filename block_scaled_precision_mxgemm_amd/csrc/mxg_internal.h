@@ -62,4 +62,48 @@ hipError_t launch_epilogue(const float* X, int64_t M, int64_t N, const Epi& e, h
 // Largest M served by the split-K streaming kernel.
 constexpr int64_t kSkinnyMaxM = 64;
 
+// Rows of `in_type` (kOut* ids) to int8 codes with one fp32 scale per row.
+hipError_t launch_quantize_int8(const void* X, int in_type, int64_t rows, int64_t K, int8_t* Q, float* S,
+                                hipStream_t stream);
+// int8 product, dense or by expert (I8Args in mxg_int8.h).
+struct I8Args;
+hipError_t launch_int8(const I8Args& a, hipStream_t stream);
+
+constexpr int kScoreSoftmax = 0;
+constexpr int kScoreSigmoid = 1;
+
+// Routing of T tokens to k of E experts (logits T x E of a kOut* type).
+struct RouteArgs {
+  const void* logits;
+  const float* bias;  // E, or nullptr
+  int64_t T;
+  int E, k;
+  int score, groups, top_groups, group_top, renormalize;
+  float scale;
+  int32_t* ids;    // T x k (read by the gradient)
+  float* weights;  // T x k
+};
+hipError_t launch_route(const RouteArgs& a, int in_type, hipStream_t stream);
+hipError_t launch_route_backward(const RouteArgs& a, int in_type, const float* d_w, void* d_logits,
+                                 hipStream_t stream);
+// Stable sort of the n slots by expert; `workspace`: plan_workspace(n, E) bytes.
+int64_t plan_workspace(int64_t n, int E);
+hipError_t launch_plan(const int32_t* ids, int64_t n, int E, int32_t* offsets, int32_t* order, int32_t* position,
+                       void* workspace, hipStream_t stream);
+
+// Weighted sum of k rows of Y (rows x N) per token; `out` is T x N (the
+// gradient reads it as the gradient of the sums).
+struct CombineArgs {
+  const void* Y;
+  int64_t rows, N;
+  const int32_t* position;  // T x k
+  const float* weights;     // T x k
+  int64_t T;
+  int k;
+  void* out;
+};
+hipError_t launch_combine(const CombineArgs& a, int y_type, int out_type, hipStream_t stream);
+hipError_t launch_combine_backward(const CombineArgs& a, int y_type, int out_type, void* dY, float* dW,
+                                   hipStream_t stream);
+
 }  // namespace mxg

@@ -44,7 +44,12 @@ ACT_NONE = 0
 ACT_GELU = 1
 # kind of mxgemm_mfma_ceiling beside the FMT_* pairs
 CEIL_FP16 = 16
+# scores of expert_route (MXG_SCORE_*) and the largest K of an int8 product
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+INT8_MAX_K = 131056
 _OUT_DTYPES = {OUT_F32: torch.float32, OUT_BF16: torch.bfloat16, OUT_F16: torch.float16}
+_DTYPE_IDS = {t: i for i, t in _OUT_DTYPES.items()}
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxgemm.so")
 
@@ -81,6 +86,20 @@ def _load():
     lib.fp16gemm_run.restype = ci
     lib.mxgemm_mfma_ceiling.argtypes = [p, i64, p, i64, ci, i64, ci, p, p, p]
     lib.mxgemm_mfma_ceiling.restype = ci
+    cf = ctypes.c_float
+    lib.int8gemm_quantize.argtypes = [p, ci, i64, i64, p, p, p]
+    lib.int8gemm_run.argtypes = [p, p, p, p, p, i64, i64, i64, p, ci, ci, p]
+    lib.int8gemm_run_grouped.argtypes = [p, p, i64, p, p, p, i64, i64, i64, i64, p, p, ci, p, ci, ci, p]
+    lib.expert_route.argtypes = [p, ci, i64, i64, ci, ci, p, ci, ci, ci, ci, cf, p, p, p]
+    lib.expert_route_backward.argtypes = [p, ci, i64, i64, p, p, ci, ci, ci, cf, p, p]
+    lib.expert_plan.argtypes = [p, i64, ci, i64, p, p, p, p, p]
+    lib.expert_combine.argtypes = [p, ci, i64, i64, p, p, i64, ci, p, ci, p]
+    lib.expert_combine_backward.argtypes = [p, ci, p, ci, i64, i64, p, p, i64, ci, p, p, p]
+    for name in ("int8gemm_quantize", "int8gemm_run", "int8gemm_run_grouped", "expert_route", "expert_route_backward",
+                 "expert_plan", "expert_combine", "expert_combine_backward"):
+        getattr(lib, name).restype = ci
+    lib.expert_plan_workspace.argtypes = [i64, ci, i64]
+    lib.expert_plan_workspace.restype = i64
     lib.mxgemm_device_supported.argtypes = []
     lib.mxgemm_device_supported.restype = ci
     lib.mxgemm_status_string.argtypes = [ci]
@@ -279,6 +298,213 @@ def mxgemm_mfma_ceiling(ops: torch.Tensor, scales: torch.Tensor | None, kind: in
                                      None if clocks is None else clocks.data_ptr(), _stream(stream))
     _check(rc, "mxgemm_mfma_ceiling")
     return out
+
+
+# ---- int8 products and experts ----------------------------------------------
+
+
+def _arg(t, name: str, dtypes, shape=None, dim: int | None = None, like: torch.Tensor | None = None) -> torch.Tensor:
+    """A contiguous GPU tensor of one of `dtypes`, of the shape or number of
+    dimensions given, on the device of `like`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(name + " must be a GPU tensor")
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, not %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if dim is not None and t.dim() != dim:
+        raise ValueError("%s must have %d dimensions" % (name, dim))
+    if not t.is_contiguous():
+        raise ValueError(name + " must be contiguous")
+    if like is not None and t.device != like.device:
+        raise ValueError("%s is on %s, the other operands on %s" % (name, t.device, like.device))
+    return t
+
+
+def _out(t, name: str, dtype, shape, like: torch.Tensor) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _arg(t, name, (dtype,), shape, like=like)
+
+
+_FLOATS = tuple(_DTYPE_IDS)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name: str, device: torch.device, stream, *args):
+    """An entry point on the operands' own device; without a stream, on that
+    device's current one."""
+    with torch.cuda.device(device):
+        _check(getattr(_load(), name)(*args, _stream(stream)), name)
+
+
+def int8gemm_quantize(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tensor | None = None, stream=None):
+    """Quantize rows (rows x K of float32, bfloat16 or float16, K a multiple of
+    16) to (int8 codes, fp32 scale per row): tokens, or the N x K weights of a
+    layer with a scale per output channel."""
+    x = _arg(x, "x", _FLOATS, dim=2)
+    rows, K = x.shape
+    q = _out(q, "q", torch.int8, (rows, K), x)
+    s = _out(s, "s", torch.float32, (rows,), x)
+    _call("int8gemm_quantize", x.device, stream, x.data_ptr(), _DTYPE_IDS[x.dtype], rows, K, q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def int8gemm_run(a_q, a_s, b_q, b_s, bias: torch.Tensor | None = None, act: int = ACT_NONE, out_type: int = OUT_F32,
+                 out: torch.Tensor | None = None, stream=None):
+    """C = out_type(act(a_s[i] b_s[j] sum_k a_q[i][k] b_q[j][k] + bias[j])); a_q: M x K,
+    b_q: N x K int8; a_s: M, b_s: N float32 scales per token and per channel."""
+    if out_type not in _OUT_DTYPES:
+        raise ValueError("unknown out_type %r" % (out_type,))
+    a_q = _arg(a_q, "a_q", (torch.int8,), dim=2)
+    M, K = a_q.shape
+    b_q = _arg(b_q, "b_q", (torch.int8,), dim=2, like=a_q)
+    N = b_q.shape[0]
+    if b_q.shape[1] != K:
+        raise ValueError("inner dimensions disagree: a_q %s, b_q %s" % (tuple(a_q.shape), tuple(b_q.shape)))
+    a_s = _arg(a_s, "a_s", (torch.float32,), (M,), like=a_q)
+    b_s = _arg(b_s, "b_s", (torch.float32,), (N,), like=a_q)
+    if bias is not None:
+        bias = _arg(bias, "bias", (torch.float32,), (N,), like=a_q)
+    out = _out(out, "out", _OUT_DTYPES[out_type], (M, N), a_q)
+    _call("int8gemm_run", a_q.device, stream, a_q.data_ptr(), a_s.data_ptr(), b_q.data_ptr(), b_s.data_ptr(),
+          out.data_ptr(), M, N, K, _ptr(bias), act, out_type)
+    return out
+
+
+def int8gemm_run_grouped(a_q, a_s, b_q, b_s, offsets, index: torch.Tensor | None = None, index_div: int = 1,
+                         bias: torch.Tensor | None = None, act: int = ACT_NONE, out_type: int = OUT_F32,
+                         out: torch.Tensor | None = None, stream=None):
+    """The products of E experts: rows offsets[e] .. offsets[e+1]-1 of the result
+    with b_q[e] (E x N x K), b_s[e] and bias[e] (E x N).  Row p takes row
+    index[p] // index_div of a_q, or row p without an index.  offsets (E + 1)
+    and index are int32 tensors, as expert_plan gives them.  Rows outside the
+    offsets are left as they were; without `out` they hold nothing defined."""
+    if out_type not in _OUT_DTYPES:
+        raise ValueError("unknown out_type %r" % (out_type,))
+    a_q = _arg(a_q, "a_q", (torch.int8,), dim=2)
+    rows_a, K = a_q.shape
+    b_q = _arg(b_q, "b_q", (torch.int8,), dim=3, like=a_q)
+    E, N = b_q.shape[:2]
+    if b_q.shape[2] != K:
+        raise ValueError("inner dimensions disagree: a_q %s, b_q %s" % (tuple(a_q.shape), tuple(b_q.shape)))
+    a_s = _arg(a_s, "a_s", (torch.float32,), (rows_a,), like=a_q)
+    b_s = _arg(b_s, "b_s", (torch.float32,), (E, N), like=a_q)
+    offsets = _arg(offsets, "offsets", (torch.int32,), (E + 1,), like=a_q)
+    rows = rows_a
+    if index is not None:
+        index = _arg(index, "index", (torch.int32,), dim=1, like=a_q)
+        rows = index.shape[0]
+    if bias is not None:
+        bias = _arg(bias, "bias", (torch.float32,), (E, N), like=a_q)
+    out = _out(out, "out", _OUT_DTYPES[out_type], (rows, N), a_q)
+    _call("int8gemm_run_grouped", a_q.device, stream, a_q.data_ptr(), a_s.data_ptr(), rows_a, b_q.data_ptr(),
+          b_s.data_ptr(), out.data_ptr(), rows, N, K, E, offsets.data_ptr(), _ptr(index), index_div, _ptr(bias), act,
+          out_type)
+    return out
+
+
+def expert_route(logits, k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor | None = None, groups: int = 1,
+                 top_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+                 ids: torch.Tensor | None = None, weights: torch.Tensor | None = None, stream=None):
+    """The k experts of each token (T x E logits) and their weights: (ids T x k
+    int32, weights T x k float32).  bias (E float32) counts for the choice
+    alone; with groups > 1 only the top_groups groups with the largest sum of
+    their group_top largest scores are chosen from.  Experts with a logit of
+    -inf are not chosen; missing choices are -1 with weight 0."""
+    logits = _arg(logits, "logits", _FLOATS, dim=2)
+    T, E = logits.shape
+    if bias is not None:
+        bias = _arg(bias, "bias", (torch.float32,), (E,), like=logits)
+    if not 1 <= k <= E:
+        raise ValueError("k must be 1 .. %d" % E)
+    ids = _out(ids, "ids", torch.int32, (T, k), logits)
+    weights = _out(weights, "weights", torch.float32, (T, k), logits)
+    _call("expert_route", logits.device, stream, logits.data_ptr(), _DTYPE_IDS[logits.dtype], T, E, k, score, _ptr(bias),
+          groups, top_groups, group_top, int(renormalize), scale, ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def expert_route_backward(logits, ids, d_weights, score: int = SCORE_SOFTMAX, renormalize: bool = True,
+                          scale: float = 1.0, d_logits: torch.Tensor | None = None, stream=None):
+    """Gradient of the logits (T x E, in their type) from that of expert_route's
+    weights (T x k float32), the choice `ids` held."""
+    logits = _arg(logits, "logits", _FLOATS, dim=2)
+    T, E = logits.shape
+    ids = _arg(ids, "ids", (torch.int32,), dim=2, like=logits)
+    k = ids.shape[1]
+    if ids.shape[0] != T:
+        raise ValueError("ids must have %d rows" % T)
+    d_weights = _arg(d_weights, "d_weights", (torch.float32,), (T, k), like=logits)
+    d_logits = _out(d_logits, "d_logits", logits.dtype, (T, E), logits)
+    _call("expert_route_backward", logits.device, stream, logits.data_ptr(), _DTYPE_IDS[logits.dtype], T, E,
+          ids.data_ptr(), d_weights.data_ptr(), k, score, int(renormalize), scale, d_logits.data_ptr())
+    return d_logits
+
+
+def expert_plan(ids, experts: int, offsets: torch.Tensor | None = None, order: torch.Tensor | None = None,
+                position: torch.Tensor | None = None, stream=None):
+    """Slots (token * k + choice) sorted by expert, from ids (T x k int32; values
+    outside 0 .. experts-1 are slots without an expert): (offsets E + 1, order
+    T * k, position T x k), int32.  order[p] is the slot in row p, -1 behind the
+    last expert's rows; position[t][j] is the slot's row, or -1."""
+    ids = _arg(ids, "ids", (torch.int32,), dim=2)
+    T, k = ids.shape
+    lib = _load()
+    need = lib.expert_plan_workspace(T, k, experts)
+    if need < 0:
+        _check(1, "expert_plan")
+    offsets = _out(offsets, "offsets", torch.int32, (experts + 1,), ids)
+    order = _out(order, "order", torch.int32, (T * k,), ids)
+    position = _out(position, "position", torch.int32, (T, k), ids)
+    workspace = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+    if workspace is not None and stream is not None:
+        workspace.record_stream(stream)
+    _call("expert_plan", ids.device, stream, ids.data_ptr(), T, k, experts, offsets.data_ptr(), order.data_ptr(),
+          position.data_ptr(), _ptr(workspace))
+    return offsets, order, position
+
+
+def _combine_args(y, position, weights):
+    y = _arg(y, "y", _FLOATS, dim=2)
+    position = _arg(position, "position", (torch.int32,), dim=2, like=y)
+    T, k = position.shape
+    weights = _arg(weights, "weights", (torch.float32,), (T, k), like=y)
+    return y, position, weights, y.shape[0], y.shape[1], T, k
+
+
+def expert_combine(y, position, weights, out_type: int | None = None, out: torch.Tensor | None = None, stream=None):
+    """out[t] = sum_j weights[t][j] y[position[t][j]] (y: rows x N; position: T x k
+    int32, values outside the rows add nothing; weights: T x k float32), summed
+    in fp32, in out_type (y's type unless given)."""
+    y, position, weights, rows, N, T, k = _combine_args(y, position, weights)
+    out_type = _DTYPE_IDS[y.dtype] if out_type is None else out_type
+    if out_type not in _OUT_DTYPES:
+        raise ValueError("unknown out_type %r" % (out_type,))
+    out = _out(out, "out", _OUT_DTYPES[out_type], (T, N), y)
+    _call("expert_combine", y.device, stream, y.data_ptr(), _DTYPE_IDS[y.dtype], rows, N, position.data_ptr(),
+          weights.data_ptr(), T, k, out.data_ptr(), out_type)
+    return out
+
+
+def expert_combine_backward(d_out, y, position, weights, d_y: torch.Tensor | None = None,
+                            d_weights: torch.Tensor | None = None, stream=None):
+    """Gradients (d_y in y's type, d_weights T x k float32) of expert_combine from
+    that of its result.  Rows of d_y that no position names are left as they
+    were; without `d_y` they are zero."""
+    y, position, weights, rows, N, T, k = _combine_args(y, position, weights)
+    d_out = _arg(d_out, "d_out", _FLOATS, (T, N), like=y)
+    if d_y is None:
+        d_y = torch.zeros_like(y)
+    d_y = _arg(d_y, "d_y", (y.dtype,), (rows, N), like=y)
+    d_weights = _out(d_weights, "d_weights", torch.float32, (T, k), y)
+    _call("expert_combine_backward", y.device, stream, d_out.data_ptr(), _DTYPE_IDS[d_out.dtype], y.data_ptr(),
+          _DTYPE_IDS[y.dtype], rows, N, position.data_ptr(), weights.data_ptr(), T, k, d_y.data_ptr(),
+          d_weights.data_ptr())
+    return d_y, d_weights
 
 
 def raw_library():

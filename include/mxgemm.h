@@ -308,6 +308,185 @@ int mxgemm_device_supported(void);
  */
 const char *mxgemm_status_string(int status);
 
+/*
+ * ---- 8-bit integer products with a scale per token and per channel --------
+ *
+ * int8gemm_quantize - rows of fp32, bf16 or fp16 -> int8 codes plus one fp32
+ * scale per row (activations: a scale per token; weights stored N x K: a scale
+ * per output channel).  For every row r:
+ *   S[r]    = amax / 127 rounded to fp32, amax = max_k |X[r][k]|, at least
+ *             2^-126 when amax > 0; S[r] = 0 when amax = 0;
+ *   Q[r][k] = X[r][k] / S[r] rounded to the nearest integer, ties to even
+ *             (-127 .. 127; 0 where S[r] = 0).
+ * The quotient is the real one, not an fp32 quotient.  A row holding a NaN or
+ * an infinity gets S = NaN and zero codes.
+ *
+ *   X        device, rows x K elements of in_type (MXG_OUT_F32, _BF16 or
+ *            _F16), row-major, 16-byte aligned (read only)
+ *   rows     >= 1;  K >= 16, K % 16 == 0
+ *   Q        device, rows x K int8, 16-byte aligned (written)
+ *   S        device, rows fp32, 4-byte aligned (written)
+ * Returns MXG_OK or an error status.  The output is bit-for-bit deterministic.
+ */
+int int8gemm_quantize(const void *X, int in_type, int64_t rows, int64_t K,
+                      int8_t *Q, float *S, void *stream);
+
+/* Largest K of an int8 product: below it the sum of K products of any codes
+ * fits 32 bits. */
+#define MXG_INT8_MAX_K 131056
+
+/*
+ * int8gemm_run - C[i][j] = out_type(act(scaleA[i] * scaleB[j] * s + bias[j])),
+ * s = sum_k A[i][k] * B[j][k] over int8 codes, summed exactly in 32-bit
+ * integers on the int8 MFMA.  In fp32: s rounded once, times scaleA[i], times
+ * scaleB[j], then the output step of mxgemm_run_fused.
+ *
+ *   A        device, M x K int8 (any codes, -128 too), 16-byte aligned
+ *   scaleA   device, M fp32, 4-byte aligned
+ *   B        device, N x K int8, 16-byte aligned
+ *   scaleB   device, N fp32, 16-byte aligned
+ *   C        device, M x N elements of out_type, 16-byte aligned; overwritten
+ *   M, N     >= 1;  K >= 16, K % 16 == 0, K <= MXG_INT8_MAX_K
+ *   bias, act, out_type  as for mxgemm_run_fused
+ * Returns MXG_OK or an error status.  Deterministic: the same sums whatever
+ * the kernel.
+ */
+int int8gemm_run(const int8_t *A, const float *scaleA, const int8_t *B,
+                 const float *scaleB, void *C, int64_t M, int64_t N, int64_t K,
+                 const float *bias, int act, int out_type, void *stream);
+
+/* Largest number of experts, of choices per token and of groups of experts,
+ * and of rows of the experts' products. */
+#define MXG_MAX_EXPERTS 1024
+#define MXG_MAX_CHOICES 64
+#define MXG_MAX_GROUPS 64
+#define MXG_MAX_SLOTS (64 << 20)
+
+/*
+ * int8gemm_run_grouped - the products of E experts in one call: rows
+ * offsets[e] .. offsets[e+1]-1 of C are products with B, scaleB and bias of
+ * expert e, as int8gemm_run forms them.  Row p of C takes row
+ * index[p] / index_div of A and scaleA (index == NULL: row p).  With the
+ * `offsets` and `order` of expert_plan and index_div = k this is the first
+ * product of the experts over the tokens' rows; with index == NULL it is one
+ * over rows already sorted.
+ *
+ *   A, scaleA  rowsA rows (1 .. MXG_MAX_SLOTS)
+ *   B          E x N x K int8; scaleB E x N fp32; bias E x N fp32 or NULL
+ *   C          rows x N elements of out_type (rows 1 .. MXG_MAX_SLOTS; with
+ *              index == NULL at most rowsA)
+ *   E          1 .. MXG_MAX_EXPERTS
+ *   offsets    device, E + 1 int32, ascending; read when the work runs.
+ *              Experts without rows are allowed.  Offsets outside 0 .. rows
+ *              count as the nearer bound, one below an earlier one as that.
+ *   index      device, `rows` int32, or NULL;  index_div >= 1
+ * Rows of C outside offsets[0] .. offsets[E]-1 are left as they were.  A row
+ * whose index is negative or outside A is NaN.
+ * Returns MXG_OK or an error status.  Deterministic.
+ */
+int int8gemm_run_grouped(const int8_t *A, const float *scaleA, int64_t rowsA,
+                         const int8_t *B, const float *scaleB, void *C,
+                         int64_t rows, int64_t N, int64_t K, int64_t E,
+                         const int32_t *offsets, const int32_t *index,
+                         int index_div, const float *bias, int act,
+                         int out_type, void *stream);
+
+/* Scores of expert_route. */
+#define MXG_SCORE_SOFTMAX 0  /* over the E logits of a token */
+#define MXG_SCORE_SIGMOID 1  /* of each logit */
+
+/*
+ * expert_route - choice of k of E experts for each token, and their weights.
+ *   s = softmax(logits[t]) or sigmoid(logits[t]);   c = s + bias
+ *   groups > 1: the experts form `groups` runs of E / groups; a run's score
+ *     is the sum of its group_top (1 or 2) largest c, and the top_groups runs
+ *     of largest score stay (ties: the lower run);
+ *   ids[t]     = the k experts of largest c that stay, in falling order of c
+ *                (ties: the lower expert);
+ *   weights[t] = scale * s[ids], divided by the sum of s[ids] when renormalize.
+ * The bias counts for the choice alone.  A logit of -inf takes its expert out;
+ * where fewer than k experts are left, ids ends in -1 with weight 0.  A NaN
+ * score ranks below every number (softmax: a NaN or +inf logit makes the whole
+ * row NaN: its available experts are taken in order, with NaN weights).
+ * Without bias and with group_top == 1 the order is that of the logits, which
+ * is that of the scores; otherwise c is formed in 64 bits.
+ *
+ *   logits      device, T x E elements of in_type, aligned to an element
+ *   T           >= 1;  E 1 .. MXG_MAX_EXPERTS;  k 1 .. MXG_MAX_CHOICES, at most
+ *               top_groups * (E / groups)
+ *   bias        device, E fp32, or NULL
+ *   groups      1 .. MXG_MAX_GROUPS, dividing E;  top_groups 1 .. groups
+ *   renormalize 0 or 1
+ *   ids         device, T x k int32 (written);  weights  T x k fp32 (written)
+ * Returns MXG_OK or an error status.  Deterministic.
+ */
+int expert_route(const void *logits, int in_type, int64_t T, int64_t E, int k,
+                 int score, const float *bias, int groups, int top_groups,
+                 int group_top, int renormalize, float scale, int32_t *ids,
+                 float *weights, void *stream);
+
+/*
+ * expert_route_backward - gradient of expert_route's weights with respect to
+ * the logits, the choice held: d_logits[t][e] = sum_j d_weights[t][j] *
+ * d weights[t][j] / d logits[t][e].  score, renormalize and scale as in the
+ * forward call; an id outside 0 .. E-1 has no gradient.  All of d_logits
+ * (T x E of in_type) is written.
+ */
+int expert_route_backward(const void *logits, int in_type, int64_t T, int64_t E,
+                          const int32_t *ids, const float *d_weights, int k,
+                          int score, int renormalize, float scale,
+                          void *d_logits, void *stream);
+
+/*
+ * expert_plan - the T * k slots (slot t * k + j is choice j of token t) sorted
+ * by expert, slots of one expert in ascending order:
+ *   offsets[e]  = slots of experts below e (E + 1 values)
+ *   order[p]    = the slot in row p; -1 from row offsets[E] on
+ *   position[s] = the row of slot s; -1 where ids[s] is outside 0 .. E-1
+ *
+ *   ids        device, T x k int32 (read only)
+ *   offsets    device, E + 1 int32;  order, position  T * k int32 (written)
+ *   workspace  device, expert_plan_workspace(T, k, E) bytes, 4-byte aligned;
+ *              NULL when that is 0.  Holds nothing between calls.
+ * Returns MXG_OK or an error status.  Deterministic.  expert_plan_workspace
+ * returns -1 for arguments that expert_plan refuses.
+ */
+int64_t expert_plan_workspace(int64_t T, int k, int64_t E);
+int expert_plan(const int32_t *ids, int64_t T, int k, int64_t E,
+                int32_t *offsets, int32_t *order, int32_t *position,
+                void *workspace, void *stream);
+
+/*
+ * expert_combine - out[t] = sum_j weights[t][j] * Y[position[t][j]], the sum
+ * in fp32 with j ascending, rounded once to out_type.  A position outside
+ * 0 .. rows-1 adds nothing.
+ *
+ *   Y         device, rows x N elements of y_type, 16-byte aligned
+ *   rows      1 .. MXG_MAX_SLOTS;  N, T >= 1;  k 1 .. MXG_MAX_CHOICES
+ *   position  device, T x k int32;  weights  device, T x k fp32
+ *   out       device, T x N elements of out_type, 16-byte aligned (written)
+ * Returns MXG_OK or an error status.  Deterministic.
+ */
+int expert_combine(const void *Y, int y_type, int64_t rows, int64_t N,
+                   const int32_t *position, const float *weights, int64_t T,
+                   int k, void *out, int out_type, void *stream);
+
+/*
+ * expert_combine_backward - gradients of expert_combine from that of its
+ * result: dY[position[t][j]] = weights[t][j] * dOut[t] and dW[t][j] = sum_n
+ * dOut[t][n] * Y[position[t][j]][n] (fp32; 0 where the position is outside
+ * 0 .. rows-1).  The positions have to differ, as a plan's do.  Rows of dY
+ * that no position names are left as they were.
+ *
+ *   dOut  device, T x N elements of out_type;  Y, dY  rows x N of y_type, each
+ *         16-byte aligned;  dW  device, T x k fp32 (written)
+ */
+int expert_combine_backward(const void *dOut, int out_type, const void *Y,
+                            int y_type, int64_t rows, int64_t N,
+                            const int32_t *position, const float *weights,
+                            int64_t T, int k, void *dY, float *dW,
+                            void *stream);
+
 #ifdef __cplusplus
 }
 #endif

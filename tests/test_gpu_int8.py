@@ -1,0 +1,443 @@
+"""int8 quantizer and products (dense and by expert) against 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+import experts_ref as ref
+from gpu_util import binding, poison_lds, say
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TYPES = {0: torch.float32, 1: torch.bfloat16, 2: torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    assert binding().mxgemm_device_supported()
+    yield
+
+
+def dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+# ---- quantizer --------------------------------------------------------------
+
+
+def _check_quantize(x):
+    b = binding()
+    rows, K = x.shape
+    q = torch.full((rows, K), 77, dtype=torch.int8, device=DEV)
+    s = torch.full((rows,), -5.0, device=DEV)
+    b.int8gemm_quantize(x, q=q, s=s)
+    torch.cuda.synchronize()
+    qr, sr = ref.quantize(x.float().cpu().numpy())
+    assert np.array_equal(s.cpu().numpy(), sr, equal_nan=True)
+    assert np.array_equal(q.cpu().numpy(), qr)
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("rows,K", [(1, 16), (3, 48), (5, 2032), (4, 2064), (300, 1024), (17, 8192), (9, 14336), (2, 65552)])
+def test_quantize(kind, rows, K):
+    say("quantize", kind, rows, K)
+    rng = np.random.default_rng(rows * K + kind)
+    x = rng.standard_normal((rows, K), dtype=np.float32)
+    x[:, ::97] *= 20.0
+    _check_quantize(dev(x).to(TYPES[kind]))
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+def test_quantize_special_rows(kind):
+    say("quantize special", kind)
+    K = 272
+    x = np.random.default_rng(1).standard_normal((14, K)).astype(np.float32)
+    x[0] = 0.0
+    x[1] = -0.0
+    x[2, 100] = np.nan
+    x[3, 271] = np.inf
+    x[4, 0] = -np.inf
+    # scale 1: every half is a tie
+    x[5] = np.arange(K) % 127 - 63.5
+    x[5, 7] = 127.0
+    # scale 2^-10, ties again
+    x[6] = (np.arange(K) % 200 - 99.5) * 2.0 ** -10
+    x[6, 3] = -127.0 * 2.0 ** -10
+    x[7] = 0.0
+    x[7, 5] = 1.0
+    x[8] = 3.0
+    x[9] *= np.float32(2.0 ** -120)
+    x[10] *= np.float32(2.0 ** -125)   # scale held at 2^-126 (fp32; others are zero there)
+    x[11] *= np.float32(2.0 ** -140)
+    x[12] *= np.float32(1e4)
+    x[13, :] = 1e-7
+    x[13, 0] = 60000.0
+    _check_quantize(dev(x).to(TYPES[kind]))
+
+
+def test_quantize_near_borders():
+    """fp32 values one step to either side of every border between two codes."""
+    say("quantize borders")
+    rows = []
+    rng = np.random.default_rng(2)
+    for amax in rng.uniform(0.5, 2.0, 40).astype(np.float32):
+        s = np.float32(np.float64(amax) / 127.0)
+        border = ((np.arange(-127, 127) + 0.5) * np.float64(s)).astype(np.float32)
+        vals = np.concatenate([border, np.nextafter(border, np.float32(np.inf)), np.nextafter(border, np.float32(-np.inf)),
+                               np.full(6, amax, np.float32)])
+        rows.append(np.clip(vals, -amax, amax))
+    _check_quantize(dev(np.stack(rows)))
+
+
+# ---- products ---------------------------------------------------------------
+
+
+def _codes(rng, rows, K):
+    return rng.integers(-128, 128, (rows, K), dtype=np.int64).astype(np.int8)
+
+
+def _check(got, want, tol, kind, what):
+    got = got.float().cpu().numpy().astype(np.float64)
+    # a result of size |y| + tol is rounded by half a step of it; below the
+    # type's smallest normal value the step no longer shrinks, so half of that
+    # value's step is added (fp16: 2^-14 * 2^-11 = 2^-25)
+    half = ref.half_step(TYPES[kind])
+    bound = tol + half * (np.abs(want) + tol) + half * torch.finfo(TYPES[kind]).smallest_normal
+    off = np.abs(got - want)
+    worst = np.max(off / np.maximum(bound, 1e-300))
+    say("  %s: error / bound %.3g" % (what, worst))
+    assert np.isfinite(got).all()
+    assert worst <= 1.0
+
+
+def _dense(M, N, K, kind, bias, act, seed):
+    rng = np.random.default_rng(seed)
+    a, w = _codes(rng, M, K), _codes(rng, N, K)
+    a_s = rng.uniform(0.5, 1.5, M).astype(np.float32) / 128
+    b_s = rng.uniform(0.5, 1.5, N).astype(np.float32) / (128 * np.sqrt(K).astype(np.float32))
+    bi = rng.standard_normal(N).astype(np.float32) if bias else None
+    want, tol = ref.product(a, a_s, w, b_s, bi, act)
+    b = binding()
+    out = torch.full((M, N), float("nan"), dtype=TYPES[kind], device=DEV)
+    poison_lds()
+    b.int8gemm_run(dev(a), dev(a_s), dev(w), dev(b_s), bias=None if bi is None else dev(bi),
+                   act=b.ACT_GELU if act else b.ACT_NONE, out_type=kind, out=out)
+    torch.cuda.synchronize()
+    _check(out, want, tol, kind, "%dx%dx%d" % (M, N, K))
+    return out
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 16), (1, 3, 48), (1, 4096, 4096), (2, 100, 80), (5, 17, 2064), (15, 256, 1024), (16, 1000, 8192), (17, 260, 4096),
+    (31, 64, 144), (32, 512, 2048), (33, 1028, 1040), (48, 300, 512), (64, 4100, 2064), (65, 129, 272), (100, 1000, 1008),
+    (128, 128, 128), (129, 257, 4096), (256, 256, 64), (300, 640, 2000), (512, 512, 1024), (1000, 200, 16), (777, 1031, 528),
+    (64, 5000, 96), (1, 20000, 32)])
+def test_product(M, N, K):
+    say("product", M, N, K)
+    _dense(M, N, K, 0, False, False, M * 7 + N * 3 + K)
+
+
+@pytest.mark.parametrize("M,N,K", [(1024, 2048, 1024), (2304, 2560, 256), (2049, 2300, 400)])
+def test_product_larger(M, N, K):
+    say("product", M, N, K)
+    _dense(M, N, K, 1, True, False, 5)
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("bias,act", [(True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("M,N,K", [(3, 67, 160), (16, 512, 1024), (70, 132, 272), (260, 516, 1040)])
+def test_product_output_step(kind, bias, act, M, N, K):
+    say("product output", kind, bias, act, M, N, K)
+    _dense(M, N, K, kind, bias, act, M + N + K + kind)
+
+
+@pytest.mark.parametrize("M", [1, 20, 130, 300])
+@pytest.mark.parametrize("a,b", [(-128, -128), (127, -128), (-127, 127)])
+def test_product_largest_sums(M, a, b):
+    """Every product at its largest, at the largest K: the sum fills 32 bits."""
+    say("largest sums", M, a, b)
+    bd = binding()
+    K = bd.INT8_MAX_K
+    N = 34
+    out = bd.int8gemm_run(torch.full((M, K), a, dtype=torch.int8, device=DEV), torch.ones(M, device=DEV),
+                          torch.full((N, K), b, dtype=torch.int8, device=DEV), torch.ones(N, device=DEV))
+    torch.cuda.synchronize()
+    want = np.float32(a * b * K)
+    assert (out.cpu().numpy() == want).all()
+
+
+def test_product_scale_values():
+    """A zero, an infinite and a NaN scale reach their row or column alone."""
+    say("scale values")
+    b = binding()
+    rng = np.random.default_rng(3)
+    for M in (5, 140):
+        N, K = 40, 64
+        a, w = _codes(rng, M, K), _codes(rng, N, K)
+        a_s, b_s = np.ones(M, np.float32), np.ones(N, np.float32)
+        a_s[2], a_s[3], b_s[7], b_s[9] = 0.0, np.nan, np.inf, np.nan
+        got = b.int8gemm_run(dev(a), dev(a_s), dev(w), dev(b_s)).cpu().numpy()
+        s = (a.astype(np.int64) @ w.astype(np.int64).T).astype(np.float32)
+        with np.errstate(all="ignore"):
+            want = (s * a_s[:, None]) * b_s[None, :]
+        assert np.array_equal(got, want, equal_nan=True)
+
+
+# ---- by expert --------------------------------------------------------------
+
+
+def _experts(offsets, rows, N, K, kind=0, tokens=None, div=1, bias=False, act=False, seed=0, index=None):
+    """Runs the experts' products into a filled buffer; (result, expected, tolerance, rows that belong to an expert)."""
+    rng = np.random.default_rng(seed)
+    E = len(offsets) - 1
+    rows_a = rows if tokens is None else tokens
+    a, w = _codes(rng, rows_a, K), _codes(rng, E * N, K).reshape(E, N, K)
+    a_s = rng.uniform(0.5, 1.5, rows_a).astype(np.float32) / 128
+    b_s = (rng.uniform(0.5, 1.5, (E, N)) / (128 * np.sqrt(K))).astype(np.float32)
+    bi = rng.standard_normal((E, N)).astype(np.float32) if bias else None
+    if tokens is not None and index is None:
+        index = rng.permutation(tokens * div)[:rows].astype(np.int32)
+    src = np.arange(rows) if index is None else np.where(index < 0, -1, index // div)
+    src = np.where(src >= rows_a, -1, src)
+    want, tol = np.full((rows, N), np.nan), np.zeros((rows, N))
+    owned = np.zeros(rows, bool)
+    edges = np.maximum.accumulate(np.clip(np.asarray(offsets, np.int64), 0, rows))
+    for e in range(E):
+        mine = np.arange(edges[e], edges[e + 1])
+        owned[mine] = True
+        ok = mine[src[mine] >= 0]
+        if ok.size:
+            want[ok], tol[ok] = ref.product(a[src[ok]], a_s[src[ok]], w[e], b_s[e], None if bi is None else bi[e], act)
+    b = binding()
+    out = torch.full((rows, N), 123.0, dtype=TYPES[kind], device=DEV)
+    poison_lds()
+    b.int8gemm_run_grouped(dev(a), dev(a_s), dev(w), dev(b_s), dev(np.asarray(offsets, np.int32)),
+                           index=None if index is None else dev(index.astype(np.int32)), index_div=div,
+                           bias=None if bi is None else dev(bi), act=b.ACT_GELU if act else b.ACT_NONE, out_type=kind,
+                           out=out)
+    torch.cuda.synchronize()
+    return out, want, tol, owned
+
+
+def _check_experts(out, want, tol, owned, kind, what):
+    assert (out.float().cpu().numpy()[~owned] == 123.0).all(), "rows of no expert were written"
+    bad = owned & np.isnan(want).any(1)
+    assert torch.isnan(out).cpu().numpy()[bad].all()
+    good = owned & ~bad
+    if good.any():
+        _check(out[torch.from_numpy(good).to(DEV)], want[good], tol[good], kind, what)
+
+
+def _counts(rng, E, rows, skew):
+    p = rng.dirichlet(np.full(E, skew))
+    return np.concatenate([[0], np.cumsum(rng.multinomial(rows, p))])
+
+
+@pytest.mark.parametrize("E,rows,N,K,skew", [
+    (1, 1, 16, 16, 1.0), (8, 5, 64, 64, 1.0), (64, 64, 128, 256, 1.0), (64, 40, 100, 272, 0.1), (5, 300, 132, 144, 1.0),
+    (16, 1000, 260, 512, 0.3), (3, 700, 512, 1024, 5.0), (1024, 2000, 20, 32, 0.5), (100, 3000, 68, 80, 0.05),
+    (7, 2000, 300, 208, 1.0), (2, 4096, 256, 128, 50.0), (130, 130, 33, 48, 1.0)])
+def test_experts(E, rows, N, K, skew):
+    say("experts", E, rows, N, K)
+    off = _counts(np.random.default_rng(E + rows), E, rows, skew)
+    _check_experts(*_experts(off, rows, N, K, seed=E), 0, "experts")
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("E,tokens,div,N,K", [(8, 16, 4, 128, 256), (16, 200, 2, 72, 144), (32, 1, 8, 256, 512),
+                                              (4, 600, 3, 260, 272)])
+def test_experts_with_index(kind, E, tokens, div, N, K):
+    say("experts index", kind, E, tokens, div, N, K)
+    rows = tokens * div
+    off = _counts(np.random.default_rng(rows), E, rows, 1.0)
+    _check_experts(*_experts(off, rows, N, K, kind, tokens=tokens, div=div, bias=True, act=kind != 0, seed=rows), kind,
+                   "experts")
+
+
+@pytest.mark.parametrize("rows", [7, 40, 700])
+@pytest.mark.parametrize("offsets", [
+    (0, 0, 0, 0), (3, 3, 5, 5), (2, 4, 4, 6), (0, 7, 7, 7), (-5, 2, 3, 1000000), (5, 2, 6, 4), (7, 7, 7, 9), (0, 1, 2, 3),
+    (-2147483648, 2147483647, 0, 3)])
+def test_experts_offsets(rows, offsets):
+    """Empty experts, rows in front and behind left alone, offsets outside the rows and falling."""
+    say("experts offsets", rows, offsets)
+    _check_experts(*_experts(offsets, rows, 36, 80, seed=9), 0, "experts")
+
+
+@pytest.mark.parametrize("rows", [12, 400])
+def test_experts_index_outside(rows):
+    say("experts index outside", rows)
+    index = np.arange(rows, dtype=np.int32)
+    index[[1, 5]] = -1
+    index[3] = rows * 2
+    index[7] = 2147483647
+    index[9] = -2147483648
+    index[10] = 2                                   # the same row twice
+    off = (0, rows // 3, rows // 3, rows)
+    out = _experts(off, rows, 44, 64, tokens=rows // 2, div=2, index=index, seed=4)
+    _check_experts(*out, 0, "experts")
+
+
+def test_dense_is_one_expert():
+    """The sums are exact, so the dense product and one expert's agree bit for bit, whatever kernels they take."""
+    b = binding()
+    rng = np.random.default_rng(8)
+    for M in (1, 16, 40, 100, 300, 600):
+        say("dense = one expert", M)
+        a, w = dev(_codes(rng, M, 528)), dev(_codes(rng, 260, 528))
+        a_s, b_s = torch.rand(M, device=DEV), torch.rand(260, device=DEV)
+        bias = torch.rand(260, device=DEV)
+        for kind in (0, 1, 2):
+            x = b.int8gemm_run(a, a_s, w, b_s, bias=bias, act=b.ACT_GELU, out_type=kind)
+            off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+            y = b.int8gemm_run_grouped(a, a_s, w[None], b_s[None], off, bias=bias[None], act=b.ACT_GELU, out_type=kind)
+            z = b.int8gemm_run_grouped(a, a_s, w[None].expand(70, -1, -1).contiguous(), b_s[None].expand(70, -1).contiguous(),
+                                       torch.tensor([0] * 35 + [M // 2] * 20 + [M] * 16, dtype=torch.int32, device=DEV),
+                                       bias=bias[None].expand(70, -1).contiguous(), act=b.ACT_GELU, out_type=kind)
+            assert torch.equal(x, y) and torch.equal(x, z)
+
+
+def test_weights_past_4_gib():
+    say("weights past 4 GiB")
+    b = binding()
+    E, N, K, rows = 70, 8192, 8192, 70
+    w = torch.empty((E, N, K), dtype=torch.int8, device=DEV).random_(-128, 128)
+    a = torch.empty((rows, K), dtype=torch.int8, device=DEV).random_(-128, 128)
+    one = torch.ones(rows, device=DEV)
+    off = torch.arange(E + 1, dtype=torch.int32, device=DEV)
+    got = b.int8gemm_run_grouped(a, one, w, torch.ones(E, N, device=DEV), off)
+    for e in (0, 31, 32, 63, 64, 69):
+        want = (a[e].double()[None] @ w[e].double().t())[0].float()
+        assert torch.equal(got[e], want), e
+
+
+def test_output_past_4_gib():
+    say("output past 4 GiB")
+    b = binding()
+    M, N, K = 70000, 16400, 16
+    a = torch.empty((M, K), dtype=torch.int8, device=DEV).random_(-128, 128)
+    w = torch.empty((N, K), dtype=torch.int8, device=DEV).random_(-128, 128)
+    got = b.int8gemm_run(a, torch.ones(M, device=DEV), w, torch.ones(N, device=DEV))
+    for r in (slice(0, 64), slice(32700, 32840), slice(65400, 65600), slice(M - 70, M)):
+        assert torch.equal(got[r], (a[r].double() @ w.double().t()).float())
+
+
+# ---- streams, graphs, refusals ----------------------------------------------
+
+
+def test_side_stream():
+    """The call joins the stream it is given, and the current one without."""
+    say("side stream")
+    b = binding()
+    rng = np.random.default_rng(11)
+    x = dev(rng.standard_normal((64, 2048)).astype(np.float32))
+    w, w_s = b.int8gemm_quantize(dev(rng.standard_normal((512, 2048)).astype(np.float32)))
+    want = b.int8gemm_run(*b.int8gemm_quantize(x), w, w_s)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for given in (True, False):
+        big = torch.zeros(64 << 20, device=DEV)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            y = torch.zeros_like(x)
+            for _ in range(20):
+                big.add_(1.0)       # work that the call has to wait for
+            y.copy_(x)
+            if not given:
+                got = b.int8gemm_run(*b.int8gemm_quantize(y), w, w_s)
+        if given:
+            q, s = b.int8gemm_quantize(y, stream=side)
+            got = b.int8gemm_run(q, s, w, w_s, stream=side)
+        side.synchronize()
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [1, 16, 60, 300])
+def test_graph_replay(M):
+    say("graph replay int8", M)
+    b = binding()
+    rng = np.random.default_rng(M)
+    N, K, E = 516, 1040, 6
+    x = dev(rng.standard_normal((M, K)).astype(np.float32)).bfloat16()
+    w = dev(_codes(rng, E * N, K)).view(E, N, K)
+    w_s, bias = torch.rand(E, N, device=DEV), torch.rand(E, N, device=DEV)
+    off = dev(_counts(rng, E, M, 1.0).astype(np.int32))
+    q, s = torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+    dense, by = torch.empty((M, N), dtype=torch.bfloat16, device=DEV), torch.empty((M, N), device=DEV)
+
+    def run():
+        b.int8gemm_quantize(x, q=q, s=s)
+        b.int8gemm_run(q, s, w[0], w_s[0], bias=bias[0], act=b.ACT_GELU, out_type=b.OUT_BF16, out=dense)
+        b.int8gemm_run_grouped(q, s, w, w_s, off, bias=bias, out=by)
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for rep in range(3):
+        x.copy_(dev(rng.standard_normal((M, K)).astype(np.float32)))
+        off.copy_(dev(_counts(rng, E, M, 0.5).astype(np.int32)))
+        run()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (q, s, dense, by)]
+        for t in (q, s, dense, by):
+            t.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for got, t in zip((q, s, dense, by), want):
+            assert torch.equal(got, t), rep
+
+
+def test_refusals():
+    say("refusals")
+    b = binding()
+    x = torch.zeros((4, 64), device=DEV)
+    q, s = b.int8gemm_quantize(x)
+    with pytest.raises(ValueError):
+        b.int8gemm_quantize(x.t())
+    with pytest.raises(ValueError):
+        b.int8gemm_quantize(x[0])
+    with pytest.raises(TypeError):
+        b.int8gemm_quantize(x.double())
+    with pytest.raises(b.MXGemmError):
+        b.int8gemm_quantize(torch.zeros((4, 24), device=DEV))
+    with pytest.raises(b.MXGemmError):
+        b.int8gemm_quantize(torch.zeros((0, 64), device=DEV))
+    with pytest.raises(ValueError):
+        b.int8gemm_quantize(x, q=q[:2])
+    with pytest.raises(TypeError):
+        b.int8gemm_run(q.view(torch.uint8), s, q, s)
+    with pytest.raises(ValueError):
+        b.int8gemm_run(q, s[:3], q, s)
+    with pytest.raises(ValueError):
+        b.int8gemm_run(q, s, q[:, :32].contiguous(), s)
+    with pytest.raises(ValueError):
+        b.int8gemm_run(q, s, q, s.cpu())
+    with pytest.raises(ValueError):
+        b.int8gemm_run(q, s, q, s, out_type=7)
+    with pytest.raises(b.MXGemmError):
+        b.int8gemm_run(q, s, q, s, act=9)
+    with pytest.raises(ValueError):
+        b.int8gemm_run(q, s, q, s, bias=torch.zeros(5, device=DEV))
+    with pytest.raises(TypeError):
+        b.int8gemm_run(q, s, q, s, out_type=b.OUT_BF16, out=torch.zeros((4, 4), device=DEV))
+    big = torch.zeros((1, b.INT8_MAX_K + 16), dtype=torch.int8, device=DEV)
+    with pytest.raises(b.MXGemmError):
+        b.int8gemm_run(big, s[:1].clone(), big, s[:1].clone())
+    odd = torch.zeros(4 * 64 + 1, dtype=torch.int8, device=DEV)[1:].view(4, 64)
+    with pytest.raises(b.MXGemmError):
+        b.int8gemm_run(odd, s, q, s)
+    off = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    with pytest.raises(TypeError):
+        b.int8gemm_run_grouped(q, s, q[None], s[None], off.long())
+    with pytest.raises(ValueError):
+        b.int8gemm_run_grouped(q, s, q[None], s[None], off[:1])
+    with pytest.raises(ValueError):
+        b.int8gemm_run_grouped(q, s, q, s, off)
+    with pytest.raises(b.MXGemmError):
+        b.int8gemm_run_grouped(q, s, q[None], s[None], off, index=off.clone(), index_div=0)
