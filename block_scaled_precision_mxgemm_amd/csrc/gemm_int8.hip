@@ -14,24 +14,24 @@
 namespace mxg {
 namespace {
 
-// 64 x 64 tiles, 4 waves of 32 x 32, slices of 128 k.
+// ---- gathered rows of an A of 4 GiB and more --------------------------------
+//
+// The one case that the kernels below, whose gathered rows are 32-bit offsets,
+// do not take.  64 x 64 tiles, 4 waves of 32 x 32, slices of 128 k through
+// registers.
 constexpr int kBM = 64, kBN = 64, kBK = 128;
 
 __global__ __launch_bounds__(256) void int8_tile_kernel(I8Args a, int tiles_n) {
   __shared__ __attribute__((aligned(16))) uint8_t sa[kBM * kBK], sb[kBN * kBK];
-  __shared__ I8Tile tile;
   __shared__ int64_t arow[kBM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, r = lane & 15;
-  const int tm = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
-  if (wave == 0) find_tile(a, kBM, tm, lane, &tile);
-  __syncthreads();
-  const I8Tile t = tile;
-  if (t.rows <= 0) return;
+  I8Tile t;
+  if (!find_tile(a, kBM, tiles_n, blockIdx.x, lane, t)) return;
   if (tid < kBM) arow[tid] = tid < t.rows ? a_row(a, t.row0 + tid) : -1;
   __syncthreads();
   const int8_t* B = a.B + (int64_t)t.expert * a.N * a.K;
-  const int n0 = tn * kBN;
+  const int n0 = t.tn * kBN;
   const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
   v4i acc[2][2] = {};
   for (int k0 = 0; k0 < a.K; k0 += kBK) {
@@ -75,14 +75,632 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(I8Args a, int tiles_n) {
   }
 }
 
-}  // namespace
+// ---- large tiles ------------------------------------------------------------
+//
+// WM x WN waves, two per SIMD, each with a TM x TN part of the tile in 16 x 16
+// fragments.  K goes by slices of 128 (whole 128-byte lines of each row) in
+// two steps of 64; LDS holds three slices of A and two of B, filled by direct
+// global -> LDS copies.  While a wave runs the MFMAs of one step on registers
+// it reads the fragments of the next step from LDS, so only one barrier per
+// slice is needed: behind the first step's MFMAs, when slice s has been read
+// by all and slice s + 1 has arrived.  The copies of slice s + 2 are spread over
+// the steps, so that their issue does not hold up the MFMAs: B's behind the
+// barrier, into the buffer that slice s left, A's (into the buffer of slice
+// s - 1) in the step before.
+//
+// A workgroup takes tile after tile; the first copies of the next tile are
+// issued before the last step of the present one, and its output goes through
+// the third A buffer, which those copies leave alone.
+template <int BM_, int BN_, int WM_, int WN_>
+struct I8Cfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int NW = WM * WN;                // waves
+  static constexpr int TM = BM / WM, TN = BN / WN;  // a wave's part of the tile
+  static constexpr int FM = TM / 16, FN = TN / 16;  // and its fragments
+  static constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KiB copies of a wave and slice
+  static constexpr int SZA = BM * 128, SZB = BN * 128;
+  static constexpr int OFF_B = 3 * SZA;
+  // output staging, 4 KiB per wave: the third A buffer, or its own
+  static constexpr bool OWN = SZA < NW * 4096;
+  static constexpr int OFF_CST = OWN ? OFF_B + 2 * SZB : 2 * SZA;
+  static constexpr int LDS = OFF_B + 2 * SZB + (OWN ? NW * 4096 : 0);
+  static constexpr int PER_CU = LDS > 80 * 1024 ? 1 : LDS > 40 * 1024 ? 2 : 4;  // workgroups
+  static_assert(LDS <= 160 * 1024, "fits the 160 KiB LDS of a gfx950 CU");
+  static_assert(CA * NW * 8 == BM && CB * NW * 8 == BN && NW % 2 == 0, "copies split evenly over the waves");
+  static_assert(TN % 64 == 0, "output staging");
+};
 
-hipError_t launch_int8(const I8Args& a, hipStream_t stream) {
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ring_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// int8 MFMA with the accumulator tied in place in AGPRs, kept in program order:
+// left to itself the compiler moves fragments through AGPRs.
+__device__ __forceinline__ void i8_mfma_acc(v4i& c, const v4i& x, const v4i& y) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(x), "v"(y));
+}
+// wait states around the inline MFMAs, as mfma_fence_init and mfma_drain
+template <int NI, int NJ>
+__device__ __forceinline__ void i8_fence_init(v4i (&acc)[NI][NJ]) {
+#pragma unroll
+  for (int i = 0; i < NI; i++)
+#pragma unroll
+    for (int j = 0; j < NJ; j++) asm volatile("" : "+a"(acc[i][j]));
+  asm volatile("s_nop 7" ::: "memory");
+}
+template <int NI, int NJ>
+__device__ __forceinline__ void i8_drain(v4i (&acc)[NI][NJ]) {
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < NI; i++)
+#pragma unroll
+    for (int j = 0; j < NJ; j++) asm volatile("" : "+a"(acc[i][j]));
+}
+
+// A lane's number or address, in a form that the compiler cannot see through:
+// what is derived from it is formed where it is used instead of ahead of the tile loop
+// and held in registers across it.
+__device__ __forceinline__ int opaque(int lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+template <class T, bool GATHER>
+struct RingKernel {
+  static constexpr int FM = T::FM, FN = T::FN;
+
+  // MFMAs of a step, column by column of fragments, on the rows' fragments
+  // `ca` and the columns' `fb`; `also(j)` runs behind column j.  From the
+  // second column on the fragments of the next step are read: a column's into
+  // the registers that its MFMAs have left, the rows' into `na`.
+  template <class F>
+  static __device__ __forceinline__ void step(v4i (&acc)[FM][FN], const v4i (&ca)[FM], v4i (&na)[FM], v4i (&fb)[FN],
+                                              const uint8_t* ra, const uint8_t* rb, F also) {
+#pragma unroll
+    for (int j = 0; j < FN; j++) {
+#pragma unroll
+      for (int u = 0; u < FM; u++) i8_mfma_acc(acc[u][j], fb[j], ca[u]);
+      __builtin_amdgcn_sched_barrier(0);
+      also(j);
+      if (j >= 1) {
+#pragma unroll
+        for (int u = 0; u < FM; u++)
+          if (u * (FN - 1) / FM == j - 1) na[u] = *reinterpret_cast<const v4i*>(ra + u * 2048);
+        if (j == 1) fb[0] = *reinterpret_cast<const v4i*>(rb);
+        fb[j] = *reinterpret_cast<const v4i*>(rb + j * 2048);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void run(const I8Args& a, int tiles_n) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / T::WN, wn = wave % T::WN;
+    const int g = lane >> 4, r = lane & 15;
+    const int K = a.K;
+    const int S = (K + 127) >> 7, tail = K & 127;
+
+    // A copy moves 8 rows of 128 bytes: lane l fetches row l / 8, and of its
+    // chunks the one that the swizzle puts at place l % 8 (the row's swizzle
+    // depends on the parity of the copy's number, which is the wave's).
+    constexpr int kRsrcWord3 = 0x00020000;
+    const int c16 = ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
+    const uint32_t off0 = (uint32_t)((8 * wave + (lane >> 3)) * K + c16);
+    const uint32_t rows_step = (uint32_t)(8 * T::NW * K);
+    I8Tile t;
+    __amdgpu_buffer_rsrc_t rs_a, rs_b;
+    uint32_t oa[GATHER ? T::CA : 1], lim_a = 0, lim_b = 0;
+    auto set_tile = [&](int64_t tile) -> bool {
+      const int lane = opaque(threadIdx.x & 63);
+      const int c16 = ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
+      if (!find_tile(a, T::BM, tiles_n, tile, lane, t)) return false;
+      const int n0 = t.tn * T::BN, cols = min(T::BN, a.N - n0);
+      if constexpr (GATHER) {
+#pragma unroll
+        for (int u = 0; u < T::CA; u++) {
+          const int row = min((wave + T::NW * u) * 8 + (lane >> 3), t.rows - 1);
+          // a row outside A is read as row 0 (its results are NaN)
+          oa[u] = (uint32_t)(max(a_row(a, t.row0 + row), (int64_t)0) * K) + c16;
+        }
+        rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)a.A, 0, (int)(uint32_t)(a.rows_a * K), kRsrcWord3);
+      } else {
+        lim_a = (uint32_t)((t.rows - 1) * K + c16);
+        rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)(a.A + t.row0 * K), 0, t.rows * K, kRsrcWord3);
+      }
+      lim_b = (uint32_t)((cols - 1) * K + c16);
+      rs_b = __builtin_amdgcn_make_buffer_rsrc((void*)(a.B + ((int64_t)t.expert * a.N + n0) * K), 0, cols * K,
+                                               kRsrcWord3);
+      return true;
+    };
+    // Rows past the tile's are fetched as its last one; in a partial last
+    // slice, chunks past K as the slice's first one.
+    auto back = [&](int slice) {
+      const int lane = opaque(threadIdx.x & 63);
+      const int c16 = ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
+      return (tail != 0 && slice == S - 1 && c16 >= tail) ? (uint32_t)c16 : 0u;
+    };
+    auto copy_a1 = [&](int slice, int buf, uint32_t b, int u) {
+      const uint32_t o = GATHER ? oa[GATHER ? u : 0] : min(off0 + u * rows_step, lim_a);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, (lds_void*)(smem + buf * T::SZA + (wave + T::NW * u) * 1024), 16,
+                                               o - b, slice * 128, 0, 0);
+    };
+    auto copy_b1 = [&](int slice, uint32_t b, int u) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs_b, (lds_void*)(smem + T::OFF_B + (slice & 1) * T::SZB + (wave + T::NW * u) * 1024), 16,
+          min(off0 + u * rows_step, lim_b) - b, slice * 128, 0, 0);
+    };
+    auto copy_a = [&](int slice, int buf, uint32_t b) {
+#pragma unroll
+      for (int u = 0; u < T::CA; u++) copy_a1(slice, buf, b, u);
+    };
+    auto copy_b = [&](int slice, uint32_t b) {
+#pragma unroll
+      for (int u = 0; u < T::CB; u++) copy_b1(slice, b, u);
+    };
+    // zeros over the chunks of A past K that this lane fetched (their
+    // products vanish whatever B's are)
+    auto zero_tail = [&](int buf) {
+      const int lane = opaque(threadIdx.x & 63);
+      const int c16 = ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
+      if (c16 >= tail) {
+#pragma unroll
+        for (int u = 0; u < T::CA; u++)
+          *reinterpret_cast<v4i*>(smem + buf * T::SZA + (wave + T::NW * u) * 1024 + lane * 16) = v4i{0, 0, 0, 0};
+      }
+    };
+    auto start_tile = [&]() {
+      copy_a(0, 0, back(0));
+      copy_b(0, back(0));
+      if (S > 1) {
+        copy_a(1, 1, back(1));
+        copy_b(1, back(1));
+      }
+    };
+
+    int64_t tile = blockIdx.x;
+    if (!set_tile(tile)) return;
+    start_tile();
+    wait_vm<0>();
+    // lane addresses of a slice's first step (of A's and B's rows); the second
+    // step's are those with bit 6 flipped, by the swizzle
+    const int sw0 = r * 128 + ((g ^ ((r >> 1) & 7)) << 4);
+    const int la = wm * T::TM * 128, lb = T::OFF_B + wn * T::TN * 128;
+
+    for (;;) {
+      // this wave's copies of slices 0 and 1 are there (and the last tile's
+      // output is read back)
+      if (tail != 0 && S == 1) zero_tail(0);
+      ring_barrier();
+      v4i acc[FM][FN];
+#pragma unroll
+      for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++) acc[i][j] = v4i{0, 0, 0, 0};
+      i8_fence_init(acc);
+      v4i a0[FM], a1[FM], fb[FN];
+      {
+        const int lane = opaque(threadIdx.x & 63), g = lane >> 4, r = lane & 15;
+        const uint8_t* first = smem + r * 128 + ((g ^ ((r >> 1) & 7)) << 4);
+#pragma unroll
+        for (int f = 0; f < FM; f++) a0[f] = *reinterpret_cast<const v4i*>(first + la + f * 2048);
+#pragma unroll
+        for (int f = 0; f < FN; f++) fb[f] = *reinterpret_cast<const v4i*>(first + lb + f * 2048);
+      }
+      const I8Tile now = t;
+      bool next = false;
+      int ba = 0, s = 0;  // ba: A's buffer of slice s
+      for (; s + 4 < S; s++) {
+        const int bn = ba == 2 ? 0 : ba + 1, bp = ba == 0 ? 2 : ba - 1;
+        // A's slice s + 2, spread over the first step (buffer of slice s - 1)
+        step(acc, a0, a1, fb, smem + ba * T::SZA + la + (sw0 ^ 64), smem + (s & 1) * T::SZB + lb + (sw0 ^ 64),
+             [&](int j) {
+#pragma unroll
+               for (int u = 0; u < T::CA; u++)
+                 if ((u * FN) / T::CA == j) copy_a1(s + 2, bp, 0, u);
+             });
+        step(acc, a1, a0, fb, smem + bn * T::SZA + la + sw0, smem + ((s + 1) & 1) * T::SZB + lb + sw0, [&](int j) {
+          if (j == 1) {
+            // slice 1 is there since the tile's start; the last tile's stores
+            // are waited for with slice 2's copies
+            if (s > 0) wait_vm<T::CA>();
+            ring_barrier();
+          }
+#pragma unroll
+          for (int u = 0; u < T::CB; u++)
+            if (j >= 1 && 1 + (u * (FN - 1)) / T::CB == j) copy_b1(s + 2, 0, u);
+        });
+        ba = bn;
+      }
+      // the last slices: less and less is left to copy
+      for (; s < S; s++) {
+        const int bn = ba == 2 ? 0 : ba + 1, bp = ba == 0 ? 2 : ba - 1;
+        if (s + 2 < S) copy_a(s + 2, bp, back(s + 2));
+        step(acc, a0, a1, fb, smem + ba * T::SZA + la + (sw0 ^ 64), smem + (s & 1) * T::SZB + lb + (sw0 ^ 64),
+             [](int) {});
+        step(acc, a1, a0, fb, smem + bn * T::SZA + la + sw0, smem + ((s + 1) & 1) * T::SZB + lb + sw0, [&](int j) {
+          if (j != 1) return;
+          if (s > 0) {
+            if (s + 2 < S)
+              wait_vm<T::CA>();
+            else
+              wait_vm<0>();
+          }
+          if (tail != 0 && s + 2 == S) zero_tail(bn);
+          ring_barrier();
+          if (s + 2 < S) copy_b(s + 2, back(s + 2));
+          if (s + 1 == S) {
+            tile += gridDim.x;
+            next = set_tile(tile);
+            if (next) start_tile();
+          }
+        });
+        ba = bn;
+      }
+      i8_drain(acc);
+      uint8_t* cst = smem + T::OFF_CST + wave * 4096;
+      if (now.rows != T::BM || (now.tn + 1) * T::BN > a.N || (a.N & 3) != 0)
+        store<-1, 0>(a, now, acc, cst, wm, wn);
+      else if (a.e.act == kActGelu)
+        store_typed<kActGelu>(a, now, acc, cst, wm, wn);
+      else
+        store_typed<kActNone>(a, now, acc, cst, wm, wn);
+      if (!next) return;
+    }
+  }
+
+  // Output: a lane holds 4 columns of row r of each fragment.  16 rows x 64
+  // columns at a time go through 4 KiB of LDS and come back with consecutive
+  // lanes on consecutive columns, so that the stores fill whole lines.
+  // OUT >= 0: all rows and columns of the tile exist, in whole groups of 4, and
+  // type and activation are known here, so that what is run is short (each
+  // tile fetches it anew); OUT < 0: the general form.
+  template <int OUT, int ACT>
+  static __device__ __forceinline__ void store(const I8Args& a, const I8Tile& t, v4i (&acc)[FM][FN], uint8_t* cst,
+                                               int wm, int wn) {
+    constexpr bool FULL = OUT >= 0;
+    Epi e = a.e;
+    if (FULL) {
+      e.out = OUT;
+      e.act = ACT;
+    }
+    const int lane = opaque(threadIdx.x & 63);
+    const int rr = lane >> 4, cc = lane & 15;  // in a fragment: columns 4 rr, row cc; read back: row of 4, chunk
+    const int64_t eb = (int64_t)t.expert * a.N;
+    constexpr int NH = T::TN / 64;
+    const int n0 = t.tn * T::BN + wn * T::TN + cc * 4;
+    const bool vec = FULL || (a.N & 3) == 0;
+    v4f sb[NH], bias[NH];
+#pragma unroll
+    for (int h = 0; h < NH; h++) {
+      const int nc = n0 + h * 64;
+      // -0 leaves every sum as it is
+      bias[h] = v4f{-0.f, -0.f, -0.f, -0.f};
+      if (FULL) {
+        sb[h] = *reinterpret_cast<const v4f*>(a.SB + eb + nc);
+        if (a.e.bias != nullptr) bias[h] = *reinterpret_cast<const v4f*>(a.e.bias + eb + nc);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          sb[h][x] = nc + x < a.N ? a.SB[eb + nc + x] : 0.0f;
+          if (a.e.bias != nullptr && nc + x < a.N) bias[h][x] = a.e.bias[eb + nc + x];
+        }
+      }
+    }
+    float sa[FM];
+#pragma unroll
+    for (int u = 0; u < FM; u++) {
+      const int row = wm * T::TM + 16 * u + cc;
+      sa[u] = FULL || row < t.rows ? a_scale(a, GATHER ? a_row(a, t.row0 + row) : t.row0 + row) : 0.0f;
+    }
+    // the next tile's first copies are older than these loads: none of them
+    // is in flight behind this, and the stores are not waited for with them
+    wait_vm<0>();
+#pragma unroll
+    for (int u = 0; u < FM; u++) {
+#pragma unroll
+      for (int h = 0; h < NH; h++) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          v4f v;
+#pragma unroll
+          for (int x = 0; x < 4; x++) v[x] = rounded_product((float)acc[u][h * 4 + j][x], sa[u]);
+          *reinterpret_cast<v4f*>(cst + cc * 256 + (((j * 4 + rr) ^ cc) << 4)) = v;
+        }
+#pragma unroll FULL ? 4 : 1
+        for (int q = 0; q < 4; q++) {
+          const int br = q * 4 + rr;
+          v4f v = *reinterpret_cast<const v4f*>(cst + br * 256 + ((cc ^ br) << 4));
+          const int orow = wm * T::TM + 16 * u + br, nc = n0 + h * 64;
+          if (FULL || (orow < t.rows && nc < a.N)) {
+#pragma unroll
+            for (int x = 0; x < 4; x++) v[x] = rounded_product(v[x], sb[h][x]) + bias[h][x];
+            if (e.act == kActGelu) {
+#pragma unroll
+              for (int x = 0; x < 4; x++) v[x] = gelu(v[x]);
+            }
+            epi_put4<true>(e, a.N, t.row0 + orow, nc, v, vec);
+          }
+        }
+      }
+    }
+  }
+
+  template <int ACT>
+  static __device__ __forceinline__ void store_typed(const I8Args& a, const I8Tile& t, v4i (&acc)[FM][FN], uint8_t* cst,
+                                                     int wm, int wn) {
+    if (a.e.out == kOutF32)
+      store<kOutF32, ACT>(a, t, acc, cst, wm, wn);
+    else if (a.e.out == kOutBF16)
+      store<kOutBF16, ACT>(a, t, acc, cst, wm, wn);
+    else
+      store<kOutF16, ACT>(a, t, acc, cst, wm, wn);
+  }
+};
+
+template <class T, bool GATHER>
+__global__ __launch_bounds__(T::NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void int8_ring_kernel(I8Args a,
+                                                                                                      int tiles_n) {
+  RingKernel<T, GATHER>::run(a, tiles_n);
+}
+
+template <class T>
+hipError_t launch_ring(const I8Args& a, hipStream_t stream) {
+  const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
+  const int64_t tiles = tiles_n * i8_tiles_m(a, T::BM);
+  if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e != hipSuccess) return e;
+  const int64_t most = (int64_t)cus * T::PER_CU;
+  const dim3 grid((unsigned)(tiles < most ? tiles : most)), block(T::NW * 64);
+  if (a.index != nullptr)
+    hipLaunchKernelGGL((int8_ring_kernel<T, true>), grid, block, 0, stream, a, (int)tiles_n);
+  else
+    hipLaunchKernelGGL((int8_ring_kernel<T, false>), grid, block, 0, stream, a, (int)tiles_n);
+  return hipGetLastError();
+}
+
+// ---- few rows ---------------------------------------------------------------
+//
+// CW x KW waves on a tile of 16 MB rows x 16 CW NB columns: each wave has 16 NB
+// of the columns and every KW-th slice of 128 k (a line of each row).  A stage
+// of LDS holds KW slices, one for each group of waves; D stages are in flight
+// or in use, so that a CU keeps most of its LDS of memory requests going, which
+// is what bounds such products.  The groups' sums are exact and are added
+// through LDS at the end.
+template <int MB_, int NB_, int CW_, int KW_, int D_>
+struct I8Few {
+  static constexpr int MB = MB_, NB = NB_, CW = CW_, KW = KW_, D = D_;
+  static constexpr int BM = 16 * MB, BN = 16 * CW * NB, NW = CW * KW;
+  static constexpr int PART = (BM + BN) * 128, STAGE = KW * PART, LDS = D * STAGE;
+  // copies of 8 rows: RG for a slice, NC for a stage, of which a wave issues
+  // MIN or (the first REM waves) one more
+  static constexpr int RG = (BM + BN) / 8, NC = RG * KW, MIN = NC / NW, REM = NC % NW, MAX = MIN + (REM ? 1 : 0);
+  static_assert(LDS <= 160 * 1024 && LDS >= NW * MB * NB * 1024 && D >= 3, "stages, and the sums of all waves");
+};
+
+template <class T, bool GATHER>
+__global__ __launch_bounds__(T::NW * 64) void int8_few_kernel(I8Args a, int tiles_n) {
+  constexpr int MB = T::MB, NB = T::NB, CW = T::CW, KW = T::KW, NW = T::NW, D = T::D;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cw = wave % CW, kw = wave / CW;
+  const int g = lane >> 4, r = lane & 15;
+  I8Tile t;
+  if (!find_tile(a, T::BM, tiles_n, blockIdx.x, lane, t)) return;
+  const int K = a.K, n0 = t.tn * T::BN, cols = min(T::BN, a.N - n0);
+  const int S = (K + 127) >> 7, tail = K & 127;  // slices
+  const int I = (S + KW - 1) / KW;               // stages
+
+  constexpr int kRsrcWord3 = 0x00020000;
+  const auto rs_a = GATHER
+                        ? __builtin_amdgcn_make_buffer_rsrc((void*)a.A, 0, (int)(uint32_t)(a.rows_a * K), kRsrcWord3)
+                        : __builtin_amdgcn_make_buffer_rsrc((void*)(a.A + t.row0 * K), 0, t.rows * K, kRsrcWord3);
+  const auto rs_b = __builtin_amdgcn_make_buffer_rsrc((void*)(a.B + ((int64_t)t.expert * a.N + n0) * K), 0, cols * K,
+                                                      kRsrcWord3);
+  // Copy u of this wave: rows 8 rg .. of slice kp of the stage, A's rows first.
+  // Rows past the end are fetched as the last one, rows outside A as row 0.
+  uint32_t off[T::MAX];
+#pragma unroll
+  for (int u = 0; u < T::MAX; u++) {
+    const int rg = (wave + NW * u) % T::RG;
+    const int c16 = ((lane & 7) ^ (4 * (rg & 1) + (lane >> 4))) * 16;
+    int64_t row;
+    if (rg < T::BM / 8) {
+      row = min(rg * 8 + (lane >> 3), t.rows - 1);
+      if (GATHER) row = max(a_row(a, t.row0 + row), (int64_t)0);
+    } else {
+      row = min(rg * 8 - T::BM + (lane >> 3), cols - 1);
+    }
+    off[u] = (uint32_t)(row * K) + c16;
+  }
+  auto issue = [&](int i, int stage) {
+#pragma unroll
+    for (int u = 0; u < T::MAX; u++) {
+      const int q = wave + NW * u;
+      if (u < T::MIN || wave < T::REM) {
+        const int kp = q / T::RG, rg = q % T::RG;
+        const int slice = min(i * KW + kp, S - 1);  // past K: not used
+        uint32_t o = off[u];
+        if (tail != 0 && slice == S - 1) {
+          // chunks past K are fetched as the slice's first one
+          const int c16 = ((lane & 7) ^ (4 * (rg & 1) + (lane >> 4))) * 16;
+          if (c16 >= tail) o -= c16;
+        }
+        lds_void* to = (lds_void*)(smem + stage * T::STAGE + kp * T::PART + rg * 1024);
+        if (rg < T::BM / 8)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, to, 16, o, slice * 128, 0, 0);
+        else
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, to, 16, o, slice * 128, 0, 0);
+      }
+    }
+  };
+  v4i acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; i++)
+#pragma unroll
+    for (int j = 0; j < NB; j++) acc[i][j] = v4i{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < D - 1; i++)
+    if (i < I) issue(i, i);
+  const int sw0 = r * 128 + ((g ^ ((r >> 1) & 7)) << 4);
+  int stage = 0;
+  for (int i = 0; i < I; i++) {
+    // this wave's copies of stage i are there, then everybody's; the stage
+    // before has been read by all
+    if (i + D - 2 >= I)
+      wait_vm<0>();
+    else if (wave < T::REM)
+      wait_vm<(D - 2) * T::MAX>();
+    else
+      wait_vm<(D - 2) * T::MIN>();
+    ring_barrier();
+    if (i + D - 1 < I) issue(i + D - 1, stage == 0 ? D - 1 : stage - 1);
+    const int slice = i * KW + kw;
+    if (slice < S) {
+      const uint8_t* pa = smem + stage * T::STAGE + kw * T::PART;
+      const uint8_t* pb = pa + T::BM * 128 + cw * NB * 2048;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int sw = sw0 ^ (64 * h);
+        v4i fa[MB], fb[NB];
+#pragma unroll
+        for (int u = 0; u < MB; u++) fa[u] = *reinterpret_cast<const v4i*>(pa + u * 2048 + sw);
+#pragma unroll
+        for (int j = 0; j < NB; j++) fb[j] = *reinterpret_cast<const v4i*>(pb + j * 2048 + sw);
+        // codes past K count as zeros
+        if (tail != 0 && slice == S - 1 && h * 64 + g * 16 >= tail) {
+#pragma unroll
+          for (int u = 0; u < MB; u++) fa[u] = v4i{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int u = 0; u < MB; u++)
+#pragma unroll
+          for (int j = 0; j < NB; j++) acc[u][j] = mfma_i8(fb[j], fa[u], acc[u][j]);
+      }
+    }
+    stage = stage == D - 1 ? 0 : stage + 1;
+  }
+  // sums of the KW groups, a fragment per wave at a time
+  constexpr int NF = MB * NB * CW;
+  v4i* part = reinterpret_cast<v4i*>(smem);  // [KW][NF][64]
+  ring_barrier();
+#pragma unroll
+  for (int u = 0; u < MB; u++)
+#pragma unroll
+    for (int j = 0; j < NB; j++) part[((kw * NF) + (cw * NB + j) * MB + u) * 64 + lane] = acc[u][j];
+  __syncthreads();
+  for (int f = wave; f < NF; f += NW) {
+    v4i sum = part[f * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < KW; w++) sum += part[(w * NF + f) * 64 + lane];
+    const int row = 16 * (f % MB) + r, n = n0 + 16 * (f / MB) + 4 * g;
+    if (row < t.rows && n < a.N) {
+      const int64_t m = t.row0 + row;
+      store4(a, t.expert, m, n, sum, a_scale(a, GATHER ? a_row(a, m) : m));
+    }
+  }
+}
+
+template <class T>
+hipError_t launch_few(const I8Args& a, hipStream_t stream) {
+  const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
+  const int64_t tiles = tiles_n * i8_tiles_m(a, T::BM);
+  if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)tiles), block(T::NW * 64);
+  if (a.index != nullptr)
+    hipLaunchKernelGGL((int8_few_kernel<T, true>), grid, block, 0, stream, a, (int)tiles_n);
+  else
+    hipLaunchKernelGGL((int8_few_kernel<T, false>), grid, block, 0, stream, a, (int)tiles_n);
+  return hipGetLastError();
+}
+
+// ---- choice -----------------------------------------------------------------
+//
+// Each variant's time is estimated as rounds x (slices x us + extra): tiles over
+// the workgroups that run at once, us per slice of 128 k with the chip full
+// (seven tenths of it where a variant that fits twice on a CU has it for
+// itself), and what a tile costs besides; and as no less than the weights'
+// time from memory.  The smallest estimate is taken, the first of equal ones.
+// The constants are measured; what the choice is worth, in us (bf16 output):
+//   16 x 28672 x 8192      16 x 64: 46.6    32 x 64: 44.5    64 x 128: 50    128 x 128: 60
+//   16 x 4096 x 4096       16 x 16: 6.4     16 x 64: 9.9     32 x 64: 11.6   128 x 128: 20
+//   64 x 4096 x 14336      32 x 32: 21.4    16 x 64: 27      32 x 64: 31     128 x 128: 79
+//   32 x 28672 x 8192      32 x 64: 44.9    16 x 64: 56      64 x 128: 46    128 x 128: 58
+//   64 x 28672 x 8192      64 x 128: 47.5   32 x 64: 64      16 x 64: 85     128 x 128: 59
+//   1024 x 4096 x 4096     128 x 128: 22.8  256 x 128: 26.8  256 x 256: 43   64 x 128: 35
+//   512 x 14336 x 4096     256 x 128: 33    128 x 128: 41    256 x 256: 49
+//   8192 x 14336 x 4096    256 x 256: 389   256 x 128: 432   128 x 128: 493
+//   16 tokens x 4 of 64 experts of 2048 x 4096    16 x 64: 66   16 x 16: 85   32 x 64: 71   64 x 128: 92
+//   2048 tokens x 4 of 16 of 4096 x 2048          128 x 128: 118   256 x 256: 122   64 x 128: 242
+struct Variant {
+  int bm, bn, per_cu;
+  double us, extra;
+  hipError_t (*launch)(const I8Args&, hipStream_t);
+};
+using Tile16x16 = I8Few<1, 1, 1, 4, 5>;
+using Tile16x64 = I8Few<1, 1, 4, 2, 4>;
+using Tile32x32 = I8Few<2, 1, 2, 4, 4>;
+using Tile32x64 = I8Few<2, 1, 4, 2, 3>;
+using Tile64x128 = I8Few<4, 2, 4, 2, 3>;
+using Tile128x128 = I8Cfg<128, 128, 2, 2>;
+using Tile256x128 = I8Cfg<256, 128, 4, 2>;
+using Tile256x256 = I8Cfg<256, 256, 4, 2>;
+
+const Variant kVariants[] = {
+    {16, 16, 2, 0.18, 1.8, launch_few<Tile16x16>},    {16, 64, 2, 0.42, 1.5, launch_few<Tile16x64>},
+    {32, 32, 1, 0.19, 2.4, launch_few<Tile32x32>},    {32, 64, 2, 0.52, 1.5, launch_few<Tile32x64>},
+    {64, 128, 1, 0.70, 1.0, launch_few<Tile64x128>},  {128, 128, 2, 1.00, 2.0, launch_ring<Tile128x128>},
+    {256, 128, 1, 0.87, 3.0, launch_ring<Tile256x128>}, {256, 256, 1, 1.45, 8.0, launch_ring<Tile256x256>}};
+
+constexpr double kCus = 256, kBytesPerUs = 5.2e6;
+
+double estimate(const Variant& v, const I8Args& a) {
+  // by expert the rows' split is not known here: half a tile more for each
+  // expert that can have rows
+  const double experts = a.offsets == nullptr ? 0.0 : (double)(a.E < a.M ? a.E : a.M);
+  const double tiles_m =
+      a.offsets == nullptr ? (double)((a.M + v.bm - 1) / v.bm) : (double)a.M / v.bm + 0.5 * experts;
+  const double tiles = tiles_m * (double)((a.N + v.bn - 1) / v.bn);
+  const double full = tiles / (kCus * v.per_cu);
+  const double rounds = full > 4.0 ? full + 0.5 : __builtin_ceil(full);
+  const double us = v.per_cu == 2 && tiles <= kCus ? 0.7 * v.us : v.us;
+  const double t = rounds * ((a.K + 127) / 128 * us + v.extra);
+  // experts that get rows when m rows fall on E of them evenly: E m / (m + 0.6 E)
+  const double used = a.offsets == nullptr ? 1.0 : (double)a.E * a.M / (a.M + 0.6 * a.E);
+  const double floor = used * a.N * a.K / kBytesPerUs;
+  return t > floor ? t : floor;
+}
+
+hipError_t launch_gathered_far(const I8Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + kBN - 1) / kBN;
   const int64_t tiles = tiles_n * i8_tiles_m(a, kBM);
   if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(int8_tile_kernel, dim3((unsigned)tiles), dim3(256), 0, stream, a, (int)tiles_n);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_int8(const I8Args& a, hipStream_t stream) {
+  // gathered rows are addressed by 32-bit offsets from A's start
+  if (a.index != nullptr && a.rows_a * a.K >= ((int64_t)1 << 32)) return launch_gathered_far(a, stream);
+  const Variant* best = nullptr;
+  double least = 0.0;
+  for (const Variant& v : kVariants) {
+    const double t = estimate(v, a);
+    if (best == nullptr || t < least) {
+      best = &v;
+      least = t;
+    }
+  }
+  return best->launch(a, stream);
 }
 
 }  // namespace mxg

@@ -37,23 +37,61 @@ inline int64_t i8_tiles_m(const I8Args& a, int bm) {
 
 struct I8Tile {
   int64_t row0;  // first row of C
-  int rows;      // rows of this tile (0: no such tile)
+  int rows;      // rows of this tile
   int expert;
+  int tn;        // column tile
 };
 
-// The tile `tm` of the experts' tiles of bm rows, by one wave: each lane takes
-// a run of experts, and the lane whose run holds the tile writes it.  The
-// offsets count as kept inside 0 .. M and never falling (each at least the
-// largest before it), so that whatever they hold, no row has two experts.
-__device__ __forceinline__ void find_tile(const I8Args& a, int bm, int tm, int lane, I8Tile* out) {
+// Workgroup id -> tile id: workgroups are dispatched round-robin over the 8
+// XCDs, so each XCD gets a contiguous range of tile ids; within the range,
+// groups of 8 row tiles take the column tiles in turn, so that what runs at
+// once on an XCD shares rows of A and of B in its L2.
+__device__ __forceinline__ void tile_order(int bid, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int total = tiles_m * tiles_n;
+  const int x = bid & 7, rem = total & 7;
+  const int id = x * (total >> 3) + min(x, rem) + (bid >> 3);
+  const int group = id / (8 * tiles_n);
+  const int first = group * 8;
+  const int rows = min(tiles_m - first, 8);
+  const int in = id - group * 8 * tiles_n;
+  tm = first + in % rows;
+  tn = in / rows;
+}
+
+// Inclusive scans over the lanes of a wave by DPP (shifts within rows of 16,
+// then the rows' last values passed on): a few cycles a step, where a shuffle
+// goes through LDS.
+template <bool MAX>
+__device__ __forceinline__ int scan_op(int x, int y) {
+  return MAX ? max(x, y) : x + y;
+}
+template <bool MAX>
+__device__ __forceinline__ int wave_scan(int x) {  // MAX: values of at least 0
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
+  return x;
+}
+
+// Tile `bid` in that order, found by a wave (every lane gets it); false if
+// there is none.  By expert, each lane takes a run of experts and the lane
+// whose run holds the tile passes it on.  The offsets count as kept inside
+// 0 .. M and never falling (each at least the largest before it), so that
+// whatever they hold, no row has two experts.
+__device__ __forceinline__ bool find_tile(const I8Args& a, int bm, int tiles_n, int64_t bid, int lane, I8Tile& t) {
   const int M = (int)a.M;
+  int tm;
   if (a.offsets == nullptr) {
-    if (lane == 0) {
-      const int64_t row0 = (int64_t)tm * bm;
-      const int64_t left = a.M - row0;
-      *out = I8Tile{row0, left < bm ? (int)left : bm, 0};
-    }
-    return;
+    const int tiles_m = (M + bm - 1) / bm;
+    if (bid >= (int64_t)tiles_m * tiles_n) return false;
+    tile_order((int)bid, tiles_m, tiles_n, tm, t.tn);
+    t.row0 = (int64_t)tm * bm;
+    t.rows = min(M - tm * bm, bm);
+    t.expert = 0;
+    return true;
   }
   const int per = (a.E + 63) / 64;
   const int e0 = lane * per, e1 = min(e0 + per, a.E);
@@ -61,11 +99,7 @@ __device__ __forceinline__ void find_tile(const I8Args& a, int bm, int tm, int l
   int top = 0;
   for (int e = e0; e < e1; e++) top = max(top, min(a.offsets[e + 1], M));
   if (lane == 0) top = max(top, min(a.offsets[0], M));
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(top, d);
-    if (lane >= d) top = max(top, o);
-  }
+  top = wave_scan<true>(top);
   int first = __shfl_up(top, 1);
   if (lane == 0) first = max(0, min(a.offsets[0], M));
   int mine = 0;
@@ -75,28 +109,33 @@ __device__ __forceinline__ void find_tile(const I8Args& a, int bm, int tm, int l
     mine += (hi - lo + bm - 1) / bm;
     lo = hi;
   }
-  int before = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(before, d);
-    if (lane >= d) before += o;
-  }
-  const int total = __shfl(before, 63);
+  int before = wave_scan<false>(mine);
+  const int total = __builtin_amdgcn_readlane(before, 63);
+  if (bid >= (int64_t)total * tiles_n) return false;
+  tile_order((int)bid, total, tiles_n, tm, t.tn);
   before -= mine;
-  if (lane == 0 && tm >= total) *out = I8Tile{0, 0, 0};
-  if (tm < before || tm >= before + mine) return;
-  lo = first;
-  for (int e = e0; e < e1; e++) {
-    const int hi = max(lo, min(a.offsets[e + 1], M));
-    const int n = (hi - lo + bm - 1) / bm;
-    if (tm < before + n) {
-      const int row0 = lo + (tm - before) * bm;
-      *out = I8Tile{row0, min(hi - row0, bm), e};
-      return;
+  int row0 = 0, rows = 0, expert = 0;
+  const bool holds = tm >= before && tm < before + mine;
+  if (holds) {
+    lo = first;
+    for (int e = e0; e < e1; e++) {
+      const int hi = max(lo, min(a.offsets[e + 1], M));
+      const int n = (hi - lo + bm - 1) / bm;
+      if (tm < before + n) {
+        row0 = lo + (tm - before) * bm;
+        rows = min(hi - row0, bm);
+        expert = e;
+        break;
+      }
+      before += n;
+      lo = hi;
     }
-    before += n;
-    lo = hi;
   }
+  const int src = __builtin_ctzll(__ballot(holds));
+  t.row0 = __builtin_amdgcn_readlane(row0, src);
+  t.rows = __builtin_amdgcn_readlane(rows, src);
+  t.expert = __builtin_amdgcn_readlane(expert, src);
+  return true;
 }
 
 // Row of A that row p of C takes; -1 for an index outside A.
@@ -114,6 +153,13 @@ __device__ __forceinline__ float a_scale(const I8Args& a, int64_t row) {
 
 __device__ __forceinline__ v4i mfma_i8(const v4i& x, const v4i& y, const v4i& c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, c, 0, 0, 0);
+}
+
+// A product that is rounded before a sum takes it up (no fma), so that every
+// kernel gives the same bits.
+__device__ __forceinline__ float rounded_product(float x, float y) {
+#pragma clang fp contract(off)
+  return x * y;
 }
 
 // Output step of 4 columns n .. n+3 of row m: the sum rounded to fp32 (one
@@ -135,7 +181,7 @@ __device__ __forceinline__ void store4(const I8Args& a, int expert, int64_t m, i
   }
   v4f v;
 #pragma unroll
-  for (int i = 0; i < 4; i++) v[i] = ((float)sum[i] * s) * c[i];
+  for (int i = 0; i < 4; i++) v[i] = rounded_product(rounded_product((float)sum[i], s), c[i]);
   epi_store4<false>(e, a.N, m, n, v, vec);
 }
 

@@ -313,6 +313,23 @@ def test_weights_past_4_gib():
         assert torch.equal(got[e], want), e
 
 
+def test_gathered_rows_past_4_gib():
+    say("gathered rows past 4 GiB")
+    b = binding()
+    T, K, N, E = 262144 + 70, 16384, 100, 3
+    a = torch.empty((T, K), dtype=torch.int8, device=DEV)
+    index = torch.tensor([T - 1, 0, 262143, 262144, T, -1, 131072, T - 1], dtype=torch.int32, device=DEV)
+    rows = index[[0, 1, 2, 3, 6]].long()
+    a[rows] = torch.empty((5, K), dtype=torch.int8, device=DEV).random_(-128, 128)
+    w = torch.empty((E, N, K), dtype=torch.int8, device=DEV).random_(-128, 128)
+    off = torch.tensor([0, 3, 3, 8], dtype=torch.int32, device=DEV)
+    got = b.int8gemm_run_grouped(a, torch.ones(T, device=DEV), w, torch.ones(E, N, device=DEV), off, index=index)
+    for p, e in ((0, 0), (1, 0), (2, 0), (3, 2), (6, 2), (7, 2)):
+        want = (a[int(index[p])].double()[None] @ w[e].double().t())[0].float()
+        assert torch.equal(got[p], want), p
+    assert torch.isnan(got[4:6]).all()
+
+
 def test_output_past_4_gib():
     say("output past 4 GiB")
     b = binding()
