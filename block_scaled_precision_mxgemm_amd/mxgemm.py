@@ -310,7 +310,7 @@ def _arg(t, name: str, dtypes, shape=None, dim: int | None = None, like: torch.T
         raise ValueError(name + " must be a GPU tensor")
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, not %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
     if dim is not None and t.dim() != dim:
         raise ValueError("%s must have %d dimensions" % (name, dim))
@@ -334,11 +334,26 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (2 us less per
+# call, of about 9), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _call(name: str, device: torch.device, stream, *args):
     """An entry point on the operands' own device; without a stream, on that
     device's current one."""
-    with torch.cuda.device(device):
-        _check(getattr(_load(), name)(*args, _stream(stream)), name)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(name, device, stream, *args)
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = torch.cuda.current_stream().cuda_stream
+    rc = getattr(_load(), name)(*args, handle)
+    if rc:
+        _check(rc, name)
 
 
 def int8gemm_quantize(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tensor | None = None, stream=None):
