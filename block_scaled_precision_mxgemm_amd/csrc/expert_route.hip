@@ -443,8 +443,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
 constexpr int kPlanWaves = 16;
 constexpr int kPlanThreads = kPlanWaves * 64;
 constexpr int kMaxExperts = 1024;
-// One workgroup alone takes 9 us for 4096 slots and 150 us for 131072; the two
-// kernels together about 12 us up to there.
+// One workgroup alone takes 7.4 us for 4096 slots of 128 experts and 1.1 us for
+// each 1000 more (131072: 150); the two kernels 7.8 us for 6000, 10.5 for
+// 131072 and 22 for 2^20.
 constexpr int64_t kPlanRun = 4096;
 constexpr int64_t kPlanRuns = 256;
 
