@@ -257,7 +257,7 @@ int int8gemm_run(const int8_t* A, const float* scaleA, const int8_t* B, const fl
                  int64_t N, int64_t K, const float* bias, int act, int out_type, void* stream) {
   if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return MXG_EINVAL;
   return run_int8(mxg::I8Args{A, scaleA, M, B, scaleB, mxg::Epi{C, bias, out_type, act}, M, (int)N, (int)K, 1, nullptr,
-                              nullptr, 1},
+                              nullptr, 1, 0, 0},
                   bias, act, out_type, (hipStream_t)stream);
 }
 
@@ -269,7 +269,7 @@ int int8gemm_run_grouped(const int8_t* A, const float* scaleA, int64_t rowsA, co
   if (!dim_ok(N) || !dim_ok(K) || E < 1 || E > MXG_MAX_EXPERTS || index_div < 1) return MXG_EINVAL;
   if (index == nullptr && rowsA < rows) return MXG_EINVAL;
   return run_int8(mxg::I8Args{A, scaleA, rowsA, B, scaleB, mxg::Epi{C, bias, out_type, act}, rows, (int)N, (int)K,
-                              (int)E, offsets, index, index_div},
+                              (int)E, offsets, index, index_div, 0, 0},
                   bias, act, out_type, (hipStream_t)stream);
 }
 

@@ -4,8 +4,9 @@
 // Sums are in fp32, j ascending.  A position outside 0 .. rows-1 (a slot
 // without an expert) adds nothing, and its weight's gradient is zero.
 //
-// Rows whose bytes are a multiple of 16 move in 16-byte pieces, others by
-// element.
+// Both are bound by the rows' bytes.  A lane takes 8 columns; rows of any length
+// start at any element's address (global memory takes such vectors in one
+// instruction), and only a row's last columns go by element.
 #include "mxg_internal.h"
 #include "mxg_rows.h"
 
@@ -13,17 +14,19 @@ namespace mxg {
 namespace {
 
 constexpr int kCThreads = 256;
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
 
-// 8 columns n .. n+7 of a row, fp32; `vec`: whole 16-byte pieces
+// 8 columns n .. n+7 of a row, fp32; zeros past its end
 template <int TYPE>
-__device__ __forceinline__ void load8(const void* base, int64_t row, int64_t N, int64_t n, bool vec, float (&f)[8]) {
+__device__ __forceinline__ void load8(const void* base, int64_t row, int64_t N, int64_t n, float (&f)[8]) {
   using E = RowElem<TYPE>;
   const auto* p = reinterpret_cast<const typename E::type*>(base) + row * N + n;
-  if (vec) {
+  if (n + 7 < N) {
 #pragma unroll
     for (int h = 0; h < 8 / E::VEC; h++) {
       float x[E::VEC];
-      unpack16<TYPE>(*reinterpret_cast<const v4i*>(p + h * E::VEC), x);
+      const v4i w = *reinterpret_cast<const v4i_any*>(p + h * E::VEC);
+      unpack16<TYPE>(w, x);
 #pragma unroll
       for (int i = 0; i < E::VEC; i++) f[h * E::VEC + i] = x[i];
     }
@@ -33,16 +36,16 @@ __device__ __forceinline__ void load8(const void* base, int64_t row, int64_t N, 
   }
 }
 template <int TYPE>
-__device__ __forceinline__ void save8(void* base, int64_t row, int64_t N, int64_t n, bool vec, const float (&f)[8]) {
+__device__ __forceinline__ void save8(void* base, int64_t row, int64_t N, int64_t n, const float (&f)[8]) {
   using E = RowElem<TYPE>;
   auto* p = reinterpret_cast<typename E::type*>(base) + row * N + n;
-  if (vec) {
+  if (n + 7 < N) {
 #pragma unroll
     for (int h = 0; h < 8 / E::VEC; h++) {
       float x[E::VEC];
 #pragma unroll
       for (int i = 0; i < E::VEC; i++) x[i] = f[h * E::VEC + i];
-      *reinterpret_cast<v4i*>(p + h * E::VEC) = pack16<TYPE>(x);
+      *reinterpret_cast<v4i_any*>(p + h * E::VEC) = pack16<TYPE>(x);
     }
   } else {
 #pragma unroll
@@ -51,25 +54,34 @@ __device__ __forceinline__ void save8(void* base, int64_t row, int64_t N, int64_
   }
 }
 
+// A workgroup per token and 2048 columns: the positions and weights are the
+// same for all its lanes, and the rows of 4 choices are loaded at a time.
 template <int Y, int O>
 __global__ __launch_bounds__(kCThreads) void combine_kernel(CombineArgs a) {
-  const bool vec = (a.N & 7) == 0;
-  const int64_t nq = (a.N + 7) >> 3;
-  const int64_t total = a.T * nq;
-  for (int64_t u = (int64_t)blockIdx.x * kCThreads + threadIdx.x; u < total; u += (int64_t)gridDim.x * kCThreads) {
-    const int64_t t = u / nq, n = (u - t * nq) << 3;
-    float s[8] = {};
-    for (int j = 0; j < a.k; j++) {
-      const int p = a.position[t * a.k + j];
-      if (p < 0 || p >= a.rows) continue;
-      const float w = a.weights[t * a.k + j];
-      float y[8];
-      load8<Y>(a.Y, p, a.N, n, vec, y);
+  const int64_t t = blockIdx.x;
+  const int64_t n = ((int64_t)blockIdx.y * kCThreads + threadIdx.x) * 8;
+  if (n >= a.N) return;
+  const int32_t* pos = a.position + t * a.k;
+  const float* wt = a.weights + t * a.k;
+  float s[8] = {};
+  for (int j = 0; j < a.k; j += 4) {
+    float y[4][8];
+    bool there[4];
 #pragma unroll
-      for (int i = 0; i < 8; i++) s[i] = fmaf(w, y[i], s[i]);
+    for (int u = 0; u < 4; u++) {
+      const int p = j + u < a.k ? pos[j + u] : -1;
+      there[u] = p >= 0 && p < a.rows;
+      if (there[u]) load8<Y>(a.Y, p, a.N, n, y[u]);
     }
-    save8<O>(a.out, t, a.N, n, vec, s);
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+      if (there[u]) {
+        const float w = wt[j + u];
+#pragma unroll
+        for (int i = 0; i < 8; i++) s[i] = fmaf(w, y[u][i], s[i]);
+      }
   }
+  save8<O>(a.out, t, a.N, n, s);
 }
 
 // one wave per slot
@@ -83,19 +95,18 @@ __global__ __launch_bounds__(kCThreads) void combine_backward_kernel(CombineArgs
   const int p = a.position[slot];
   const bool live = p >= 0 && p < a.rows;
   const float w = live ? a.weights[slot] : 0.0f;
-  const bool vec = (a.N & 7) == 0;
   float dot = 0.0f;
   if (live)
     for (int64_t n = lane * 8; n < a.N; n += 512) {
       float d[8], y[8];
-      load8<O>(a.out, t, a.N, n, vec, d);
-      load8<Y>(a.Y, p, a.N, n, vec, y);
+      load8<O>(a.out, t, a.N, n, d);
+      load8<Y>(a.Y, p, a.N, n, y);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         dot = fmaf(d[i], y[i], dot);
         d[i] *= w;
       }
-      save8<Y>(dY, p, a.N, n, vec, d);
+      save8<Y>(dY, p, a.N, n, d);
     }
   dot = wave_sum(dot);
   if (lane == 0) dW[slot] = dot;
@@ -107,9 +118,8 @@ hipError_t combine_launch(const CombineArgs& a, void* dY, float* dW, hipStream_t
     const int64_t grid = (a.T * a.k + kCThreads / 64 - 1) / (kCThreads / 64);
     hipLaunchKernelGGL((combine_backward_kernel<Y, O>), dim3((unsigned)grid), dim3(kCThreads), 0, stream, a, dY, dW);
   } else {
-    int64_t grid = (a.T * ((a.N + 7) >> 3) + kCThreads - 1) / kCThreads;
-    if (grid > 256 * 64) grid = 256 * 64;
-    hipLaunchKernelGGL((combine_kernel<Y, O>), dim3((unsigned)grid), dim3(kCThreads), 0, stream, a);
+    const unsigned cols = (unsigned)((a.N + kCThreads * 8 - 1) / (kCThreads * 8));
+    hipLaunchKernelGGL((combine_kernel<Y, O>), dim3((unsigned)a.T, cols), dim3(kCThreads), 0, stream, a);
   }
   return hipGetLastError();
 }

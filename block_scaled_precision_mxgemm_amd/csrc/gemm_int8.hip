@@ -342,7 +342,7 @@ struct RingKernel {
       }
       i8_drain(acc);
       uint8_t* cst = smem + T::OFF_CST + wave * 4096;
-      if (now.rows != T::BM || (now.tn + 1) * T::BN > a.N || (a.N & 3) != 0)
+      if (now.rows != T::BM || (now.tn + 1) * T::BN > a.N)
         store<-1, 0>(a, now, acc, cst, wm, wn);
       else if (a.e.act == kActGelu)
         store_typed<kActGelu>(a, now, acc, cst, wm, wn);
@@ -355,8 +355,7 @@ struct RingKernel {
   // Output: a lane holds 4 columns of row r of each fragment.  16 rows x 64
   // columns at a time go through 4 KiB of LDS and come back with consecutive
   // lanes on consecutive columns, so that the stores fill whole lines.
-  // OUT >= 0: all rows and columns of the tile exist, in whole groups of 4, and
-  // type and activation are known here, so that what is run is short (each
+  // OUT >= 0: all rows and columns of the tile exist, and type and activation are known here, so that what is run is short (each
   // tile fetches it anew); OUT < 0: the general form.
   template <int OUT, int ACT>
   static __device__ __forceinline__ void store(const I8Args& a, const I8Tile& t, v4i (&acc)[FM][FN], uint8_t* cst,
@@ -372,7 +371,6 @@ struct RingKernel {
     const int64_t eb = (int64_t)t.expert * a.N;
     constexpr int NH = T::TN / 64;
     const int n0 = t.tn * T::BN + wn * T::TN + cc * 4;
-    const bool vec = FULL || (a.N & 3) == 0;
     v4f sb[NH], bias[NH];
 #pragma unroll
     for (int h = 0; h < NH; h++) {
@@ -380,14 +378,11 @@ struct RingKernel {
       // -0 leaves every sum as it is
       bias[h] = v4f{-0.f, -0.f, -0.f, -0.f};
       if (FULL) {
-        sb[h] = *reinterpret_cast<const v4f*>(a.SB + eb + nc);
-        if (a.e.bias != nullptr) bias[h] = *reinterpret_cast<const v4f*>(a.e.bias + eb + nc);
+        sb[h] = *reinterpret_cast<const v4f_any*>(a.SB + eb + nc);
+        if (a.e.bias != nullptr) bias[h] = *reinterpret_cast<const v4f_any*>(a.e.bias + eb + nc);
       } else {
-#pragma unroll
-        for (int x = 0; x < 4; x++) {
-          sb[h][x] = nc + x < a.N ? a.SB[eb + nc + x] : 0.0f;
-          if (a.e.bias != nullptr && nc + x < a.N) bias[h][x] = a.e.bias[eb + nc + x];
-        }
+        sb[h] = load_columns(a.SB + eb, nc, a.N, 0.0f);
+        if (a.e.bias != nullptr) bias[h] = load_columns(a.e.bias + eb, nc, a.N, 0.0f);
       }
     }
     float sa[FM];
@@ -422,7 +417,7 @@ struct RingKernel {
 #pragma unroll
               for (int x = 0; x < 4; x++) v[x] = gelu(v[x]);
             }
-            epi_put4<true>(e, a.N, t.row0 + orow, nc, v, vec);
+            store_columns<true>(e, a.N, t.row0 + orow, nc, v);
           }
         }
       }
@@ -688,7 +683,9 @@ hipError_t launch_gathered_far(const I8Args& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_int8(const I8Args& a, hipStream_t stream) {
+hipError_t launch_int8(const I8Args& args, hipStream_t stream) {
+  I8Args a = args;
+  set_division(a);
   // gathered rows are addressed by 32-bit offsets from A's start
   if (a.index != nullptr && a.rows_a * a.K >= ((int64_t)1 << 32)) return launch_gathered_far(a, stream);
   const Variant* best = nullptr;

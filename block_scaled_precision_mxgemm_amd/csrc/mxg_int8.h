@@ -26,7 +26,20 @@ struct I8Args {
   const int32_t* offsets;   // E + 1
   const int32_t* index;     // M, or nullptr
   int index_div;
+  // i / index_div for 0 <= i < 2^31 is i * div_mul >> div_shift (set_division)
+  uint32_t div_mul;
+  int div_shift;
 };
+
+// With 2^(s-1) < d <= 2^s and m = floor(2^(31+s) / d) + 1, m d exceeds 2^(31+s)
+// by at most d <= 2^s, so i m / 2^(31+s) exceeds i / d by less than 1 / d for
+// i < 2^31, and its floor is that of i / d.
+inline void set_division(I8Args& a) {
+  int s = 0;
+  while (((int64_t)1 << s) < a.index_div) s++;
+  a.div_mul = (uint32_t)(((uint64_t)1 << (31 + s)) / (uint32_t)a.index_div + 1);
+  a.div_shift = 31 + s;
+}
 
 // Tiles of `bm` rows that any offsets can ask for.
 inline int64_t i8_tiles_m(const I8Args& a, int bm) {
@@ -142,7 +155,7 @@ __device__ __forceinline__ bool find_tile(const I8Args& a, int bm, int tiles_n, 
 __device__ __forceinline__ int64_t a_row(const I8Args& a, int64_t p) {
   if (a.index == nullptr) return p;
   const int i = a.index[p];
-  const int64_t row = i < 0 ? -1 : i / a.index_div;
+  const int64_t row = i < 0 ? -1 : (int64_t)(((uint64_t)(uint32_t)i * a.div_mul) >> a.div_shift);
   return row < a.rows_a ? row : -1;
 }
 
@@ -162,27 +175,70 @@ __device__ __forceinline__ float rounded_product(float x, float y) {
   return x * y;
 }
 
+// Vectors at any element's address: rows of C, of the scales and of the bias
+// start there when N is not a multiple of 4 (global memory takes such accesses
+// in one instruction).
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef int v2i_any __attribute__((ext_vector_type(2), aligned(2)));
+
+// Values p[0 .. 3] of a row's columns n .. n+3, `other` past its end.
+__device__ __forceinline__ v4f load_columns(const float* p, int n, int N, float other) {
+  if (n + 3 < N) return *reinterpret_cast<const v4f_any*>(p + n);
+  v4f v;
+#pragma unroll
+  for (int i = 0; i < 4; i++) v[i] = n + i < N ? p[n + i] : other;
+  return v;
+}
+
+// Store of 4 finished values to C[m][n .. n+3]; past the row's end nothing.
+template <bool NT>
+__device__ __forceinline__ void store_columns(Epi e, int64_t N, int64_t m, int n, v4f v) {
+  if (e.out == kOutF32) {
+    float* p = reinterpret_cast<float*>(e.C) + m * N + n;
+    if (n + 3 < N) {
+      if (NT)
+        __builtin_nontemporal_store((v4f_any)v, reinterpret_cast<v4f_any*>(p));
+      else
+        *reinterpret_cast<v4f_any*>(p) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; i++)
+        if (n + i < N) p[i] = v[i];
+    }
+    return;
+  }
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) h[i] = e.out == kOutBF16 ? bf16_bits(v[i]) : f16_bits(v[i]);
+  uint16_t* p = reinterpret_cast<uint16_t*>(e.C) + m * N + n;
+  if (n + 3 < N) {
+    const v2i_any w = {(int)(h[0] | (h[1] << 16)), (int)(h[2] | (h[3] << 16))};
+    if (NT)
+      __builtin_nontemporal_store(w, reinterpret_cast<v2i_any*>(p));
+    else
+      *reinterpret_cast<v2i_any*>(p) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; i++)
+      if (n + i < N) p[i] = (uint16_t)h[i];
+  }
+}
+
 // Output step of 4 columns n .. n+3 of row m: the sum rounded to fp32 (one
 // rounding of at most 2^-24 of it; exact below 2^24), times the row's scale,
 // times the column's, then bias, activation and the output type.
 __device__ __forceinline__ void store4(const I8Args& a, int expert, int64_t m, int n, const v4i& sum, float s) {
   const int64_t base = (int64_t)expert * a.N;
-  const bool vec = (a.N & 3) == 0;
-  Epi e = a.e;
-  if (e.bias != nullptr) e.bias += base;
-  const float* sb = a.SB + base;
-  v4f c = {0.f, 0.f, 0.f, 0.f};
-  if (vec) {
-    c = *reinterpret_cast<const v4f*>(sb + n);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-      if (n + i < a.N) c[i] = sb[n + i];
-  }
+  const v4f c = load_columns(a.SB + base, n, a.N, 0.0f);
   v4f v;
 #pragma unroll
   for (int i = 0; i < 4; i++) v[i] = rounded_product(rounded_product((float)sum[i], s), c[i]);
-  epi_store4<false>(e, a.N, m, n, v, vec);
+  if (a.e.bias != nullptr) v += load_columns(a.e.bias + base, n, a.N, 0.0f);
+  if (a.e.act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = gelu(v[i]);
+  }
+  store_columns<false>(a.e, a.N, m, n, v);
 }
 
 }  // namespace mxg
