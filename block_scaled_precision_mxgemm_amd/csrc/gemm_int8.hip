@@ -79,31 +79,34 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(I8Args a, int tiles_n) {
 //
 // WM x WN waves, two per SIMD, each with a TM x TN part of the tile in 16 x 16
 // fragments.  K goes by slices of 128 (whole 128-byte lines of each row) in
-// two steps of 64; LDS holds three slices of A and two of B, filled by direct
+// two steps of 64; LDS holds DB slices of B and one more of A, filled by direct
 // global -> LDS copies.  While a wave runs the MFMAs of one step on registers
 // it reads the fragments of the next step from LDS, so only one barrier per
 // slice is needed: behind the first step's MFMAs, when slice s has been read
-// by all and slice s + 1 has arrived.  The copies of slice s + 2 are spread over
+// by all and slice s + 1 has arrived.  The copies of slice s + DB are spread over
 // the steps, so that their issue does not hold up the MFMAs: B's behind the
 // barrier, into the buffer that slice s left, A's (into the buffer of slice
 // s - 1) in the step before.
 //
 // A workgroup takes tile after tile; the first copies of the next tile are
 // issued before the last step of the present one, and its output goes through
-// the third A buffer, which those copies leave alone.
-template <int BM_, int BN_, int WM_, int WN_>
+// the last A buffer, which those copies leave alone.
+template <int BM_, int BN_, int WM_, int WN_, int DB_ = 2>
 struct I8Cfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int DB = DB_, DA = DB + 1;       // slices of B and of A in LDS
   static constexpr int NW = WM * WN;                // waves
   static constexpr int TM = BM / WM, TN = BN / WN;  // a wave's part of the tile
   static constexpr int FM = TM / 16, FN = TN / 16;  // and its fragments
   static constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KiB copies of a wave and slice
   static constexpr int SZA = BM * 128, SZB = BN * 128;
-  static constexpr int OFF_B = 3 * SZA;
-  // output staging, 4 KiB per wave: the third A buffer, or its own
+  static constexpr int OFF_B = DA * SZA;
+  // output staging, 4 KiB per wave: the last A buffer, or its own
   static constexpr bool OWN = SZA < NW * 4096;
-  static constexpr int OFF_CST = OWN ? OFF_B + 2 * SZB : 2 * SZA;
-  static constexpr int LDS = OFF_B + 2 * SZB + (OWN ? NW * 4096 : 0);
+  static constexpr int OFF_CST = OWN ? OFF_B + DB * SZB : DB * SZA;
+  static constexpr int LDS = OFF_B + DB * SZB + (OWN ? NW * 4096 : 0);
+  // copies issued after slice s + 1's when it is waited for in slice s
+  static constexpr int NEWER = (DB - 2) * (CA + CB) + CA;
   static constexpr int PER_CU = LDS > 80 * 1024 ? 1 : LDS > 40 * 1024 ? 2 : 4;  // workgroups
   static_assert(LDS <= 160 * 1024, "fits the 160 KiB LDS of a gfx950 CU");
   static_assert(CA * NW * 8 == BM && CB * NW * 8 == BN && NW % 2 == 0, "copies split evenly over the waves");
@@ -228,18 +231,18 @@ struct RingKernel {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, (lds_void*)(smem + buf * T::SZA + (wave + T::NW * u) * 1024), 16,
                                                o - b, slice * 128, 0, 0);
     };
-    auto copy_b1 = [&](int slice, uint32_t b, int u) {
+    auto copy_b1 = [&](int slice, int buf, uint32_t b, int u) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs_b, (lds_void*)(smem + T::OFF_B + (slice & 1) * T::SZB + (wave + T::NW * u) * 1024), 16,
+          rs_b, (lds_void*)(smem + T::OFF_B + buf * T::SZB + (wave + T::NW * u) * 1024), 16,
           min(off0 + u * rows_step, lim_b) - b, slice * 128, 0, 0);
     };
     auto copy_a = [&](int slice, int buf, uint32_t b) {
 #pragma unroll
       for (int u = 0; u < T::CA; u++) copy_a1(slice, buf, b, u);
     };
-    auto copy_b = [&](int slice, uint32_t b) {
+    auto copy_b = [&](int slice, int buf, uint32_t b) {
 #pragma unroll
-      for (int u = 0; u < T::CB; u++) copy_b1(slice, b, u);
+      for (int u = 0; u < T::CB; u++) copy_b1(slice, buf, b, u);
     };
     // zeros over the chunks of A past K that this lane fetched (their
     // products vanish whatever B's are)
@@ -253,26 +256,30 @@ struct RingKernel {
       }
     };
     auto start_tile = [&]() {
-      copy_a(0, 0, back(0));
-      copy_b(0, back(0));
-      if (S > 1) {
-        copy_a(1, 1, back(1));
-        copy_b(1, back(1));
-      }
+#pragma unroll
+      for (int i = 0; i < T::DB; i++)
+        if (i < S) {
+          copy_a(i, i, back(i));
+          copy_b(i, i, back(i));
+        }
     };
 
     int64_t tile = blockIdx.x;
     if (!set_tile(tile)) return;
     start_tile();
-    wait_vm<0>();
+    bool first = true;
+    if (S >= T::DB)
+      wait_vm<(T::DB - 1) * (T::CA + T::CB)>();
+    else
+      wait_vm<0>();
     // lane addresses of a slice's first step (of A's and B's rows); the second
     // step's are those with bit 6 flipped, by the swizzle
     const int sw0 = r * 128 + ((g ^ ((r >> 1) & 7)) << 4);
     const int la = wm * T::TM * 128, lb = T::OFF_B + wn * T::TN * 128;
 
     for (;;) {
-      // this wave's copies of slices 0 and 1 are there (and the last tile's
-      // output is read back)
+      // this wave's copies of slice 0 are there (and the last tile's output is
+      // read back)
       if (tail != 0 && S == 1) zero_tail(0);
       ring_barrier();
       v4i acc[FM][FN];
@@ -292,54 +299,59 @@ struct RingKernel {
       }
       const I8Tile now = t;
       bool next = false;
-      int ba = 0, s = 0;  // ba: A's buffer of slice s
-      for (; s + 4 < S; s++) {
-        const int bn = ba == 2 ? 0 : ba + 1, bp = ba == 0 ? 2 : ba - 1;
-        // A's slice s + 2, spread over the first step (buffer of slice s - 1)
-        step(acc, a0, a1, fb, smem + ba * T::SZA + la + (sw0 ^ 64), smem + (s & 1) * T::SZB + lb + (sw0 ^ 64),
-             [&](int j) {
+      int ba = 0, bb = 0, s = 0;  // buffers of slice s
+      // Slices that the tile started with are there since then, except in the
+      // first tile; the last tile's stores are waited for with the copies that
+      // follow them.
+      for (; s + T::DB + 1 < S; s++) {
+        const int an = ba == T::DB ? 0 : ba + 1, ap = ba == 0 ? T::DB : ba - 1;
+        const int bn = bb == T::DB - 1 ? 0 : bb + 1;
+        // A's slice s + DB, into the buffer of slice s - 1
+        step(acc, a0, a1, fb, smem + ba * T::SZA + la + (sw0 ^ 64), smem + bb * T::SZB + lb + (sw0 ^ 64), [&](int j) {
 #pragma unroll
-               for (int u = 0; u < T::CA; u++)
-                 if ((u * FN) / T::CA == j) copy_a1(s + 2, bp, 0, u);
-             });
-        step(acc, a1, a0, fb, smem + bn * T::SZA + la + sw0, smem + ((s + 1) & 1) * T::SZB + lb + sw0, [&](int j) {
+          for (int u = 0; u < T::CA; u++)
+            if ((u * FN) / T::CA == j) copy_a1(s + T::DB, ap, 0, u);
+        });
+        step(acc, a1, a0, fb, smem + an * T::SZA + la + sw0, smem + bn * T::SZB + lb + sw0, [&](int j) {
           if (j == 1) {
-            // slice 1 is there since the tile's start; the last tile's stores
-            // are waited for with slice 2's copies
-            if (s > 0) wait_vm<T::CA>();
+            if (first || s >= T::DB - 1) wait_vm<T::NEWER>();
             ring_barrier();
           }
 #pragma unroll
           for (int u = 0; u < T::CB; u++)
-            if (j >= 1 && 1 + (u * (FN - 1)) / T::CB == j) copy_b1(s + 2, 0, u);
+            if (j >= 1 && 1 + (u * (FN - 1)) / T::CB == j) copy_b1(s + T::DB, bb, 0, u);
         });
-        ba = bn;
+        ba = an;
+        bb = bn;
       }
       // the last slices: less and less is left to copy
       for (; s < S; s++) {
-        const int bn = ba == 2 ? 0 : ba + 1, bp = ba == 0 ? 2 : ba - 1;
-        if (s + 2 < S) copy_a(s + 2, bp, back(s + 2));
-        step(acc, a0, a1, fb, smem + ba * T::SZA + la + (sw0 ^ 64), smem + (s & 1) * T::SZB + lb + (sw0 ^ 64),
-             [](int) {});
-        step(acc, a1, a0, fb, smem + bn * T::SZA + la + sw0, smem + ((s + 1) & 1) * T::SZB + lb + sw0, [&](int j) {
+        const int an = ba == T::DB ? 0 : ba + 1, ap = ba == 0 ? T::DB : ba - 1;
+        const int bn = bb == T::DB - 1 ? 0 : bb + 1;
+        const bool more = s + T::DB < S;
+        if (more) copy_a(s + T::DB, ap, back(s + T::DB));
+        step(acc, a0, a1, fb, smem + ba * T::SZA + la + (sw0 ^ 64), smem + bb * T::SZB + lb + (sw0 ^ 64), [](int) {});
+        step(acc, a1, a0, fb, smem + an * T::SZA + la + sw0, smem + bn * T::SZB + lb + sw0, [&](int j) {
           if (j != 1) return;
-          if (s > 0) {
-            if (s + 2 < S)
-              wait_vm<T::CA>();
+          if (first || s >= T::DB - 1) {
+            if (more)
+              wait_vm<T::NEWER>();
             else
               wait_vm<0>();
           }
-          if (tail != 0 && s + 2 == S) zero_tail(bn);
+          if (tail != 0 && s + 2 == S) zero_tail(an);
           ring_barrier();
-          if (s + 2 < S) copy_b(s + 2, back(s + 2));
+          if (more) copy_b(s + T::DB, bb, back(s + T::DB));
           if (s + 1 == S) {
             tile += gridDim.x;
             next = set_tile(tile);
             if (next) start_tile();
           }
         });
-        ba = bn;
+        ba = an;
+        bb = bn;
       }
+      first = false;
       i8_drain(acc);
       uint8_t* cst = smem + T::OFF_CST + wave * 4096;
       if (now.rows != T::BM || (now.tn + 1) * T::BN > a.N)
@@ -629,7 +641,9 @@ hipError_t launch_few(const I8Args& a, hipStream_t stream) {
 //   64 x 4096 x 14336      32 x 32: 21.4    16 x 64: 27      32 x 64: 31     128 x 128: 79
 //   32 x 28672 x 8192      32 x 64: 44.9    16 x 64: 56      64 x 128: 46    128 x 128: 58
 //   64 x 28672 x 8192      64 x 128: 47.5   32 x 64: 64      16 x 64: 85     128 x 128: 59
-//   1024 x 4096 x 4096     128 x 128: 22.8  256 x 128: 26.8  256 x 256: 43   64 x 128: 35
+//   1024 x 4096 x 4096     128 x 128: 22.8  deep: 20.5       256 x 128: 26.8  256 x 256: 43
+//   2048 x 2048 x 2048     128 x 128: 14.9  deep: 13.3       256 x 128: 17.6  64 x 128: 24.8
+//   1024 tokens x 8 of 64 of 2048 x 4096          128 x 128: 165   deep: 175    256 x 256: 220
 //   512 x 14336 x 4096     256 x 128: 33    128 x 128: 41    256 x 256: 49
 //   8192 x 14336 x 4096    256 x 256: 389   256 x 128: 432   128 x 128: 493
 //   16 tokens x 4 of 64 experts of 2048 x 4096    16 x 64: 66   16 x 16: 85   32 x 64: 71   64 x 128: 92
@@ -645,6 +659,9 @@ using Tile32x32 = I8Few<2, 1, 2, 4, 4>;
 using Tile32x64 = I8Few<2, 1, 4, 2, 3>;
 using Tile64x128 = I8Few<4, 2, 4, 2, 3>;
 using Tile128x128 = I8Cfg<128, 128, 2, 2>;
+// with a CU to itself: 8 waves, as one wave alone cannot issue 16 x 16 MFMAs at
+// the rate that the matrix core takes them, and a slice more in flight
+using Tile128x128Deep = I8Cfg<128, 128, 4, 2, 3>;
 using Tile256x128 = I8Cfg<256, 128, 4, 2>;
 using Tile256x256 = I8Cfg<256, 256, 4, 2>;
 
@@ -652,6 +669,7 @@ const Variant kVariants[] = {
     {16, 16, 2, 0.18, 1.8, launch_few<Tile16x16>},    {16, 64, 2, 0.42, 1.5, launch_few<Tile16x64>},
     {32, 32, 1, 0.19, 2.4, launch_few<Tile32x32>},    {32, 64, 2, 0.52, 1.5, launch_few<Tile32x64>},
     {64, 128, 1, 0.70, 1.0, launch_few<Tile64x128>},  {128, 128, 2, 1.00, 2.0, launch_ring<Tile128x128>},
+    {128, 128, 1, 0.55, 3.0, launch_ring<Tile128x128Deep>},
     {256, 128, 1, 0.87, 3.0, launch_ring<Tile256x128>}, {256, 256, 1, 1.45, 8.0, launch_ring<Tile256x256>}};
 
 constexpr double kCus = 256, kBytesPerUs = 5.2e6;
