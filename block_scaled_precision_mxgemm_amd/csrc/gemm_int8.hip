@@ -474,26 +474,26 @@ hipError_t launch_ring(const I8Args& a, hipStream_t stream) {
 
 // ---- few rows ---------------------------------------------------------------
 //
-// CW x KW waves on a tile of 16 MB rows x 16 CW NB columns: each wave has 16 NB
-// of the columns and every KW-th slice of 128 k (a line of each row).  A stage
+// CW x KW waves on a tile of 16 MB rows x 16 CW columns: each wave has 16 of the
+// columns and every KW-th slice of 128 k (a line of each row).  A stage
 // of LDS holds KW slices, one for each group of waves; D stages are in flight
 // or in use, so that a CU keeps most of its LDS of memory requests going, which
 // is what bounds such products.  The groups' sums are exact and are added
 // through LDS at the end.
-template <int MB_, int NB_, int CW_, int KW_, int D_>
+template <int MB_, int CW_, int KW_, int D_>
 struct I8Few {
-  static constexpr int MB = MB_, NB = NB_, CW = CW_, KW = KW_, D = D_;
-  static constexpr int BM = 16 * MB, BN = 16 * CW * NB, NW = CW * KW;
+  static constexpr int MB = MB_, CW = CW_, KW = KW_, D = D_;
+  static constexpr int BM = 16 * MB, BN = 16 * CW, NW = CW * KW;
   static constexpr int PART = (BM + BN) * 128, STAGE = KW * PART, LDS = D * STAGE;
   // copies of 8 rows: RG for a slice, NC for a stage, of which a wave issues
   // MIN or (the first REM waves) one more
   static constexpr int RG = (BM + BN) / 8, NC = RG * KW, MIN = NC / NW, REM = NC % NW, MAX = MIN + (REM ? 1 : 0);
-  static_assert(LDS <= 160 * 1024 && LDS >= NW * MB * NB * 1024 && D >= 3, "stages, and the sums of all waves");
+  static_assert(LDS <= 160 * 1024 && LDS >= NW * MB * 1024 && D >= 3, "stages, and the sums of all waves");
 };
 
 template <class T, bool GATHER>
 __global__ __launch_bounds__(T::NW * 64) void int8_few_kernel(I8Args a, int tiles_n) {
-  constexpr int MB = T::MB, NB = T::NB, CW = T::CW, KW = T::KW, NW = T::NW, D = T::D;
+  constexpr int MB = T::MB, CW = T::CW, KW = T::KW, NW = T::NW, D = T::D;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -548,11 +548,9 @@ __global__ __launch_bounds__(T::NW * 64) void int8_few_kernel(I8Args a, int tile
       }
     }
   };
-  v4i acc[MB][NB];
+  v4i acc[MB];
 #pragma unroll
-  for (int i = 0; i < MB; i++)
-#pragma unroll
-    for (int j = 0; j < NB; j++) acc[i][j] = v4i{0, 0, 0, 0};
+  for (int i = 0; i < MB; i++) acc[i] = v4i{0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < D - 1; i++)
     if (i < I) issue(i, i);
@@ -572,36 +570,31 @@ __global__ __launch_bounds__(T::NW * 64) void int8_few_kernel(I8Args a, int tile
     const int slice = i * KW + kw;
     if (slice < S) {
       const uint8_t* pa = smem + stage * T::STAGE + kw * T::PART;
-      const uint8_t* pb = pa + T::BM * 128 + cw * NB * 2048;
+      const uint8_t* pb = pa + T::BM * 128 + cw * 2048;
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         const int sw = sw0 ^ (64 * h);
-        v4i fa[MB], fb[NB];
+        v4i fa[MB];
 #pragma unroll
         for (int u = 0; u < MB; u++) fa[u] = *reinterpret_cast<const v4i*>(pa + u * 2048 + sw);
-#pragma unroll
-        for (int j = 0; j < NB; j++) fb[j] = *reinterpret_cast<const v4i*>(pb + j * 2048 + sw);
+        const v4i fb = *reinterpret_cast<const v4i*>(pb + sw);
         // codes past K count as zeros
         if (tail != 0 && slice == S - 1 && h * 64 + g * 16 >= tail) {
 #pragma unroll
           for (int u = 0; u < MB; u++) fa[u] = v4i{0, 0, 0, 0};
         }
 #pragma unroll
-        for (int u = 0; u < MB; u++)
-#pragma unroll
-          for (int j = 0; j < NB; j++) acc[u][j] = mfma_i8(fb[j], fa[u], acc[u][j]);
+        for (int u = 0; u < MB; u++) acc[u] = mfma_i8(fb, fa[u], acc[u]);
       }
     }
     stage = stage == D - 1 ? 0 : stage + 1;
   }
   // sums of the KW groups, a fragment per wave at a time
-  constexpr int NF = MB * NB * CW;
+  constexpr int NF = MB * CW;
   v4i* part = reinterpret_cast<v4i*>(smem);  // [KW][NF][64]
   ring_barrier();
 #pragma unroll
-  for (int u = 0; u < MB; u++)
-#pragma unroll
-    for (int j = 0; j < NB; j++) part[((kw * NF) + (cw * NB + j) * MB + u) * 64 + lane] = acc[u][j];
+  for (int u = 0; u < MB; u++) part[(kw * NF + cw * MB + u) * 64 + lane] = acc[u];
   __syncthreads();
   for (int f = wave; f < NF; f += NW) {
     v4i sum = part[f * 64 + lane];
@@ -635,29 +628,30 @@ hipError_t launch_few(const I8Args& a, hipStream_t stream) {
 // (seven tenths of it where a variant that fits twice on a CU has it for
 // itself), and what a tile costs besides; and as no less than the weights'
 // time from memory.  The smallest estimate is taken, the first of equal ones.
-// The constants are measured; what the choice is worth, in us (bf16 output):
-//   16 x 28672 x 8192      16 x 64: 46.6    32 x 64: 44.5    64 x 128: 50    128 x 128: 60
-//   16 x 4096 x 4096       16 x 16: 6.4     16 x 64: 9.9     32 x 64: 11.6   128 x 128: 20
-//   64 x 4096 x 14336      32 x 32: 21.4    16 x 64: 27      32 x 64: 31     128 x 128: 79
-//   32 x 28672 x 8192      32 x 64: 44.9    16 x 64: 56      64 x 128: 46    128 x 128: 58
-//   64 x 28672 x 8192      64 x 128: 47.5   32 x 64: 64      16 x 64: 85     128 x 128: 59
-//   1024 x 4096 x 4096     128 x 128: 22.8  deep: 20.5       256 x 128: 26.8  256 x 256: 43
-//   2048 x 2048 x 2048     128 x 128: 14.9  deep: 13.3       256 x 128: 17.6  64 x 128: 24.8
-//   1024 tokens x 8 of 64 of 2048 x 4096          128 x 128: 165   deep: 175    256 x 256: 220
-//   512 x 14336 x 4096     256 x 128: 33    128 x 128: 41    256 x 256: 49
-//   8192 x 14336 x 4096    256 x 256: 389   256 x 128: 432   128 x 128: 493
-//   16 tokens x 4 of 64 experts of 2048 x 4096    16 x 64: 66   16 x 16: 85   32 x 64: 71   64 x 128: 92
-//   2048 tokens x 4 of 16 of 4096 x 2048          128 x 128: 118   256 x 256: 122   64 x 128: 242
+// The constants are measured; what the choice is worth, in us (bf16 output,
+// weights from memory; dense M x N x K, or tokens x choices of experts of N x K):
+//                                  16x16  16x32  32x32  32x64  deep  128x128 256x128 256x256
+//   16 x 4096 x 4096                 6.3    6.8    8.0    11.6  20     20      25      42
+//   16 x 28672 x 8192                46     44     49     46.7  52     60      66      90
+//   32 x 28672 x 8192                73     61     54     46.7  53     60      66      90
+//   64 x 4096 x 14336                34     26     21     31    54     80      83      137
+//   256 x 4096 x 4096                39     27     26     16.6  17     21      25      42
+//   1024 x 4096 x 4096               -      -      -      59    20.5   22.8    27      43
+//   512 x 14336 x 4096               -      -      -      -     -      41      33      49
+//   8192 x 14336 x 4096              -      -      -      1300  636    490     427     375
+//   16 x 4 of 64 of 2048 x 4096      93     68     87     77    98     98      105     118
+//   256 x 4 of 64 of 2048 x 4096     186    132    152    117   134    141     157     161
+//   1024 x 8 of 64 of 2048 x 4096    -      -      -      297   175    165     202     220
+//   2048 x 4 of 16 of 4096 x 2048    -      -      -      282   136    118     118     112
 struct Variant {
   int bm, bn, per_cu;
   double us, extra;
   hipError_t (*launch)(const I8Args&, hipStream_t);
 };
-using Tile16x16 = I8Few<1, 1, 1, 4, 5>;
-using Tile16x64 = I8Few<1, 1, 4, 2, 4>;
-using Tile32x32 = I8Few<2, 1, 2, 4, 4>;
-using Tile32x64 = I8Few<2, 1, 4, 2, 3>;
-using Tile64x128 = I8Few<4, 2, 4, 2, 3>;
+using Tile16x16 = I8Few<1, 1, 4, 5>;
+using Tile16x32 = I8Few<1, 2, 4, 3>;
+using Tile32x32 = I8Few<2, 2, 4, 4>;
+using Tile32x64 = I8Few<2, 4, 2, 3>;
 using Tile128x128 = I8Cfg<128, 128, 2, 2>;
 // with a CU to itself: 8 waves, as one wave alone cannot issue 16 x 16 MFMAs at
 // the rate that the matrix core takes them, and a slice more in flight
@@ -666,11 +660,14 @@ using Tile256x128 = I8Cfg<256, 128, 4, 2>;
 using Tile256x256 = I8Cfg<256, 256, 4, 2>;
 
 const Variant kVariants[] = {
-    {16, 16, 2, 0.18, 1.8, launch_few<Tile16x16>},    {16, 64, 2, 0.42, 1.5, launch_few<Tile16x64>},
-    {32, 32, 1, 0.19, 2.4, launch_few<Tile32x32>},    {32, 64, 2, 0.52, 1.5, launch_few<Tile32x64>},
-    {64, 128, 1, 0.70, 1.0, launch_few<Tile64x128>},  {128, 128, 2, 1.00, 2.0, launch_ring<Tile128x128>},
+    {16, 16, 2, 0.18, 1.8, launch_few<Tile16x16>},
+    {16, 32, 2, 0.22, 1.8, launch_few<Tile16x32>},
+    {32, 32, 1, 0.19, 2.4, launch_few<Tile32x32>},
+    {32, 64, 2, 0.52, 1.5, launch_few<Tile32x64>},
     {128, 128, 1, 0.55, 3.0, launch_ring<Tile128x128Deep>},
-    {256, 128, 1, 0.87, 3.0, launch_ring<Tile256x128>}, {256, 256, 1, 1.45, 8.0, launch_ring<Tile256x256>}};
+    {128, 128, 2, 1.00, 2.0, launch_ring<Tile128x128>},
+    {256, 128, 1, 0.87, 3.0, launch_ring<Tile256x128>},
+    {256, 256, 1, 1.45, 8.0, launch_ring<Tile256x256>}};
 
 constexpr double kCus = 256, kBytesPerUs = 5.2e6;
 

@@ -321,9 +321,18 @@ def _arg(t, name: str, dtypes, shape=None, dim: int | None = None, like: torch.T
     return t
 
 
-def _out(t, name: str, dtype, shape, like: torch.Tensor) -> torch.Tensor:
+def _new(shape, dtype, like: torch.Tensor, stream=None, make=torch.empty) -> torch.Tensor:
+    """A tensor for a call on `stream`: it is made there, since memory of the
+    current stream's pool may still be in use by work queued on that one."""
+    if stream is None:
+        return make(*shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return make(*shape, dtype=dtype, device=like.device)
+
+
+def _out(t, name: str, dtype, shape, like: torch.Tensor, stream=None) -> torch.Tensor:
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _new(shape, dtype, like, stream)
     return _arg(t, name, (dtype,), shape, like=like)
 
 
@@ -362,8 +371,8 @@ def int8gemm_quantize(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.T
     layer with a scale per output channel."""
     x = _arg(x, "x", _FLOATS, dim=2)
     rows, K = x.shape
-    q = _out(q, "q", torch.int8, (rows, K), x)
-    s = _out(s, "s", torch.float32, (rows,), x)
+    q = _out(q, "q", torch.int8, (rows, K), x, stream)
+    s = _out(s, "s", torch.float32, (rows,), x, stream)
     _call("int8gemm_quantize", x.device, stream, x.data_ptr(), _DTYPE_IDS[x.dtype], rows, K, q.data_ptr(), s.data_ptr())
     return q, s
 
@@ -384,7 +393,7 @@ def int8gemm_run(a_q, a_s, b_q, b_s, bias: torch.Tensor | None = None, act: int 
     b_s = _arg(b_s, "b_s", (torch.float32,), (N,), like=a_q)
     if bias is not None:
         bias = _arg(bias, "bias", (torch.float32,), (N,), like=a_q)
-    out = _out(out, "out", _OUT_DTYPES[out_type], (M, N), a_q)
+    out = _out(out, "out", _OUT_DTYPES[out_type], (M, N), a_q, stream)
     _call("int8gemm_run", a_q.device, stream, a_q.data_ptr(), a_s.data_ptr(), b_q.data_ptr(), b_s.data_ptr(),
           out.data_ptr(), M, N, K, _ptr(bias), act, out_type)
     return out
@@ -415,7 +424,7 @@ def int8gemm_run_grouped(a_q, a_s, b_q, b_s, offsets, index: torch.Tensor | None
         rows = index.shape[0]
     if bias is not None:
         bias = _arg(bias, "bias", (torch.float32,), (E, N), like=a_q)
-    out = _out(out, "out", _OUT_DTYPES[out_type], (rows, N), a_q)
+    out = _out(out, "out", _OUT_DTYPES[out_type], (rows, N), a_q, stream)
     _call("int8gemm_run_grouped", a_q.device, stream, a_q.data_ptr(), a_s.data_ptr(), rows_a, b_q.data_ptr(),
           b_s.data_ptr(), out.data_ptr(), rows, N, K, E, offsets.data_ptr(), _ptr(index), index_div, _ptr(bias), act,
           out_type)
@@ -436,8 +445,8 @@ def expert_route(logits, k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor 
         bias = _arg(bias, "bias", (torch.float32,), (E,), like=logits)
     if not 1 <= k <= E:
         raise ValueError("k must be 1 .. %d" % E)
-    ids = _out(ids, "ids", torch.int32, (T, k), logits)
-    weights = _out(weights, "weights", torch.float32, (T, k), logits)
+    ids = _out(ids, "ids", torch.int32, (T, k), logits, stream)
+    weights = _out(weights, "weights", torch.float32, (T, k), logits, stream)
     _call("expert_route", logits.device, stream, logits.data_ptr(), _DTYPE_IDS[logits.dtype], T, E, k, score, _ptr(bias),
           groups, top_groups, group_top, int(renormalize), scale, ids.data_ptr(), weights.data_ptr())
     return ids, weights
@@ -454,7 +463,7 @@ def expert_route_backward(logits, ids, d_weights, score: int = SCORE_SOFTMAX, re
     if ids.shape[0] != T:
         raise ValueError("ids must have %d rows" % T)
     d_weights = _arg(d_weights, "d_weights", (torch.float32,), (T, k), like=logits)
-    d_logits = _out(d_logits, "d_logits", logits.dtype, (T, E), logits)
+    d_logits = _out(d_logits, "d_logits", logits.dtype, (T, E), logits, stream)
     _call("expert_route_backward", logits.device, stream, logits.data_ptr(), _DTYPE_IDS[logits.dtype], T, E,
           ids.data_ptr(), d_weights.data_ptr(), k, score, int(renormalize), scale, d_logits.data_ptr())
     return d_logits
@@ -468,16 +477,20 @@ def expert_plan(ids, experts: int, offsets: torch.Tensor | None = None, order: t
     last expert's rows; position[t][j] is the slot's row, or -1."""
     ids = _arg(ids, "ids", (torch.int32,), dim=2)
     T, k = ids.shape
-    lib = _load()
-    need = lib.expert_plan_workspace(T, k, experts)
+    need = _load().expert_plan_workspace(T, k, experts)
     if need < 0:
         _check(1, "expert_plan")
-    offsets = _out(offsets, "offsets", torch.int32, (experts + 1,), ids)
-    order = _out(order, "order", torch.int32, (T * k,), ids)
-    position = _out(position, "position", torch.int32, (T, k), ids)
-    workspace = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
-    if workspace is not None and stream is not None:
-        workspace.record_stream(stream)
+    n = T * k
+    if offsets is None and order is None and position is None:
+        # one allocation for the three (2 us less than three)
+        offsets, order, position = _new((experts + 1 + 2 * n,), torch.int32, ids, stream).split_with_sizes(
+            (experts + 1, n, n))
+        position = position.view(T, k)
+    else:
+        offsets = _out(offsets, "offsets", torch.int32, (experts + 1,), ids, stream)
+        order = _out(order, "order", torch.int32, (n,), ids, stream)
+        position = _out(position, "position", torch.int32, (T, k), ids, stream)
+    workspace = _new((need,), torch.uint8, ids, stream) if need else None
     _call("expert_plan", ids.device, stream, ids.data_ptr(), T, k, experts, offsets.data_ptr(), order.data_ptr(),
           position.data_ptr(), _ptr(workspace))
     return offsets, order, position
@@ -499,7 +512,7 @@ def expert_combine(y, position, weights, out_type: int | None = None, out: torch
     out_type = _DTYPE_IDS[y.dtype] if out_type is None else out_type
     if out_type not in _OUT_DTYPES:
         raise ValueError("unknown out_type %r" % (out_type,))
-    out = _out(out, "out", _OUT_DTYPES[out_type], (T, N), y)
+    out = _out(out, "out", _OUT_DTYPES[out_type], (T, N), y, stream)
     _call("expert_combine", y.device, stream, y.data_ptr(), _DTYPE_IDS[y.dtype], rows, N, position.data_ptr(),
           weights.data_ptr(), T, k, out.data_ptr(), out_type)
     return out
@@ -513,9 +526,9 @@ def expert_combine_backward(d_out, y, position, weights, d_y: torch.Tensor | Non
     y, position, weights, rows, N, T, k = _combine_args(y, position, weights)
     d_out = _arg(d_out, "d_out", _FLOATS, (T, N), like=y)
     if d_y is None:
-        d_y = torch.zeros_like(y)
+        d_y = _new((rows, N), y.dtype, y, stream, torch.zeros)
     d_y = _arg(d_y, "d_y", (y.dtype,), (rows, N), like=y)
-    d_weights = _out(d_weights, "d_weights", torch.float32, (T, k), y)
+    d_weights = _out(d_weights, "d_weights", torch.float32, (T, k), y, stream)
     _call("expert_combine_backward", y.device, stream, d_out.data_ptr(), _DTYPE_IDS[d_out.dtype], y.data_ptr(),
           _DTYPE_IDS[y.dtype], rows, N, position.data_ptr(), weights.data_ptr(), T, k, d_y.data_ptr(),
           d_weights.data_ptr())

@@ -372,6 +372,33 @@ def test_side_stream():
         assert torch.equal(got, want)
 
 
+def test_outputs_of_another_stream():
+    """What a call on another stream allocates is not memory that the current
+    stream's queued work still uses."""
+    say("outputs of another stream")
+    b = binding()
+    x = torch.randn((512, 4096), device=DEV)
+    want, _ = b.int8gemm_quantize(x)
+    y, pos, w = torch.randn((64, 256), device=DEV), torch.arange(64, dtype=torch.int32, device=DEV).view(32, 2), torch.ones((32, 2), device=DEV)
+    want_y, _ = b.expert_combine_backward(torch.ones((32, 256), device=DEV), y, pos, w)
+    d_out = torch.ones((32, 256), device=DEV)
+    side = torch.cuda.Stream()
+    big = torch.zeros(64 << 20, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        held = [torch.empty((512, 4096), dtype=torch.int8, device=DEV), torch.empty((64, 256), device=DEV)]
+        torch.cuda.synchronize()
+        for _ in range(30):
+            big.add_(1.0)
+        for t in held:
+            t.fill_(7)
+        del held, t
+        q, _ = b.int8gemm_quantize(x, stream=side)
+        d_y, _ = b.expert_combine_backward(d_out, y, pos, w, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(q, want) and torch.equal(d_y, want_y)
+
+
 @pytest.mark.parametrize("M", [1, 16, 60, 300])
 def test_graph_replay(M):
     say("graph replay int8", M)
