@@ -42,7 +42,7 @@ __device__ __forceinline__ int key_expert(double key) {
 template <int D>
 __device__ __forceinline__ int lane_step(int x) {
   if constexpr (D <= 8)
-    return __builtin_amdgcn_update_dpp(x, x, 0x120 + D, 0xf, 0xf, false);  // row_ror:D
+    return __builtin_amdgcn_mov_dpp(x, 0x120 + D, 0xf, 0xf, true);  // row_ror:D
   else
     return __shfl_xor(x, D);
 }
@@ -54,14 +54,23 @@ template <int D>
 __device__ __forceinline__ double lane_step(double x) {
   return __hiloint2double(lane_step<D>(__double2hiint(x)), lane_step<D>(__double2loint(x)));
 }
+// fmax of values that are not NaN.  For doubles it is the instruction itself:
+// fmax first quiets both operands, which triples its cost.  The s_nop is the
+// wait of a DPP move that may read the result next.
+__device__ __forceinline__ float larger(float x, float y) { return fmaxf(x, y); }
+__device__ __forceinline__ double larger(double x, double y) {
+  double r;
+  asm("v_max_f64 %0, %1, %2\n\ts_nop 1" : "=v"(r) : "v"(x), "v"(y));
+  return r;
+}
 template <int L, class V>
 __device__ __forceinline__ V lanes_max(V x) {
-  if constexpr (L > 32) x = fmax(x, lane_step<32>(x));
-  if constexpr (L > 16) x = fmax(x, lane_step<16>(x));
-  x = fmax(x, lane_step<8>(x));
-  x = fmax(x, lane_step<4>(x));
-  x = fmax(x, lane_step<2>(x));
-  return fmax(x, lane_step<1>(x));
+  if constexpr (L > 32) x = larger(x, lane_step<32>(x));
+  if constexpr (L > 16) x = larger(x, lane_step<16>(x));
+  x = larger(x, lane_step<8>(x));
+  x = larger(x, lane_step<4>(x));
+  x = larger(x, lane_step<2>(x));
+  return larger(x, lane_step<1>(x));
 }
 template <int L, class V>
 __device__ __forceinline__ V lanes_sum(V x) {
@@ -123,6 +132,13 @@ __device__ __forceinline__ double reciprocal(double x) {
   double r = __builtin_amdgcn_rcp(x);
   r = fma(fma(-x, r, 1.0), r, r);
   return fma(fma(-x, r, 1.0), r, r);
+}
+
+// The same in fp32, for the weights (each exponential is off by a few roundings
+// and one for each unit of its argument).
+__device__ __forceinline__ float chosen_score32(int score, float l, float m) {
+  if (score == kScoreSoftmax) return __expf(l - m);
+  return l < 0.0f ? __expf(l - m) / (1.0f + __expf(l)) : __expf(-m) / (1.0f + __expf(-l));
 }
 
 // Choices of a token, L a round.
@@ -244,7 +260,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a, bo
   for (int j = 0; j < a.k; j++) {
     double best = key[0];
 #pragma unroll
-    for (int v = 1; v < VPL; v++) best = fmax(best, key[v]);
+    for (int v = 1; v < VPL; v++) best = larger(best, key[v]);
     best = lanes_max<L>(best);
     const int e = best > -0x1.8p1023 ? key_expert(best) : -1;
     if (lane == 0) chosen[tok][j] = e;
@@ -256,7 +272,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a, bo
   }
   __builtin_amdgcn_wave_barrier();
   // weights: a lane takes choices lane, lane + L, ...
-  double p[kRounds<L>], total = 0.0;
+  float p[kRounds<L>], total = 0.0f;
   int id[kRounds<L>];
   float lc[kRounds<L>], mc = -__builtin_inff();
 #pragma unroll
@@ -266,29 +282,23 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a, bo
     lc[i] = id[i] >= 0 ? RowElem<IN>::get(row[id[i]]) : -__builtin_inff();
     mc = fmaxf(mc, lc[i]);
   }
-  if (a.renormalize) {
-    mc = lanes_max<L>(mc);
-    if (!softmax) mc = fminf(mc, 0.0f);
-  }
+  mc = a.renormalize ? lanes_max<L>(mc) : softmax ? m : 0.0f;
+  if (!softmax) mc = fminf(mc, 0.0f);
 #pragma unroll
   for (int i = 0; i < kRounds<L>; i++) {
-    p[i] = 0.0;
+    p[i] = 0.0f;
     if (i * L < a.k && id[i] >= 0) {
-      p[i] = chosen_score(a.score, (double)lc[i], a.renormalize ? (double)mc : softmax ? (double)m : 0.0);
+      p[i] = chosen_score32(a.score, lc[i], mc);
       total += p[i];
     }
   }
-  if (a.renormalize)
-    total = lanes_sum<L>(total);
-  else
-    total = sum;
-  const double f = (double)a.scale / (a.renormalize ? total : softmax ? sum : 1.0);
+  const float f = a.scale / (a.renormalize ? lanes_sum<L>(total) : softmax ? (float)sum : 1.0f);
 #pragma unroll
   for (int i = 0; i < kRounds<L>; i++) {
     const int j = lane + i * L;
     if (live && j < a.k) {
       a.ids[t * a.k + j] = id[i];
-      a.weights[t * a.k + j] = id[i] >= 0 ? (nan_row ? __builtin_nanf("") : (float)(p[i] * f)) : 0.0f;
+      a.weights[t * a.k + j] = id[i] >= 0 ? (nan_row ? __builtin_nanf("") : p[i] * f) : 0.0f;
     }
   }
 }
