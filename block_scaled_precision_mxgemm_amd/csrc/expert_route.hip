@@ -225,14 +225,14 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a, bo
 #pragma unroll
       for (int v = 0; v < VPL; v++) keys[tok][e0 + v] = key[v];
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     const int n = whole ? per / VPL * 2 : per;
     for (int i = lane; i < a.groups; i += L) {
       double first = -kInf, second = -kInf;
       for (int e = i * n; e < (i + 1) * n; e++) two_largest(first, second, keys[tok][e]);
       group_key[tok][i] = a.group_top == 2 && second > -kInf ? fmax(first + second, -kMaxKey) : first;
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     int i = e0 / per, in = e0 - i * per;  // group of expert e0 + v, and its place there
     bool out = false;
 #pragma unroll
@@ -270,7 +270,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a, bo
       key[v] = __hiloint2double(e == e0 + v ? (int)0xFFEFFFFF : hi, __double2loint(key[v]));
     }
   }
-  __builtin_amdgcn_wave_barrier();
+  wave_sync();
   // weights: a lane takes choices lane, lane + L, ...
   float p[kRounds<L>], total = 0.0f;
   int id[kRounds<L>];
@@ -399,7 +399,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
       grad[tok][j] = (float)g[i];
     }
   }
-  __builtin_amdgcn_wave_barrier();
+  wave_sync();
   float acc[VPL];
   const float each = -(float)dot / sum;
 #pragma unroll
@@ -559,9 +559,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
       order[p] = e < E ? (int32_t)i : -1;
       position[i] = e < E ? p : -1;
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     if (live && (same >> lane) == 1) mine[e] += __popcll(same);
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
   }
 }
 

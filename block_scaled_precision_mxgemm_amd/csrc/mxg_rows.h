@@ -59,6 +59,14 @@ __device__ __forceinline__ v4i pack16(const float (&f)[RowElem<TYPE>::VEC]) {
   return w;
 }
 
+// LDS written by some lanes of a wave is read by others behind this (the wave's
+// LDS instructions run in order; the fences keep the compiler to it).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 template <class V>
 __device__ __forceinline__ V wave_sum(V x) {
 #pragma unroll

@@ -408,8 +408,10 @@ int int8gemm_run_grouped(const int8_t *A, const float *scaleA, int64_t rowsA,
  * where fewer than k experts are left, ids ends in -1 with weight 0.  A NaN
  * score ranks below every number (softmax: a NaN or +inf logit makes the whole
  * row NaN: its available experts are taken in order, with NaN weights).
- * Without bias and with group_top == 1 the order is that of the logits, which
- * is that of the scores; otherwise c is formed in 64 bits.
+ * Without bias and with group_top == 1 (or one group) the order is that of the
+ * logits, which is that of the scores; otherwise c is formed in 64 bits, and
+ * values of c that agree in their first 42 bits count as equal.  weights are
+ * formed in fp32.
  *
  *   logits      device, T x E elements of in_type, aligned to an element
  *   T           >= 1;  E 1 .. MXG_MAX_EXPERTS;  k 1 .. MXG_MAX_CHOICES, at most

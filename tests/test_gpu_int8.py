@@ -145,6 +145,58 @@ def test_product_larger(M, N, K):
     _dense(M, N, K, 1, True, False, 5)
 
 
+def _exact64(a, a_s, w, w_s):
+    """The product in float64 on the GPU (integers below 2^53: the sums are
+    exact), and the tolerance of its fp32 evaluation without bias and activation."""
+    y = (a.double() @ w.double().t()) * a_s.double()[:, None] * w_s.double()[None, :]
+    return y, 3.01 * 2.0 ** -24 * y.abs()
+
+
+# sizes that take each tile shape, with more tiles than run at once, ragged
+# rows and columns and a partial last slice
+@pytest.mark.parametrize("M,N,K", [
+    (515, 966, 4800), (489, 2034, 5488), (931, 515, 4624), (1939, 2046, 1776), (8192, 4301, 400), (2050, 8203, 2000),
+    (5000, 9001, 1104), (4097, 4099, 144)])
+def test_product_many_tiles(M, N, K):
+    say("product many tiles", M, N, K)
+    b = binding()
+    g = torch.Generator(device=DEV).manual_seed(M)
+    a, w = (torch.empty((n, K), dtype=torch.int8, device=DEV).random_(-128, 128, generator=g) for n in (M, N))
+    a_s, w_s = (torch.rand(n, device=DEV, generator=g) + 0.5 for n in (M, N))
+    out = torch.full((M, N), float("nan"), device=DEV)
+    poison_lds()
+    b.int8gemm_run(a, a_s, w, w_s, out=out)
+    want, tol = _exact64(a, a_s, w, w_s)
+    assert ((out.double() - want).abs() <= tol + 2.0 ** -24 * want.abs()).all()
+
+
+@pytest.mark.parametrize("E,tokens,div,N,K", [
+    (40, 111, 2, 587, 3488), (40, 255, 2, 3201, 624), (2, 1966, 3, 3331, 1344), (3, 4500, 2, 6101, 2064),
+    (5, 2250, 4, 4201, 1040), (2, 32, 2, 301, 8208), (30, 30, 2, 2101, 4112), (64, 225, 4, 1101, 2064)])
+def test_experts_many_tiles(E, tokens, div, N, K):
+    say("experts many tiles", E, tokens, div, N, K)
+    b = binding()
+    rows = tokens * div
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    a = torch.empty((tokens, K), dtype=torch.int8, device=DEV).random_(-128, 128, generator=g)
+    w = torch.empty((E, N, K), dtype=torch.int8, device=DEV).random_(-128, 128, generator=g)
+    a_s, w_s = torch.rand(tokens, device=DEV, generator=g) + 0.5, torch.rand((E, N), device=DEV, generator=g) + 0.5
+    off = _counts(np.random.default_rng(rows), E, rows, 0.7).astype(np.int32)
+    index = torch.randperm(rows, device=DEV, generator=g).int()
+    out = torch.full((rows, N), float("nan"), device=DEV)
+    poison_lds()
+    b.int8gemm_run_grouped(a, a_s, w, w_s, dev(off), index=index, index_div=div, out=out)
+    src = (index // div).long()
+    for e in range(E):
+        mine = slice(int(off[e]), int(off[e + 1]))
+        if off[e + 1] > off[e]:
+            want, tol = _exact64(a[src[mine]], a_s[src[mine]], w[e], w_s[e])
+            assert ((out[mine].double() - want).abs() <= tol + 2.0 ** -24 * want.abs()).all(), e
+    # rows already sorted: the same without an index
+    again = b.int8gemm_run_grouped(a[src], a_s[src], w, w_s, dev(off))
+    assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("kind", [0, 1, 2])
 @pytest.mark.parametrize("bias,act", [(True, False), (False, True), (True, True)])
 @pytest.mark.parametrize("M,N,K", [(3, 67, 160), (16, 512, 1024), (70, 132, 272), (260, 516, 1040)])
@@ -339,6 +391,38 @@ def test_output_past_4_gib():
     got = b.int8gemm_run(a, torch.ones(M, device=DEV), w, torch.ones(N, device=DEV))
     for r in (slice(0, 64), slice(32700, 32840), slice(65400, 65600), slice(M - 70, M)):
         assert torch.equal(got[r], (a[r].double() @ w.double().t()).float())
+
+
+def test_two_calls_at_once():
+    """Products, routing and plans of two streams side by side give what they give alone."""
+    say("two calls at once")
+    b = binding()
+    sets = []
+    for seed, T in ((1, 3000), (2, 40)):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        x = torch.randn((T, 528), device=DEV, generator=g)
+        w, w_s = b.int8gemm_quantize(torch.randn((8 * 700, 528), device=DEV, generator=g))
+        logits = torch.randn((T, 8), device=DEV, generator=g)
+        sets.append((x, w.view(8, 700, 528), w_s.view(8, 700), logits))
+
+    def work(x, w, w_s, logits):
+        ids, weights = b.expert_route(logits, 2)
+        off, order, pos = b.expert_plan(ids, 8)
+        q, s = b.int8gemm_quantize(x)
+        y = b.int8gemm_run_grouped(q, s, w, w_s, off, index=order, index_div=2)
+        return y, b.expert_combine(y, pos, weights), b.int8gemm_run(q, s, w[3], w_s[3])
+
+    alone = [work(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append(work(*s))
+        torch.cuda.synchronize()
+        for x, y in zip(got, alone):
+            assert all(torch.equal(u, v) for u, v in zip(x, y))
 
 
 # ---- streams, graphs, refusals ----------------------------------------------
