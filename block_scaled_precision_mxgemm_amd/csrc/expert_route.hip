@@ -454,7 +454,7 @@ constexpr int kPlanWaves = 16;
 constexpr int kPlanThreads = kPlanWaves * 64;
 constexpr int kMaxExperts = 1024;
 // One workgroup alone takes 7.4 us for 4096 slots of 128 experts and 1.1 us for
-// each 1000 more (131072: 150); the two kernels 7.8 us for 6000, 10.5 for
+// each 1000 more (131072: 150); the two kernels 7 us for 6000, 10.3 for
 // 131072 and 22 for 2^20.
 constexpr int64_t kPlanRun = 4096;
 constexpr int64_t kPlanRuns = 256;
@@ -501,11 +501,20 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
     const int groups = kPlanThreads / E1 > 0 ? kPlanThreads / E1 : 1;
     for (int i = tid; i < groups * E1; i += kPlanThreads) {
       const int e = i % E1;
+      // 8 runs' counts are loaded at a time
       int all = 0, ahead = 0;
-      for (int b = i / E1; b < runs; b += groups) {
-        const int c = counts[(int64_t)b * E1 + e];
-        all += c;
-        ahead += b < (int)blockIdx.x ? c : 0;
+      for (int b0 = i / E1; b0 < runs; b0 += 8 * groups) {
+        int c[8];
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+          const int b = b0 + u * groups;
+          c[u] = b < runs ? counts[(int64_t)b * E1 + e] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+          all += c[u];
+          ahead += b0 + u * groups < (int)blockIdx.x ? c[u] : 0;
+        }
       }
       atomicAdd(&total[e], all);
       atomicAdd(&before[e], ahead);
@@ -527,11 +536,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
     int s = 0;
     for (int i = 0; i < per; i++)
       if (lane * per + i < E1) s += total[lane * per + i];
-    int at = s;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(at, d);
-      if (lane >= d) at += o;
-    }
+    int at = wave_scan<false>(s);
     at -= s;
     for (int i = 0; i < per; i++) {
       const int e = lane * per + i;

@@ -9,7 +9,7 @@
 // columns of one row of C.
 #pragma once
 
-#include "mxg_epilogue.h"
+#include "mxg_rows.h"
 
 namespace mxg {
 
@@ -69,24 +69,6 @@ __device__ __forceinline__ void tile_order(int bid, int tiles_m, int tiles_n, in
   const int in = id - group * 8 * tiles_n;
   tm = first + in % rows;
   tn = in / rows;
-}
-
-// Inclusive scans over the lanes of a wave by DPP (shifts within rows of 16,
-// then the rows' last values passed on): a few cycles a step, where a shuffle
-// goes through LDS.
-template <bool MAX>
-__device__ __forceinline__ int scan_op(int x, int y) {
-  return MAX ? max(x, y) : x + y;
-}
-template <bool MAX>
-__device__ __forceinline__ int wave_scan(int x) {  // MAX: values of at least 0
-  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
-  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
-  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
-  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
-  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
-  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
-  return x;
 }
 
 // Tile `bid` in that order, found by a wave (every lane gets it); false if

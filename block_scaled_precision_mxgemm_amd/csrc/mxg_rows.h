@@ -67,6 +67,24 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Inclusive scans over the lanes of a wave by DPP (shifts within rows of 16,
+// then the rows' last values passed on): a few cycles a step, where a shuffle
+// goes through LDS.
+template <bool MAX>
+__device__ __forceinline__ int scan_op(int x, int y) {
+  return MAX ? max(x, y) : x + y;
+}
+template <bool MAX>
+__device__ __forceinline__ int wave_scan(int x) {  // MAX: values of at least 0
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
+  x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
+  return x;
+}
+
 template <class V>
 __device__ __forceinline__ V wave_sum(V x) {
 #pragma unroll
