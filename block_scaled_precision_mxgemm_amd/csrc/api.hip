@@ -158,7 +158,7 @@ const char* mxgemm_status_string(int status) {
     case MXG_OK:
       return "ok";
     case MXG_EINVAL:
-      return "invalid argument (null pointer, dimension out of range, K not a multiple of 32, or unknown format)";
+      return "invalid argument (null pointer, dimension out of range, K not a multiple of 32 (int8: 16), or unknown format)";
     case MXG_EALIGN:
       return "data pointer not 16-byte aligned";
     case MXG_EUNSUPPORTED:
