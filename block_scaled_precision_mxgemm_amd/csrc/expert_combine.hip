@@ -101,7 +101,8 @@ template <int Y, int O>
 __global__ __launch_bounds__(kCThreads) void combine_backward_kernel(CombineArgs a, void* __restrict__ dY,
                                                                      float* __restrict__ dW) {
   const int lane = threadIdx.x & 63;
-  const int64_t slot = (int64_t)blockIdx.x * (kCThreads / 64) + (threadIdx.x >> 6);
+  const int64_t group = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t slot = group * (kCThreads / 64) + (threadIdx.x >> 6);
   if (slot >= a.T * a.k) return;
   const int64_t t = slot / a.k;
   const int p = a.position[slot];
@@ -135,8 +136,10 @@ __global__ __launch_bounds__(kCThreads) void combine_backward_kernel(CombineArgs
 template <int Y, int O>
 hipError_t combine_launch(const CombineArgs& a, void* dY, float* dW, hipStream_t stream) {
   if (dW != nullptr) {
-    const int64_t grid = (a.T * a.k + kCThreads / 64 - 1) / (kCThreads / 64);
-    hipLaunchKernelGGL((combine_backward_kernel<Y, O>), dim3((unsigned)grid), dim3(kCThreads), 0, stream, a, dY, dW);
+    // in two dimensions: a launch has less than 2^32 threads in one
+    const int64_t groups = (a.T * a.k + kCThreads / 64 - 1) / (kCThreads / 64), most = 1 << 20;
+    const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)((groups + most - 1) / most));
+    hipLaunchKernelGGL((combine_backward_kernel<Y, O>), grid, dim3(kCThreads), 0, stream, a, dY, dW);
   } else {
     const unsigned cols = (unsigned)((a.N + kCThreads * 8 - 1) / (kCThreads * 8));
     hipLaunchKernelGGL((combine_kernel<Y, O>), dim3((unsigned)a.T, cols), dim3(kCThreads), 0, stream, a);

@@ -265,6 +265,25 @@ def test_plan_edges(n):
     _check_plan(ids, 9)
 
 
+@pytest.mark.parametrize("E", [1, 1024])
+def test_plan_most_slots(E):
+    """As many slots as a call can have."""
+    say("plan most slots", E)
+    b = binding()
+    T, k = 1 << 20, 64
+    ids = torch.empty((T, k), dtype=torch.int32, device=DEV).random_(-1, E + 1)
+    off, order, pos = b.expert_plan(ids, E)
+    flat = torch.where((ids < 0) | (ids >= E), E, ids).flatten().to(torch.int16)
+    by, slot = torch.sort(flat, stable=True)
+    counts = torch.bincount(flat.int(), minlength=E + 1)
+    live = int(counts[:E].sum())
+    assert torch.equal(off.long(), torch.cat([counts.new_zeros(1), counts[:E].cumsum(0)]))
+    assert torch.equal(order[:live], slot[:live].int()) and (order[live:] == -1).all()
+    p = pos.flatten()
+    assert (p[slot[live:]] == -1).all()
+    assert torch.equal(p[slot[:live]], torch.arange(live, dtype=torch.int32, device=DEV))
+
+
 # ---- combination ------------------------------------------------------------
 
 
@@ -363,6 +382,25 @@ def test_combine_rows_past_4_gib():
     d_y, d_w = b.expert_combine_backward(torch.ones((1, N), dtype=torch.bfloat16, device=DEV), y, pos, w, d_y=y)
     assert torch.equal(d_w.cpu(), torch.tensor([[2.0 * N, 3.0 * N, 5.0 * N]]))
     assert (d_y[-1] == 1).all() and (d_y[70000] == 10).all() and (d_y[3] == 100).all()
+
+
+def test_combine_most_slots():
+    """As many slots as a call can have: 2^20 tokens of 64 choices."""
+    say("combine most slots")
+    b = binding()
+    T, k = 1 << 20, 64
+    n = T * k
+    slot = torch.arange(n, dtype=torch.int32, device=DEV)
+    pos = (n - 1 - slot).view(T, k)
+    y = (slot % 5 - 2).to(torch.bfloat16)[:, None]
+    w = (slot % 3 - 1).float().view(T, k)
+    d = (torch.arange(T, device=DEV) % 7 - 3).to(torch.bfloat16)[:, None]
+    at = y[:, 0].flip(0).view(T, k).float()  # y of a slot's row
+    # small whole numbers: every sum is exact
+    assert torch.equal(b.expert_combine(y, pos, w, out_type=b.OUT_F32)[:, 0], (at * w).sum(1))
+    d_y, d_w = b.expert_combine_backward(d, y, pos, w)
+    assert torch.equal(d_w, at * d.float())
+    assert torch.equal(d_y[:, 0].flip(0).view(T, k), (w * d.float()).to(torch.bfloat16))
 
 
 # ---- together ---------------------------------------------------------------
