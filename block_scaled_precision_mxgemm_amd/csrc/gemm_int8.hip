@@ -27,50 +27,52 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(I8Args a, int tiles_n) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, r = lane & 15;
   I8Tile t;
-  if (!find_tile(a, kBM, tiles_n, blockIdx.x, lane, t)) return;
-  if (tid < kBM) arow[tid] = tid < t.rows ? a_row(a, t.row0 + tid) : -1;
-  __syncthreads();
-  const int8_t* B = a.B + (int64_t)t.expert * a.N * a.K;
-  const int n0 = t.tn * kBN;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  v4i acc[2][2] = {};
-  for (int k0 = 0; k0 < a.K; k0 += kBK) {
-    for (int c = tid; c < kBM * 8; c += 256) {
-      const int row = c >> 3, ch = c & 7, k = k0 + ch * 16;
-      const int64_t ar = arow[row];
-      v4i va = {0, 0, 0, 0}, vb = {0, 0, 0, 0};
-      if (ar >= 0 && k < a.K) va = *reinterpret_cast<const v4i*>(a.A + ar * a.K + k);
-      if (n0 + row < a.N && k < a.K) vb = *reinterpret_cast<const v4i*>(B + (int64_t)(n0 + row) * a.K + k);
-      const int o = row * kBK + ((ch ^ swz8(row)) << 4);
-      *reinterpret_cast<v4i*>(sa + o) = va;
-      *reinterpret_cast<v4i*>(sb + o) = vb;
-    }
+  for (int64_t tile = blockIdx.x; find_tile(a, kBM, tiles_n, tile, lane, t); tile += gridDim.x) {
+    __syncthreads();  // the rows of the tile before have been looked up by all
+    if (tid < kBM) arow[tid] = tid < t.rows ? a_row(a, t.row0 + tid) : -1;
     __syncthreads();
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      v4i fa[2], fb[2];
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const int ra = wm + 16 * i + r, rb = wn + 16 * i + r;
-        fa[i] = *reinterpret_cast<const v4i*>(sa + ra * kBK + (((4 * h + g) ^ swz8(ra)) << 4));
-        fb[i] = *reinterpret_cast<const v4i*>(sb + rb * kBK + (((4 * h + g) ^ swz8(rb)) << 4));
+    const int8_t* B = a.B + (int64_t)t.expert * a.N * a.K;
+    const int n0 = t.tn * kBN;
+    const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+    v4i acc[2][2] = {};
+    for (int k0 = 0; k0 < a.K; k0 += kBK) {
+      for (int c = tid; c < kBM * 8; c += 256) {
+        const int row = c >> 3, ch = c & 7, k = k0 + ch * 16;
+        const int64_t ar = arow[row];
+        v4i va = {0, 0, 0, 0}, vb = {0, 0, 0, 0};
+        if (ar >= 0 && k < a.K) va = *reinterpret_cast<const v4i*>(a.A + ar * a.K + k);
+        if (n0 + row < a.N && k < a.K) vb = *reinterpret_cast<const v4i*>(B + (int64_t)(n0 + row) * a.K + k);
+        const int o = row * kBK + ((ch ^ swz8(row)) << 4);
+        *reinterpret_cast<v4i*>(sa + o) = va;
+        *reinterpret_cast<v4i*>(sb + o) = vb;
       }
+      __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 2; i++)
+      for (int h = 0; h < 2; h++) {
+        v4i fa[2], fb[2];
 #pragma unroll
-        for (int j = 0; j < 2; j++) acc[i][j] = mfma_i8(fb[j], fa[i], acc[i][j]);
+        for (int i = 0; i < 2; i++) {
+          const int ra = wm + 16 * i + r, rb = wn + 16 * i + r;
+          fa[i] = *reinterpret_cast<const v4i*>(sa + ra * kBK + (((4 * h + g) ^ swz8(ra)) << 4));
+          fb[i] = *reinterpret_cast<const v4i*>(sb + rb * kBK + (((4 * h + g) ^ swz8(rb)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+          for (int j = 0; j < 2; j++) acc[i][j] = mfma_i8(fb[j], fa[i], acc[i][j]);
+      }
+      __syncthreads();
     }
-    __syncthreads();
-  }
 #pragma unroll
-  for (int i = 0; i < 2; i++) {
-    const int row = wm + 16 * i + r;
-    if (row >= t.rows) continue;
-    const float s = a_scale(a, arow[row]);
+    for (int i = 0; i < 2; i++) {
+      const int row = wm + 16 * i + r;
+      if (row >= t.rows) continue;
+      const float s = a_scale(a, arow[row]);
 #pragma unroll
-    for (int j = 0; j < 2; j++) {
-      const int n = n0 + wn + 16 * j + 4 * g;
-      if (n < a.N) store4(a, t.expert, t.row0 + row, n, acc[i][j], s);
+      for (int j = 0; j < 2; j++) {
+        const int n = n0 + wn + 16 * j + 4 * g;
+        if (n < a.N) store4(a, t.expert, t.row0 + row, n, acc[i][j], s);
+      }
     }
   }
 }
@@ -669,7 +671,8 @@ const Variant kVariants[] = {
     {256, 128, 1, 0.87, 3.0, launch_ring<Tile256x128>},
     {256, 256, 1, 1.45, 8.0, launch_ring<Tile256x256>}};
 
-constexpr double kCus = 256, kBytesPerUs = 5.2e6;
+constexpr int kCus = 256;
+constexpr double kBytesPerUs = 5.2e6;
 
 double estimate(const Variant& v, const I8Args& a) {
   // by expert the rows' split is not known here: half a tile more for each
@@ -692,7 +695,9 @@ hipError_t launch_gathered_far(const I8Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + kBN - 1) / kBN;
   const int64_t tiles = tiles_n * i8_tiles_m(a, kBM);
   if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(int8_tile_kernel, dim3((unsigned)tiles), dim3(256), 0, stream, a, (int)tiles_n);
+  const int64_t most = (int64_t)kCus * 8;  // what runs at once takes tile after tile
+  hipLaunchKernelGGL(int8_tile_kernel, dim3((unsigned)(tiles < most ? tiles : most)), dim3(256), 0, stream, a,
+                     (int)tiles_n);
   return hipGetLastError();
 }
 

@@ -404,10 +404,11 @@ int int8gemm_run_grouped(const int8_t *A, const float *scaleA, int64_t rowsA,
  *   ids[t]     = the k experts of largest c that stay, in falling order of c
  *                (ties: the lower expert);
  *   weights[t] = scale * s[ids], divided by the sum of s[ids] when renormalize.
- * The bias counts for the choice alone.  A logit of -inf takes its expert out;
- * where fewer than k experts are left, ids ends in -1 with weight 0.  A NaN
- * score ranks below every number (softmax: a NaN or +inf logit makes the whole
- * row NaN: its available experts are taken in order, with NaN weights).
+ * The bias counts for the choice alone.  A logit or a bias of -inf takes its
+ * expert out; where fewer than k experts are left, ids ends in -1 with weight
+ * 0.  A NaN score ranks below every number (softmax: a NaN or +inf logit makes
+ * the whole row NaN: the experts without a -inf logit are taken in order, with
+ * NaN weights).
  * Without bias and with group_top == 1 (or one group) the order is that of the
  * logits, which is that of the scores; otherwise c is formed in 64 bits, and
  * values of c that agree in their first 42 bits count as equal.  weights are

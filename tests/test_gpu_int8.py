@@ -382,6 +382,24 @@ def test_gathered_rows_past_4_gib():
     assert torch.isnan(got[4:6]).all()
 
 
+def test_many_gathered_rows_past_4_gib():
+    """More tiles than run at once of the kernel that takes such an A."""
+    say("many gathered rows past 4 GiB")
+    b = binding()
+    T, K, N, E, rows = 262144 + 70, 16384, 100, 3, 64 * 2048 + 17
+    used = torch.tensor([T - 1, 0, 262143, 262144, 131072, 7], device=DEV)
+    a = torch.empty((T, K), dtype=torch.int8, device=DEV)
+    a[used] = torch.empty((len(used), K), dtype=torch.int8, device=DEV).random_(-128, 128)
+    w = torch.empty((E, N, K), dtype=torch.int8, device=DEV).random_(-128, 128)
+    bounds = [0, 50001, 50001, rows]
+    pick = torch.arange(rows, device=DEV) * 7 // 5 % len(used)
+    got = b.int8gemm_run_grouped(a, torch.ones(T, device=DEV), w, torch.ones(E, N, device=DEV),
+                                 torch.tensor(bounds, dtype=torch.int32, device=DEV), index=used[pick].int())
+    for e in range(E):
+        want = (a[used].double() @ w[e].double().t()).float()
+        assert torch.equal(got[bounds[e]:bounds[e + 1]], want[pick[bounds[e]:bounds[e + 1]]]), e
+
+
 def test_output_past_4_gib():
     say("output past 4 GiB")
     b = binding()
