@@ -3,7 +3,9 @@
 The computation is C = (A * 2^sA)(B * 2^sB)^T over operands stored as FP8
 (E4M3, E5M2), packed E2M1, packed FP6 (E2M3, E3M2) or packed INT4 / INT2 codes
 with one UE8M0 scale per 32 contiguous K elements, fp32 output; a dense fp16
-GEMM is the comparison path.  All arithmetic runs in the
+GEMM is the comparison path.  Beside it are int8 products with one scale per
+token and output channel, dense and by expert, and the router, plan and
+combination of a layer of experts.  All arithmetic runs in the
 HIP kernels of ``libmxgemm.so`` behind a C ABI (``include/mxgemm.h``); the
 Python binding in :mod:`block_scaled_precision_mxgemm_amd.mxgemm` only
 marshals torch device tensors to it.

@@ -321,19 +321,21 @@ def _arg(t, name: str, dtypes, shape=None, dim: int | None = None, like: torch.T
     return t
 
 
-def _new(shape, dtype, like: torch.Tensor, stream=None, make=torch.empty) -> torch.Tensor:
+def _new(shape, dtype, device: torch.device, stream=None, make=torch.empty) -> torch.Tensor:
     """A tensor for a call on `stream`: it is made there, since memory of the
     current stream's pool may still be in use by work queued on that one."""
     if stream is None:
-        return make(*shape, dtype=dtype, device=like.device)
+        return make(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return make(*shape, dtype=dtype, device=like.device)
+        return make(*shape, dtype=dtype, device=device)
 
 
 def _out(t, name: str, dtype, shape, like: torch.Tensor, stream=None) -> torch.Tensor:
-    if t is None:
-        return _new(shape, dtype, like, stream)
-    return _arg(t, name, (dtype,), shape, like=like)
+    if t is not None:
+        return _arg(t, name, (dtype,), shape, like=like)
+    if stream is not None:
+        return _new(shape, dtype, like.device, stream)
+    return torch.empty(*shape, dtype=dtype, device=like.device)
 
 
 _FLOATS = tuple(_DTYPE_IDS)
@@ -343,24 +345,21 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-# The current stream's handle without a Stream object around it (2 us less per
-# call, of about 9), where this torch has it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# Without Stream and device objects around them, where this torch has them (2
+# us less per call, of about 9): the current stream's handle, the current device.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name: str, device: torch.device, stream, *args):
     """An entry point on the operands' own device; without a stream, on that
     device's current one."""
-    if torch.cuda.current_device() != device.index:
+    index = device.index
+    if _current_device() != index:
         with torch.cuda.device(device):
             return _call(name, device, stream, *args)
-    if stream is not None:
-        handle = stream.cuda_stream
-    elif _raw_stream is not None:
-        handle = _raw_stream(device.index)
-    else:
-        handle = torch.cuda.current_stream().cuda_stream
-    rc = getattr(_load(), name)(*args, handle)
+    rc = getattr(_lib or _load(), name)(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, name)
 
@@ -483,14 +482,14 @@ def expert_plan(ids, experts: int, offsets: torch.Tensor | None = None, order: t
     n = T * k
     if offsets is None and order is None and position is None:
         # one allocation for the three (2 us less than three)
-        offsets, order, position = _new((experts + 1 + 2 * n,), torch.int32, ids, stream).split_with_sizes(
+        offsets, order, position = _new((experts + 1 + 2 * n,), torch.int32, ids.device, stream).split_with_sizes(
             (experts + 1, n, n))
         position = position.view(T, k)
     else:
         offsets = _out(offsets, "offsets", torch.int32, (experts + 1,), ids, stream)
         order = _out(order, "order", torch.int32, (n,), ids, stream)
         position = _out(position, "position", torch.int32, (T, k), ids, stream)
-    workspace = _new((need,), torch.uint8, ids, stream) if need else None
+    workspace = _new((need,), torch.uint8, ids.device, stream) if need else None
     _call("expert_plan", ids.device, stream, ids.data_ptr(), T, k, experts, offsets.data_ptr(), order.data_ptr(),
           position.data_ptr(), _ptr(workspace))
     return offsets, order, position
@@ -526,7 +525,7 @@ def expert_combine_backward(d_out, y, position, weights, d_y: torch.Tensor | Non
     y, position, weights, rows, N, T, k = _combine_args(y, position, weights)
     d_out = _arg(d_out, "d_out", _FLOATS, (T, N), like=y)
     if d_y is None:
-        d_y = _new((rows, N), y.dtype, y, stream, torch.zeros)
+        d_y = _new((rows, N), y.dtype, y.device, stream, torch.zeros)
     d_y = _arg(d_y, "d_y", (y.dtype,), (rows, N), like=y)
     d_weights = _out(d_weights, "d_weights", torch.float32, (T, k), y, stream)
     _call("expert_combine_backward", y.device, stream, d_out.data_ptr(), _DTYPE_IDS[d_out.dtype], y.data_ptr(),
