@@ -91,55 +91,78 @@ __global__ __launch_bounds__(kCThreads) void combine_kernel(CombineArgs a) {
   save8<O, true>(a.out, t, a.N, n, s);
 }
 
-// A wave per slot, two pieces of a row at a time.  2047 tokens of 8 choices and
-// 4096 columns (bf16): 66 us from memory, 4.3 TB/s of reads and writes in equal
-// parts, of which a large copy reaches 5.0.  A workgroup per token, which reads
-// the token's gradient once for all its choices, takes 69 us there (8192 x 4:
-// 120 instead of 130) and twice as long for few tokens; the gradient comes from
-// the L2 for the second choice on anyway.
-template <int Y, int O>
+// W waves per slot, two pieces of a row at a time.  2047 tokens of 8 choices
+// and 4096 columns (bf16), a wave for each slot: 64 us from memory, 4.4 TB/s of
+// reads and writes in equal parts, of which a large copy reaches 5.0.  A
+// workgroup per token, which reads the token's gradient once for all its
+// choices, takes 69 us there and twice as long for few tokens; the gradient
+// comes from the L2 for the second choice on anyway.
+template <int Y, int O, int W, bool NT>  // W: 1 or 4
 __global__ __launch_bounds__(kCThreads) void combine_backward_kernel(CombineArgs a, void* __restrict__ dY,
                                                                      float* __restrict__ dW) {
-  const int lane = threadIdx.x & 63;
+  __shared__ float part[kCThreads / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t group = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-  const int64_t slot = group * (kCThreads / 64) + (threadIdx.x >> 6);
+  const int64_t slot = (group * (kCThreads / 64) + wave) / W;
   if (slot >= a.T * a.k) return;
   const int64_t t = slot / a.k;
   const int p = a.position[slot];
   const bool live = p >= 0 && p < a.rows;
   const float w = live ? a.weights[slot] : 0.0f;
+  constexpr int STEP = 512 * W;
   float dot = 0.0f;
   if (live)
-    for (int64_t n = lane * 8; n < a.N; n += 1024) {
+    for (int64_t n = (W == 1 ? lane : (int)threadIdx.x) * 8; n < a.N; n += 2 * STEP) {
       float d[2][8], y[2][8];
 #pragma unroll
       for (int u = 0; u < 2; u++)
-        if (n + 512 * u < a.N) {
-          load8<Y, true>(a.Y, p, a.N, n + 512 * u, y[u]);
-          load8<O, false>(a.out, t, a.N, n + 512 * u, d[u]);
+        if (n + STEP * u < a.N) {
+          load8<Y, true>(a.Y, p, a.N, n + STEP * u, y[u]);
+          load8<O, false>(a.out, t, a.N, n + STEP * u, d[u]);
         }
 #pragma unroll
       for (int u = 0; u < 2; u++)
-        if (n + 512 * u < a.N) {
+        if (n + STEP * u < a.N) {
 #pragma unroll
           for (int i = 0; i < 8; i++) {
             dot = fmaf(d[u][i], y[u][i], dot);
             d[u][i] *= w;
           }
-          save8<Y, false>(dY, p, a.N, n + 512 * u, d[u]);
+          save8<Y, NT>(dY, p, a.N, n + STEP * u, d[u]);
         }
     }
   dot = wave_sum(dot);
-  if (lane == 0) dW[slot] = dot;
+  if (W == 1) {
+    if (lane == 0) dW[slot] = dot;
+  } else {
+    if (lane == 0) part[wave] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) dW[slot] = (part[0] + part[1]) + (part[2] + part[3]);
+  }
+}
+
+template <int Y, int O, int W, bool NT>
+void backward_launch(const CombineArgs& a, void* dY, float* dW, hipStream_t stream) {
+  // in two dimensions: a launch has less than 2^32 threads in one
+  const int64_t groups = (a.T * a.k * W + kCThreads / 64 - 1) / (kCThreads / 64), most = 1 << 20;
+  const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)((groups + most - 1) / most));
+  hipLaunchKernelGGL((combine_backward_kernel<Y, O, W, NT>), grid, dim3(kCThreads), 0, stream, a, dY, dW);
 }
 
 template <int Y, int O>
 hipError_t combine_launch(const CombineArgs& a, void* dY, float* dW, hipStream_t stream) {
   if (dW != nullptr) {
-    // in two dimensions: a launch has less than 2^32 threads in one
-    const int64_t groups = (a.T * a.k + kCThreads / 64 - 1) / (kCThreads / 64), most = 1 << 20;
-    const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)((groups + most - 1) / most));
-    hipLaunchKernelGGL((combine_backward_kernel<Y, O>), grid, dim3(kCThreads), 0, stream, a, dY, dW);
+    // Few slots of long rows: four waves for each (64 tokens of 8 and 7168
+    // columns: 8.0 us instead of 13.8, 256 of 8: 16.8 and 20.7, 512 of 8: 29.6
+    // and 27.9).  Many: rows that leave no trace in the caches (4096 tokens of 8
+    // and 7168 columns: 191 us instead of 206; 512 of 8 and 4096: 18.5 and 17.7).
+    const int64_t slots = a.T * a.k;
+    if (slots <= 2048 && a.N > 512)
+      backward_launch<Y, O, 4, false>(a, dY, dW, stream);
+    else if (slots * a.N * (int64_t)sizeof(typename RowElem<Y>::type) > ((int64_t)96 << 20))
+      backward_launch<Y, O, 1, true>(a, dY, dW, stream);
+    else
+      backward_launch<Y, O, 1, false>(a, dY, dW, stream);
   } else {
     const unsigned cols = (unsigned)((a.N + kCThreads * 8 - 1) / (kCThreads * 8));
     hipLaunchKernelGGL((combine_kernel<Y, O>), dim3((unsigned)a.T, cols), dim3(kCThreads), 0, stream, a);

@@ -384,6 +384,38 @@ def test_combine_rows_past_4_gib():
     assert (d_y[-1] == 1).all() and (d_y[70000] == 10).all() and (d_y[3] == 100).all()
 
 
+@pytest.mark.parametrize("T,k,N", [(700, 3, 1041), (257, 8, 513), (2049, 1, 520)])
+def test_combine_long_rows_of_many_slots(T, k, N):
+    say("combine many slots", T, k, N)
+    _check_combine(T, k, N, 1, 1, T + N, missing=True)
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("T,k,N", [(6300, 8, 1027), (40, 64, 30000)])
+def test_combine_backward_of_large_rows(kind, T, k, N):
+    """Rows of more than 96 MB together, and of a few of them without a slot."""
+    say("combine backward large", kind, T, k, N)
+    b = binding()
+    rows = T * k + 5
+    slot = torch.randperm(rows, device=DEV)[:T * k]
+    pos = slot.int().view(T, k)
+    pos[1, 1] = -1
+    y = torch.randint(-2, 3, (rows, N), device=DEV).to(TYPES[kind])
+    d = torch.randint(-1, 2, (T, N), device=DEV).to(TYPES[kind])
+    w = torch.randint(-3, 4, (T, k), device=DEV).float()
+    d_y, d_w = b.expert_combine_backward(d, y, pos, w)
+    want_y = torch.zeros_like(y)
+    # whole numbers: sums below 2^24, products of at most 3
+    for j in range(k):
+        live = pos[:, j] >= 0
+        at = pos[live, j].long()
+        want_y[at] = (w[live, j, None] * d[live].float()).to(TYPES[kind])
+        want_w = torch.zeros(T, device=DEV)
+        want_w[live] = (y[at].float() * d[live].float()).sum(1)
+        assert torch.equal(d_w[:, j], want_w), j
+    assert torch.equal(d_y, want_y)
+
+
 def test_combine_most_slots():
     """As many slots as a call can have: 2^20 tokens of 64 choices."""
     say("combine most slots")
