@@ -92,11 +92,4 @@ __device__ __forceinline__ V wave_sum(V x) {
   return x;
 }
 
-// fmaxf takes the other operand of a NaN
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
-  return x;
-}
-
 }  // namespace mxg

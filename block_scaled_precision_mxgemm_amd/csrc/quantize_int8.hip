@@ -90,19 +90,20 @@ __device__ __forceinline__ float magnitude(uint32_t m) {
     return RowElem<IN>::get((uint16_t)max(m & 0xffffu, m >> 16));
 }
 
-// WPR waves per row, 4 / WPR rows per workgroup.  HELD > 0: the row's 16-byte
-// pieces, at most HELD of them a lane, stay in registers between the maximum
-// and the codes, so that the row is read once; HELD = 0: longer rows are read
-// twice, the second time from the caches.
-template <int IN, int HELD, int WPR>
-__global__ __launch_bounds__(256) void quantize_int8_kernel(const typename RowElem<IN>::type* __restrict__ X,
-                                                            int64_t rows, int64_t K, int8_t* __restrict__ Q,
-                                                            float* __restrict__ S) {
-  constexpr int VEC = RowElem<IN>::VEC, NT = WPR * 64;
-  __shared__ float part[4];
-  const int64_t row = WPR == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+// L lanes per row, in workgroups of 256 or (L = 1024) 1024.  HELD > 0: the
+// row's 16-byte pieces, at most HELD of them a lane, stay in registers between
+// the maximum and the codes, so that the row is read once; HELD = 0: longer
+// rows are read twice, the second time from the caches.
+constexpr int rows_threads(int L) { return L > 256 ? L : 256; }
+template <int IN, int HELD, int L>
+__global__ __launch_bounds__(rows_threads(L)) void quantize_int8_kernel(
+    const typename RowElem<IN>::type* __restrict__ X, int64_t rows, int64_t K, int8_t* __restrict__ Q,
+    float* __restrict__ S) {
+  constexpr int VEC = RowElem<IN>::VEC;
+  __shared__ float part[rows_threads(L) / 64];
+  const int64_t row = (int64_t)blockIdx.x * (rows_threads(L) / L) + threadIdx.x / L;
   if (row >= rows) return;
-  const int tid = threadIdx.x % NT;
+  const int tid = threadIdx.x % L;
   const v4i* x = reinterpret_cast<const v4i*>(X + row * K);
   const int nv = (int)(K / VEC);
   uint32_t most = 0;
@@ -110,22 +111,23 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(const typename RowEl
   if constexpr (HELD > 0) {
 #pragma unroll
     for (int u = 0; u < HELD; u++) {
-      const int i = tid + u * NT;
+      const int i = tid + u * L;
       held[u] = i < nv ? __builtin_nontemporal_load(x + i) : v4i{0, 0, 0, 0};
     }
 #pragma unroll
     for (int u = 0; u < HELD; u++) most = larger_bits<IN>(most, held[u]);
   } else {
-    for (int i = tid; i < nv; i += NT) most = larger_bits<IN>(most, x[i]);
+    for (int i = tid; i < nv; i += L) most = larger_bits<IN>(most, x[i]);
   }
   float amax = magnitude<IN>(most);
   if (!(amax < __builtin_inff())) amax = __builtin_inff();  // a NaN too
-  amax = wave_max(amax);
-  if constexpr (WPR == 4) {
+#pragma unroll
+  for (int d = (L < 64 ? L : 64) / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
+  if constexpr (L > 64) {
     if ((tid & 63) == 0) part[tid >> 6] = amax;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 4; w++) amax = fmaxf(amax, part[w]);
+    for (int w = 0; w < L / 64; w++) amax = fmaxf(amax, part[w]);
   }
   const bool finite = amax < __builtin_inff();
   float s = amax / 127.0f;
@@ -135,51 +137,61 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(const typename RowEl
   const float inv = live ? 1.0f / s : 0.0f, half = 0.5f * s;
   int8_t* q = Q + row * K;
   if (!live) {
-    for (int i = tid; i < (int)(K / 16); i += NT) reinterpret_cast<v4i*>(q)[i] = v4i{0, 0, 0, 0};
+    for (int i = tid; i < (int)(K / 16); i += L) reinterpret_cast<v4i*>(q)[i] = v4i{0, 0, 0, 0};
   } else if constexpr (HELD > 0) {
 #pragma unroll
     for (int u = 0; u < HELD; u++) {
-      const int i = tid + u * NT;
+      const int i = tid + u * L;
       if (i < nv) put_codes<IN>(q + (int64_t)i * VEC, held[u], s, inv, half);
     }
   } else {
-    for (int i = tid; i < nv; i += NT) put_codes<IN>(q + (int64_t)i * VEC, x[i], s, inv, half);
+    for (int i = tid; i < nv; i += L) put_codes<IN>(q + (int64_t)i * VEC, x[i], s, inv, half);
   }
 }
 
-template <int IN, int HELD, int WPR>
+template <int IN, int HELD, int L>
 void quantize_rows(const void* X, int64_t rows, int64_t K, int8_t* Q, float* S, hipStream_t stream) {
-  const int64_t grid = WPR == 4 ? rows : (rows + 3) / 4;
-  hipLaunchKernelGGL((quantize_int8_kernel<IN, HELD, WPR>), dim3((unsigned)grid), dim3(256), 0, stream,
-                     (const typename RowElem<IN>::type*)X, rows, K, Q, S);
+  constexpr int threads = rows_threads(L), per = threads / L;
+  hipLaunchKernelGGL((quantize_int8_kernel<IN, HELD, L>), dim3((unsigned)((rows + per - 1) / per)), dim3(threads), 0,
+                     stream, (const typename RowElem<IN>::type*)X, rows, K, Q, S);
 }
 
-// A wave for each row where there are enough rows to fill the chip and a row
-// is short (no barrier, no idle threads: 100000 x 512 bf16 in 43 us against
-// 82 with a workgroup each), else a workgroup for each.
+// Short rows share a wave (100000 x 128 bf16: 13 us, 34 with a wave each).  A
+// wave for each row where there are enough of them to fill the chip (no barrier,
+// no idle threads: 100000 x 512 in 43 us, 82 with a workgroup each).  Few rows,
+// and long ones, have 16 waves each (16 x 14336: 3.7 us, 5.1 with 4 waves; 4096
+// x 28672: 58 and 62; but 2047 x 8192: 15.7 and 12.6).
 template <int IN>
 void quantize_in(const void* X, int64_t rows, int64_t K, int8_t* Q, float* S, hipStream_t stream) {
   const int64_t pieces = K / RowElem<IN>::VEC;
-  if (rows >= 2048 && pieces <= 8 * 64) {
-    if (pieces <= 64)
-      quantize_rows<IN, 1, 1>(X, rows, K, Q, S, stream);
-    else if (pieces <= 2 * 64)
-      quantize_rows<IN, 2, 1>(X, rows, K, Q, S, stream);
-    else if (pieces <= 4 * 64)
-      quantize_rows<IN, 4, 1>(X, rows, K, Q, S, stream);
-    else
-      quantize_rows<IN, 8, 1>(X, rows, K, Q, S, stream);
-  } else if (pieces <= 2 * 256) {
-    quantize_rows<IN, 2, 4>(X, rows, K, Q, S, stream);
-  } else if (pieces <= 4 * 256) {
-    quantize_rows<IN, 4, 4>(X, rows, K, Q, S, stream);
-  } else if (pieces <= 8 * 256) {
-    quantize_rows<IN, 8, 4>(X, rows, K, Q, S, stream);
-  } else if (pieces <= 16 * 256) {
-    quantize_rows<IN, 16, 4>(X, rows, K, Q, S, stream);
-  } else {
-    quantize_rows<IN, 0, 4>(X, rows, K, Q, S, stream);
-  }
+  if (pieces <= 16)
+    quantize_rows<IN, 1, 16>(X, rows, K, Q, S, stream);
+  else if (pieces <= 2 * 16)
+    quantize_rows<IN, 2, 16>(X, rows, K, Q, S, stream);
+  else if (rows >= 2048 && pieces <= 64)
+    quantize_rows<IN, 1, 64>(X, rows, K, Q, S, stream);
+  else if (rows >= 2048 && pieces <= 2 * 64)
+    quantize_rows<IN, 2, 64>(X, rows, K, Q, S, stream);
+  else if (rows >= 2048 && pieces <= 4 * 64)
+    quantize_rows<IN, 4, 64>(X, rows, K, Q, S, stream);
+  else if (rows >= 2048 && pieces <= 8 * 64)
+    quantize_rows<IN, 8, 64>(X, rows, K, Q, S, stream);
+  else if (pieces <= 2 * 256)
+    quantize_rows<IN, 2, 256>(X, rows, K, Q, S, stream);
+  else if (rows > 512 && pieces <= 4 * 256)
+    quantize_rows<IN, 4, 256>(X, rows, K, Q, S, stream);
+  else if (rows > 512 && pieces <= 8 * 256)
+    quantize_rows<IN, 8, 256>(X, rows, K, Q, S, stream);
+  else if (pieces <= 2 * 1024)
+    quantize_rows<IN, 2, 1024>(X, rows, K, Q, S, stream);
+  else if (pieces <= 4 * 1024)
+    quantize_rows<IN, 4, 1024>(X, rows, K, Q, S, stream);
+  else if (pieces <= 8 * 1024)
+    quantize_rows<IN, 8, 1024>(X, rows, K, Q, S, stream);
+  else if (pieces <= 16 * 1024)
+    quantize_rows<IN, 16, 1024>(X, rows, K, Q, S, stream);
+  else
+    quantize_rows<IN, 0, 1024>(X, rows, K, Q, S, stream);
 }
 
 }  // namespace

@@ -77,6 +77,23 @@ def test_quantize_special_rows(kind):
     _check_quantize(dev(x).to(TYPES[kind]))
 
 
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("rows,K", [(1000, 16), (37, 64), (33, 128), (65, 112), (19, 256), (2050, 512), (2049, 1040),
+                                    (2051, 2048), (2048, 4096), (700, 4096), (600, 8192), (513, 16384), (512, 8208),
+                                    (3, 16400), (2, 32784), (1, 65536), (2, 131088)])
+def test_quantize_row_lengths(kind, rows, K):
+    """Every number of lanes per row; rows that are zero or not finite beside others."""
+    say("quantize row lengths", kind, rows, K)
+    x = np.random.default_rng(rows + K + kind).standard_normal((rows, K), dtype=np.float32)
+    x[:, ::53] *= 9.0
+    if rows > 16:
+        x[3::16] = 0.0
+        x[5::17, K - 1] = np.nan
+        x[7::19, 0] = np.inf
+        x[11::23, K // 2] = -np.inf
+    _check_quantize(dev(x).to(TYPES[kind]))
+
+
 def test_quantize_near_borders():
     """fp32 values one step to either side of every border between two codes."""
     say("quantize borders")
