@@ -63,11 +63,12 @@ __device__ __forceinline__ void save8(void* base, int64_t row, int64_t N, int64_
 // same for all its lanes, and the rows of 4 choices are loaded at a time.  8192
 // tokens of 4 choices and 4096 columns (bf16): 58 us, 5.8 TB/s; 66 with rows
 // that stay in the caches, 69 with a choice at a time.
-template <int Y, int O>
+// L = 16: for rows of at most 128 columns, 16 tokens in a workgroup.
+template <int Y, int O, int L>
 __global__ __launch_bounds__(kCThreads) void combine_kernel(CombineArgs a) {
-  const int64_t t = blockIdx.x;
-  const int64_t n = ((int64_t)blockIdx.y * kCThreads + threadIdx.x) * 8;
-  if (n >= a.N) return;
+  const int64_t t = (int64_t)blockIdx.x * (kCThreads / L) + (L < kCThreads ? threadIdx.x / L : 0);
+  const int64_t n = ((int64_t)blockIdx.y * L + threadIdx.x % L) * 8;
+  if (t >= a.T || n >= a.N) return;
   const int32_t* pos = a.position + t * a.k;
   const float* wt = a.weights + t * a.k;
   float s[8] = {};
@@ -91,28 +92,28 @@ __global__ __launch_bounds__(kCThreads) void combine_kernel(CombineArgs a) {
   save8<O, true>(a.out, t, a.N, n, s);
 }
 
-// W waves per slot, two pieces of a row at a time.  2047 tokens of 8 choices
+// L lanes per slot, two pieces of a row at a time.  2047 tokens of 8 choices
 // and 4096 columns (bf16), a wave for each slot: 64 us from memory, 4.4 TB/s of
 // reads and writes in equal parts, of which a large copy reaches 5.0.  A
 // workgroup per token, which reads the token's gradient once for all its
 // choices, takes 69 us there and twice as long for few tokens; the gradient
 // comes from the L2 for the second choice on anyway.
-template <int Y, int O, int W, bool NT>  // W: 1 or 4
+template <int Y, int O, int L, bool NT>
 __global__ __launch_bounds__(kCThreads) void combine_backward_kernel(CombineArgs a, void* __restrict__ dY,
                                                                      float* __restrict__ dW) {
   __shared__ float part[kCThreads / 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x % L;
   const int64_t group = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-  const int64_t slot = (group * (kCThreads / 64) + wave) / W;
+  const int64_t slot = group * (kCThreads / L) + threadIdx.x / L;
   if (slot >= a.T * a.k) return;
   const int64_t t = slot / a.k;
   const int p = a.position[slot];
   const bool live = p >= 0 && p < a.rows;
   const float w = live ? a.weights[slot] : 0.0f;
-  constexpr int STEP = 512 * W;
+  constexpr int STEP = 8 * L;
   float dot = 0.0f;
   if (live)
-    for (int64_t n = (W == 1 ? lane : (int)threadIdx.x) * 8; n < a.N; n += 2 * STEP) {
+    for (int64_t n = lane * 8; n < a.N; n += 2 * STEP) {
       float d[2][8], y[2][8];
 #pragma unroll
       for (int u = 0; u < 2; u++)
@@ -131,41 +132,56 @@ __global__ __launch_bounds__(kCThreads) void combine_backward_kernel(CombineArgs
           save8<Y, NT>(dY, p, a.N, n + STEP * u, d[u]);
         }
     }
-  dot = wave_sum(dot);
-  if (W == 1) {
-    if (lane == 0) dW[slot] = dot;
-  } else {
-    if (lane == 0) part[wave] = dot;
+#pragma unroll
+  for (int d = (L < 64 ? L : 64) / 2; d > 0; d >>= 1) dot += __shfl_xor(dot, d);
+  if constexpr (L > 64) {
+    if ((lane & 63) == 0) part[lane >> 6] = dot;
     __syncthreads();
-    if (threadIdx.x == 0) dW[slot] = (part[0] + part[1]) + (part[2] + part[3]);
+    dot = (part[0] + part[1]) + (part[2] + part[3]);
   }
+  if (lane == 0) dW[slot] = dot;
 }
 
-template <int Y, int O, int W, bool NT>
+template <int Y, int O, int L, bool NT>
 void backward_launch(const CombineArgs& a, void* dY, float* dW, hipStream_t stream) {
   // in two dimensions: a launch has less than 2^32 threads in one
-  const int64_t groups = (a.T * a.k * W + kCThreads / 64 - 1) / (kCThreads / 64), most = 1 << 20;
+  const int64_t groups = (a.T * a.k + kCThreads / L - 1) / (kCThreads / L), most = 1 << 20;
   const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)((groups + most - 1) / most));
-  hipLaunchKernelGGL((combine_backward_kernel<Y, O, W, NT>), grid, dim3(kCThreads), 0, stream, a, dY, dW);
+  hipLaunchKernelGGL((combine_backward_kernel<Y, O, L, NT>), grid, dim3(kCThreads), 0, stream, a, dY, dW);
+}
+
+template <int Y, int O, int L>
+void combine_tokens(const CombineArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.T + kCThreads / L - 1) / (kCThreads / L)), (unsigned)((a.N + L * 8 - 1) / (L * 8)));
+  hipLaunchKernelGGL((combine_kernel<Y, O, L>), grid, dim3(kCThreads), 0, stream, a);
 }
 
 template <int Y, int O>
 hipError_t combine_launch(const CombineArgs& a, void* dY, float* dW, hipStream_t stream) {
   if (dW != nullptr) {
-    // Few slots of long rows: four waves for each (64 tokens of 8 and 7168
-    // columns: 8.0 us instead of 13.8, 256 of 8: 16.8 and 20.7, 512 of 8: 29.6
-    // and 27.9).  Many: rows that leave no trace in the caches (4096 tokens of 8
-    // and 7168 columns: 191 us instead of 206; 512 of 8 and 4096: 18.5 and 17.7).
+    // Short rows: 16 lanes for each (20000 tokens of 2 and 100 columns: 11.8 us
+    // instead of 25.9).  Few slots of long rows: four waves for each (64 tokens
+    // of 8 and 7168 columns: 8.0 us instead of 13.8, 256 of 8: 16.8 and 20.7, but
+    // 512 of 8: 29.6 and 27.9).  Many: rows that leave no trace in the caches
+    // (4096 tokens of 8 and 7168 columns: 191 us instead of 206, but 512 of 8 and
+    // 4096: 18.5 and 17.7).
     const int64_t slots = a.T * a.k;
-    if (slots <= 2048 && a.N > 512)
-      backward_launch<Y, O, 4, false>(a, dY, dW, stream);
+    if (a.N <= 16 * 8)
+      backward_launch<Y, O, 16, false>(a, dY, dW, stream);
+    else if (slots <= 2048 && a.N > 64 * 8)
+      backward_launch<Y, O, 256, false>(a, dY, dW, stream);
     else if (slots * a.N * (int64_t)sizeof(typename RowElem<Y>::type) > ((int64_t)96 << 20))
-      backward_launch<Y, O, 1, true>(a, dY, dW, stream);
+      backward_launch<Y, O, 64, true>(a, dY, dW, stream);
     else
-      backward_launch<Y, O, 1, false>(a, dY, dW, stream);
+      backward_launch<Y, O, 64, false>(a, dY, dW, stream);
   } else {
-    const unsigned cols = (unsigned)((a.N + kCThreads * 8 - 1) / (kCThreads * 8));
-    hipLaunchKernelGGL((combine_kernel<Y, O>), dim3((unsigned)a.T, cols), dim3(kCThreads), 0, stream, a);
+    // Short rows share a workgroup (20000 tokens of 2 and 100 columns: 7.6 us,
+    // 22.5 with a workgroup each; with 64 lanes for up to 512 columns nothing
+    // was gained).
+    if (a.N <= 16 * 8)
+      combine_tokens<Y, O, 16>(a, stream);
+    else
+      combine_tokens<Y, O, 256>(a, stream);
   }
   return hipGetLastError();
 }

@@ -1,5 +1,5 @@
 // mxg_rows.h - rows of fp32, bf16 or fp16 elements as the int8 quantizer and
-// the expert kernels read and write them, and reductions over a wave.
+// the expert kernels read and write them, and scans over a wave.
 #pragma once
 
 #include "mxg_epilogue.h"
@@ -82,13 +82,6 @@ __device__ __forceinline__ int wave_scan(int x) {  // MAX: values of at least 0
   x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
   x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
   x = scan_op<MAX>(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
-  return x;
-}
-
-template <class V>
-__device__ __forceinline__ V wave_sum(V x) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
   return x;
 }
 

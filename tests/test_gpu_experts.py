@@ -384,9 +384,10 @@ def test_combine_rows_past_4_gib():
     assert (d_y[-1] == 1).all() and (d_y[70000] == 10).all() and (d_y[3] == 100).all()
 
 
-@pytest.mark.parametrize("T,k,N", [(700, 3, 1041), (257, 8, 513), (2049, 1, 520)])
-def test_combine_long_rows_of_many_slots(T, k, N):
-    say("combine many slots", T, k, N)
+@pytest.mark.parametrize("T,k,N", [(700, 3, 1041), (257, 8, 513), (2049, 1, 520), (1001, 2, 128), (77, 5, 129), (333, 7, 61),
+                                   (1500, 1, 16), (2, 64, 127)])
+def test_combine_row_lengths(T, k, N):
+    say("combine row lengths", T, k, N)
     _check_combine(T, k, N, 1, 1, T + N, missing=True)
 
 
