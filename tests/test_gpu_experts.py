@@ -149,6 +149,29 @@ def test_route_close_scores(score):
     _check_route(x, 8, score, bias=bias, groups=8, top_groups=3, group_top=2)
 
 
+def test_route_logits_past_4_gib():
+    """The last of 2^20 tokens over 1024 experts, against calls of those tokens alone."""
+    say("route past 4 GiB")
+    b = binding()
+    T, E, k = 1 << 20, 1024, 3
+    x = torch.empty((T, E), device=DEV)
+    rows = torch.tensor([0, 1, 524287, 524288, T - 2, T - 1], device=DEV)
+    x.fill_(0.5)
+    x[rows] = torch.randn((6, E), device=DEV)
+    bias = torch.randn(E, device=DEV) * 0.1
+    for kw in ({}, {"score": b.SCORE_SIGMOID, "bias": bias, "groups": 8, "top_groups": 2, "group_top": 2}):
+        ids, w = b.expert_route(x, k, **kw)
+        some, few = b.expert_route(x[rows].contiguous(), k, **kw)
+        assert torch.equal(ids[rows], some) and torch.equal(w[rows], few)
+    dw = torch.randn((T, k), device=DEV)
+    d = torch.full((T, E), 7.0, device=DEV)
+    for renormalize in (True, False):
+        b.expert_route_backward(x, ids, dw, renormalize=renormalize, d_logits=d)
+        want = b.expert_route_backward(x[rows].contiguous(), ids[rows].contiguous(), dw[rows].contiguous(),
+                                       renormalize=renormalize)
+        assert torch.equal(d[rows], want)
+
+
 # ---- gradient ---------------------------------------------------------------
 
 

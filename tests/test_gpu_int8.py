@@ -94,6 +94,18 @@ def test_quantize_row_lengths(kind, rows, K):
     _check_quantize(dev(x).to(TYPES[kind]))
 
 
+@pytest.mark.parametrize("rows,K", [(1 << 18, 16384), (4100, 1 << 20), (1 << 20, 4096)])
+def test_quantize_past_4_gib(rows, K):
+    say("quantize past 4 GiB", rows, K)
+    b = binding()
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device=DEV)
+    some = torch.tensor([0, rows // 2 - 1, rows // 2, rows - 2, rows - 1], device=DEV)
+    x[some] = torch.randn((5, K), device=DEV).to(torch.bfloat16)
+    q, s = b.int8gemm_quantize(x)
+    qr, sr = ref.quantize(x[some].float().cpu().numpy())
+    assert np.array_equal(s[some].cpu().numpy(), sr) and np.array_equal(q[some].cpu().numpy(), qr)
+
+
 def test_quantize_near_borders():
     """fp32 values one step to either side of every border between two codes."""
     say("quantize borders")
