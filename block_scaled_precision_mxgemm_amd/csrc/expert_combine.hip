@@ -162,15 +162,16 @@ hipError_t combine_launch(const CombineArgs& a, void* dY, float* dW, hipStream_t
     // Short rows: 16 lanes for each (20000 tokens of 2 and 100 columns: 11.8 us
     // instead of 25.9).  Few slots of long rows: four waves for each (64 tokens
     // of 8 and 7168 columns: 8.0 us instead of 13.8, 256 of 8: 16.8 and 20.7, but
-    // 512 of 8: 29.6 and 27.9).  Many: rows that leave no trace in the caches
-    // (4096 tokens of 8 and 7168 columns: 191 us instead of 206, but 512 of 8 and
-    // 4096: 18.5 and 17.7).
+    // 512 of 8: 29.6 and 27.9).  More than the last cache holds: rows that pass
+    // it by (4096 tokens of 8 and 7168 columns: 191 us instead of 206, 8192 of 4
+    // and 4096: 126 and 129; but 512 of 8 and 4096: 18.5 and 17.7, and what reads
+    // the gradient next would miss it).
     const int64_t slots = a.T * a.k;
     if (a.N <= 16 * 8)
       backward_launch<Y, O, 16, false>(a, dY, dW, stream);
     else if (slots <= 2048 && a.N > 64 * 8)
       backward_launch<Y, O, 256, false>(a, dY, dW, stream);
-    else if (slots * a.N * (int64_t)sizeof(typename RowElem<Y>::type) > ((int64_t)96 << 20))
+    else if (slots * a.N * (int64_t)sizeof(typename RowElem<Y>::type) >= ((int64_t)256 << 20))
       backward_launch<Y, O, 64, true>(a, dY, dW, stream);
     else
       backward_launch<Y, O, 64, false>(a, dY, dW, stream);

@@ -415,9 +415,9 @@ def test_combine_row_lengths(T, k, N):
 
 
 @pytest.mark.parametrize("kind", [0, 1, 2])
-@pytest.mark.parametrize("T,k,N", [(6300, 8, 1027), (40, 64, 30000)])
+@pytest.mark.parametrize("T,k,N", [(6300, 8, 1027), (40, 64, 30000), (16500, 8, 1027), (40, 64, 60000)])
 def test_combine_backward_of_large_rows(kind, T, k, N):
-    """Rows of more than 96 MB together, and of a few of them without a slot."""
+    """Rows of 100 MB and of more than 256 MB together, a few of them without a slot."""
     say("combine backward large", kind, T, k, N)
     b = binding()
     rows = T * k + 5
