@@ -363,7 +363,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
     for (int i = 0; i < kRounds<L>; i++) {
       g[i] = 0.0;
       if (i * L < a.k && id[i] >= 0) {
-        g[i] = w[i] * inv * (dw[i] - dot);
+        // one choice alone has a constant weight: no rounding is left of it
+        g[i] = w[i] * inv * (dw[i] - (w[i] == total ? dw[i] : dot));
         if (!softmax) g[i] *= 1.0 / (1.0 + exp((double)lc[i]));
       }
     }

@@ -222,6 +222,25 @@ def test_route_backward_missing_choices(score, renormalize):
     _check_backward(x, ids, rng.standard_normal((6, 4)).astype(np.float32), score, 0, renormalize)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kind", [0, 1, 2])
+def test_route_backward_of_one_choice(score, kind):
+    """A renormalized weight of one choice is constant: its gradient is zero, exactly."""
+    say("route backward of one choice", score, kind)
+    b = binding()
+    for T, E in ((149, 95), (33, 8), (20, 300)):
+        x = (torch.randn((T, E), device=DEV) * 3).to(TYPES[kind])
+        ids, w = b.expert_route(x, 1, SCORES[score])
+        assert ((w - 1).abs() <= 2.0 ** -23).all()  # p times 1 / p: two roundings
+        dw = torch.randn((T, 1), device=DEV)
+        assert (b.expert_route_backward(x, ids, dw, SCORES[score]) == 0).all()
+        ids = torch.cat([torch.full_like(ids, -1), ids, torch.full_like(ids, -1)], 1)
+        assert (b.expert_route_backward(x, ids, dw.expand(T, 3).contiguous(), SCORES[score], scale=2.5) == 0).all()
+        dw[0] = float("nan")
+        got = b.expert_route_backward(x, ids[:, 1:2].contiguous(), dw, SCORES[score])
+        assert torch.isnan(got[0, ids[0, 1].long()]) and (got[1:] == 0).all()
+
+
 def test_route_backward_against_differences():
     """The kernel's gradient against differences of the kernel's own weights.
     A step of 2^-6 costs h^2/6 times a third derivative below 2 per unit of dw
