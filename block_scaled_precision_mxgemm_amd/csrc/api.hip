@@ -246,7 +246,7 @@ int mxgemm_run_dequant_fp16(const void* A, const uint8_t* scaleA, const void* B,
 
 int int8gemm_quantize(const void* X, int in_type, int64_t rows, int64_t K, int8_t* Q, float* S, void* stream) {
   if (!X || !Q || !S || !type_ok(in_type)) return MXG_EINVAL;
-  if (!dim_ok(rows) || !dim_ok(K) || (K % 16) != 0) return MXG_EINVAL;
+  if (rows < 1 || rows > MXG_MAX_SLOTS || !dim_ok(K) || (K % 16) != 0) return MXG_EINVAL;
   if (!aligned16(X) || !aligned16(Q) || !aligned4(S)) return MXG_EALIGN;
   const int d = check_device();
   if (d != MXG_OK) return d;

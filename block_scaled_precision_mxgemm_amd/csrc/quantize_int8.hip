@@ -101,7 +101,8 @@ __global__ __launch_bounds__(rows_threads(L)) void quantize_int8_kernel(
     float* __restrict__ S) {
   constexpr int VEC = RowElem<IN>::VEC;
   __shared__ float part[rows_threads(L) / 64];
-  const int64_t row = (int64_t)blockIdx.x * (rows_threads(L) / L) + threadIdx.x / L;
+  const int64_t group = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t row = group * (rows_threads(L) / L) + threadIdx.x / L;
   if (row >= rows) return;
   const int tid = threadIdx.x % L;
   const v4i* x = reinterpret_cast<const v4i*>(X + row * K);
@@ -152,8 +153,11 @@ __global__ __launch_bounds__(rows_threads(L)) void quantize_int8_kernel(
 template <int IN, int HELD, int L>
 void quantize_rows(const void* X, int64_t rows, int64_t K, int8_t* Q, float* S, hipStream_t stream) {
   constexpr int threads = rows_threads(L), per = threads / L;
-  hipLaunchKernelGGL((quantize_int8_kernel<IN, HELD, L>), dim3((unsigned)((rows + per - 1) / per)), dim3(threads), 0,
-                     stream, (const typename RowElem<IN>::type*)X, rows, K, Q, S);
+  // in two dimensions: a launch has less than 2^32 threads in one
+  const int64_t groups = (rows + per - 1) / per, most = 1 << 20;
+  const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)((groups + most - 1) / most));
+  hipLaunchKernelGGL((quantize_int8_kernel<IN, HELD, L>), grid, dim3(threads), 0, stream,
+                     (const typename RowElem<IN>::type*)X, rows, K, Q, S);
 }
 
 // Short rows share a wave (100000 x 128 bf16: 13 us, 34 with a wave each).  A

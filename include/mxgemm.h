@@ -323,7 +323,8 @@ const char *mxgemm_status_string(int status);
  *
  *   X        device, rows x K elements of in_type (MXG_OUT_F32, _BF16 or
  *            _F16), row-major, 16-byte aligned (read only)
- *   rows     >= 1;  K >= 16, K % 16 == 0
+ *   rows     1 .. MXG_MAX_SLOTS (the rows of the experts' products are as many);
+ *            K 16 .. MXG_MAX_DIM, K % 16 == 0
  *   Q        device, rows x K int8, 16-byte aligned (written)
  *   S        device, rows fp32, 4-byte aligned (written)
  * Returns MXG_OK or an error status.  The output is bit-for-bit deterministic.
@@ -346,7 +347,7 @@ int int8gemm_quantize(const void *X, int in_type, int64_t rows, int64_t K,
  *   B        device, N x K int8, 16-byte aligned
  *   scaleB   device, N fp32, 16-byte aligned
  *   C        device, M x N elements of out_type, 16-byte aligned; overwritten
- *   M, N     >= 1;  K >= 16, K % 16 == 0, K <= MXG_INT8_MAX_K
+ *   M, N     1 .. MXG_MAX_DIM;  K >= 16, K % 16 == 0, K <= MXG_INT8_MAX_K
  *   bias, act, out_type  as for mxgemm_run_fused
  * Returns MXG_OK or an error status.  Deterministic: the same sums whatever
  * the kernel.
@@ -356,7 +357,7 @@ int int8gemm_run(const int8_t *A, const float *scaleA, const int8_t *B,
                  const float *bias, int act, int out_type, void *stream);
 
 /* Largest number of experts, of choices per token and of groups of experts,
- * and of rows of the experts' products. */
+ * and of rows of the experts' products and of the quantizer. */
 #define MXG_MAX_EXPERTS 1024
 #define MXG_MAX_CHOICES 64
 #define MXG_MAX_GROUPS 64
@@ -372,7 +373,8 @@ int int8gemm_run(const int8_t *A, const float *scaleA, const int8_t *B,
  * over rows already sorted.
  *
  *   A, scaleA  rowsA rows (1 .. MXG_MAX_SLOTS)
- *   B          E x N x K int8; scaleB E x N fp32; bias E x N fp32 or NULL
+ *   B          E x N x K int8 (N, K as for int8gemm_run); scaleB E x N fp32;
+ *              bias E x N fp32 or NULL
  *   C          rows x N elements of out_type (rows 1 .. MXG_MAX_SLOTS; with
  *              index == NULL at most rowsA)
  *   E          1 .. MXG_MAX_EXPERTS
@@ -415,8 +417,8 @@ int int8gemm_run_grouped(const int8_t *A, const float *scaleA, int64_t rowsA,
  * formed in fp32.
  *
  *   logits      device, T x E elements of in_type, aligned to an element
- *   T           >= 1;  E 1 .. MXG_MAX_EXPERTS;  k 1 .. MXG_MAX_CHOICES, at most
- *               top_groups * (E / groups)
+ *   T           1 .. MXG_MAX_DIM;  E 1 .. MXG_MAX_EXPERTS;  k 1 ..
+ *               MXG_MAX_CHOICES, at most top_groups * (E / groups)
  *   bias        device, E fp32, or NULL
  *   groups      1 .. MXG_MAX_GROUPS, dividing E;  top_groups 1 .. groups
  *   renormalize 0 or 1
@@ -447,7 +449,8 @@ int expert_route_backward(const void *logits, int in_type, int64_t T, int64_t E,
  *   order[p]    = the slot in row p; -1 from row offsets[E] on
  *   position[s] = the row of slot s; -1 where ids[s] is outside 0 .. E-1
  *
- *   ids        device, T x k int32 (read only)
+ *   ids        device, T x k int32 (read only; T 1 .. MXG_MAX_DIM, k 1 ..
+ *              MXG_MAX_CHOICES, E 1 .. MXG_MAX_EXPERTS)
  *   offsets    device, E + 1 int32;  order, position  T * k int32 (written)
  *   workspace  device, expert_plan_workspace(T, k, E) bytes, 4-byte aligned;
  *              NULL when that is 0.  Holds nothing between calls.
@@ -465,7 +468,7 @@ int expert_plan(const int32_t *ids, int64_t T, int k, int64_t E,
  * 0 .. rows-1 adds nothing.
  *
  *   Y         device, rows x N elements of y_type, 16-byte aligned
- *   rows      1 .. MXG_MAX_SLOTS;  N, T >= 1;  k 1 .. MXG_MAX_CHOICES
+ *   rows      1 .. MXG_MAX_SLOTS;  N, T 1 .. MXG_MAX_DIM;  k 1 .. MXG_MAX_CHOICES
  *   position  device, T x k int32;  weights  device, T x k fp32
  *   out       device, T x N elements of out_type, 16-byte aligned (written)
  * Returns MXG_OK or an error status.  Deterministic.

@@ -45,6 +45,12 @@ def test_quantize(lib, change, want):
     assert lib.int8gemm_quantize(p["X"], p["kind"], p["rows"], p["K"], p["Q"], p["S"], None) == want
 
 
+@pytest.mark.parametrize("rows,want", [((1 << 20) + 1, EALIGN), (64 << 20, EALIGN), ((64 << 20) + 1, EINVAL)])
+def test_quantize_rows(lib, rows, want):
+    """As many rows as the experts' products have (a misaligned S ends the call behind that check)."""
+    assert lib.int8gemm_quantize(A, 0, rows, 64, A, A + 2, None) == want
+
+
 @pytest.mark.parametrize("change,want", [
     (dict(A=None), EINVAL), (dict(SA=None), EINVAL), (dict(B=None), EINVAL), (dict(SB=None), EINVAL), (dict(C=None), EINVAL),
     (dict(M=0), EINVAL), (dict(N=-1), EINVAL), (dict(K=40), EINVAL), (dict(K=131072), EINVAL), (dict(act=2), EINVAL),

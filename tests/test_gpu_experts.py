@@ -535,6 +535,21 @@ def test_layer(T, D, H, E, k):
     assert (np.abs(out.double().cpu().numpy() - want) <= tol + ref.half_step(torch.bfloat16) * (np.abs(want) + tol)).all()
 
 
+def test_layer_of_many_tokens():
+    """More than 2^20 slots: every step of the layer takes them, and tokens that
+    repeat the first 64 come out as those."""
+    say("layer of many tokens")
+    b = binding()
+    T, k = 131073, 8
+    ops = _layer_operands(np.random.default_rng(5), 64, 64, 32, 16)
+    x = ops[0].repeat(T // 64 + 1, 1)[:T].contiguous()
+    chosen = b.expert_route(ops[0].float() @ ops[1], k, b.SCORE_SIGMOID)
+    many = tuple(c.repeat(T // 64 + 1, 1)[:T].contiguous() for c in chosen)
+    out = _layer(b, x, *ops[1:], k, ids=many)[-1]
+    few = _layer(b, *ops, k, ids=chosen)[-1]
+    assert torch.equal(out, few.repeat(T // 64 + 1, 1)[:T])
+
+
 def test_layer_with_dropped_slots():
     """A padded batch: the padding rows' logits are all -inf, so they take no expert and come out as zero."""
     say("layer with padding")

@@ -106,6 +106,21 @@ def test_quantize_past_4_gib(rows, K):
     assert np.array_equal(s[some].cpu().numpy(), sr) and np.array_equal(q[some].cpu().numpy(), qr)
 
 
+# each number of lanes per row, in more workgroups than one dimension of the
+# launch holds; the last is as many rows as a call can have
+@pytest.mark.parametrize("rows,K", [((1 << 24) + 21, 16), ((1 << 20) + 3, 4112), ((1 << 20) + 5, 16400),
+                                    ((1 << 22) + 7, 528), ((64 << 20) - 1, 272), (64 << 20, 16)])
+def test_quantize_many_rows(rows, K):
+    say("quantize many rows", rows, K)
+    b = binding()
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device=DEV)
+    some = torch.tensor([0, 1, (1 << 20) - 1, min(1 << 20, rows - 3), rows // 2, rows - 2, rows - 1], device=DEV)
+    x[some] = torch.randn((len(some), K), device=DEV).to(torch.bfloat16)
+    q, s = b.int8gemm_quantize(x)
+    qr, sr = ref.quantize(x[some].float().cpu().numpy())
+    assert np.array_equal(s[some].cpu().numpy(), sr) and np.array_equal(q[some].cpu().numpy(), qr)
+
+
 def test_quantize_near_borders():
     """fp32 values one step to either side of every border between two codes."""
     say("quantize borders")
