@@ -307,11 +307,15 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a, bo
 // experts, p their scores and w = p / sum p where they are renormalized:
 //   softmax, renormalized:  dl_c = scale w_c (dw_c - sum w dw)
 //   sigmoid, renormalized:  dl_c = scale w_c (dw_c - sum w dw) (1 - p_c)
-//   softmax:                dl_e = s_e (scale dw_e [chosen] - scale sum_c dw_c s_c)
+//   softmax:                dl_e = scale s_e (D_e - sum_f s_f D_f), D_e the sum of e's dw
 //   sigmoid:                dl_c = scale dw_c p_c (1 - p_c)
 // and zero elsewhere.  The softmax's own sum cancels in w, so that only the
 // third reads more than the chosen logits.  The few chosen terms are formed in
-// 64 bits, the third's row of scores in 32.
+// 64 bits, the third's row in 32: there all D are taken less that of the expert
+// of the largest logit, which changes nothing (the s add up to one).  Where that
+// expert has nearly all of the sum its D would cancel against the sum's, which
+// 32 bits do not hold; so its own difference is zero and the sum holds
+// what the other experts add.
 template <int IN, int L, int VPL>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteArgs a, const float* __restrict__ d_w,
                                                                           void* __restrict__ d_logits, bool vec) {
@@ -340,7 +344,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
     mc = fmaxf(mc, lc[i]);
   }
   float s[VPL];
-  float m = 0.0f, sum = 1.0f;
+  float sum = 1.0f;
   double dot = 0.0, total = 0.0;
   if (a.renormalize) {
     mc = lanes_max<L>(mc);
@@ -370,7 +374,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
     }
   } else if (softmax) {
     load_logits<IN, VPL>(row, e0, a.E, vec, s);
-    m = -__builtin_inff();
+    float m = -__builtin_inff();
 #pragma unroll
     for (int v = 0; v < VPL; v++) m = fmaxf(m, s[v]);
     m = lanes_max<L>(m);
@@ -383,10 +387,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
     sum = lanes_sum<L>(sum);
 #pragma unroll
     for (int i = 0; i < kRounds<L>; i++) {
-      g[i] = i * L < a.k && id[i] >= 0 ? exp((double)lc[i] - (double)m) / (double)sum * dw[i] : 0.0;
-      dot += g[i];
+      const int j = lane + i * L;
+      g[i] = id[i] >= 0 ? (double)d_w[t * a.k + j] : 0.0;  // the scale comes last
     }
-    dot = lanes_sum<L>(dot);
   } else {
 #pragma unroll
     for (int i = 0; i < kRounds<L>; i++)
@@ -401,22 +404,29 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
     }
   }
   wave_sync();
-  float acc[VPL];
-  const float each = -(float)dot / sum;
-#pragma unroll
-  for (int v = 0; v < VPL; v++) acc[v] = !a.renormalize && softmax && s[v] > 0.0f ? each * s[v] : 0.0f;
-  if (!a.renormalize && softmax) {
-    // a NaN among the logits is one in every term
-#pragma unroll
-    for (int v = 0; v < VPL; v++)
-      if (s[v] != s[v] || sum != sum) acc[v] = s[v] == 0.0f ? 0.0f : sum;
-  }
+  float acc[VPL] = {};
   for (int j = 0; j < a.k; j++) {
     const int at = chosen[tok][j] - e0;
     const float gj = grad[tok][j];
 #pragma unroll
     for (int v = 0; v < VPL; v++)
       if (at == v) acc[v] += gj;
+  }
+  if (!a.renormalize && softmax) {
+    // the D of a largest logit (exp(0) is one; of equal logits any will do)
+    float top = -__builtin_inff(), rest = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; v++) top = s[v] == 1.0f ? fmaxf(top, acc[v]) : top;
+    top = lanes_max<L>(top);
+#pragma unroll
+    for (int v = 0; v < VPL; v++) rest += s[v] > 0.0f ? s[v] * (acc[v] - top) : 0.0f;
+    rest = lanes_sum<L>(rest) / sum;
+    const float f = a.scale / sum;
+    // a NaN among the logits is one in every term (the sum is NaN); experts
+    // without a score have no gradient
+#pragma unroll
+    for (int v = 0; v < VPL; v++)
+      acc[v] = s[v] == 0.0f && acc[v] == 0.0f ? 0.0f : s[v] * f * ((acc[v] - top) - rest);
   }
   if (!live) return;
   auto* out = reinterpret_cast<typename R::type*>(d_logits) + t * a.E;

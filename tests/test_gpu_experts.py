@@ -241,6 +241,82 @@ def test_route_backward_of_one_choice(score, kind):
         assert torch.isnan(got[0, ids[0, 1].long()]) and (got[1:] == 0).all()
 
 
+def _check_dominated(x, ids, dw, renormalize, kind, scale=1.0):
+    """The softmax's gradient where one logit, of expert a, leads: with D_e the
+    sum of expert e's dw (and s the softmax of the chosen alone where weights are
+    renormalized), dl_e = scale s_e sum_f s_f (D_e - D_f) has no terms that
+    cancel.  Allowed are the roundings of _check_backward, of the size of
+    s_e (|D_e - D_a| + sum_f s_f |D_f - D_a|): what is left of dl_a when a has
+    nearly all of the sum, and not s_a |D_a|."""
+    b = binding()
+    t = dev(x).to(TYPES[kind])
+    x = t.float().cpu().numpy().astype(np.float64)
+    out = torch.full(x.shape, 99.0, dtype=TYPES[kind], device=DEV)
+    b.expert_route_backward(t, dev(ids), dev(dw), renormalize=renormalize, scale=scale, d_logits=out)
+    got = out.double().cpu().numpy()
+    for r in range(len(x)):
+        D, p = np.zeros(x.shape[1]), np.exp(x[r] - x[r].max())
+        np.add.at(D, ids[r], dw[r].astype(np.float64) * scale)
+        if renormalize:
+            named = np.zeros(x.shape[1], bool)
+            named[ids[r]] = True
+            p = np.where(named, np.exp(x[r] - x[r][named].max()), 0.0)
+        p = p / p.sum()
+        a = int(np.argmax(p))
+        want = p * ((D[:, None] - D[None, :]) * p).sum(1)
+        mag = p * (np.abs(D - D[a]) + (p * np.abs(D - D[a])).sum())
+        tol = (6 * (x[r].max() - x[r].min()) + 6 * x.shape[1] ** 0.5 + 6 * ids.shape[1] + 24) * U * mag
+        tol = tol + ref.half_step(TYPES[kind]) * (np.abs(want) + tol + torch.finfo(TYPES[kind]).smallest_normal) + 2.0 ** -126 * np.abs(D).max()
+        worst = np.max(np.abs(got[r] - want) / np.maximum(tol, 1e-300))
+        say("  lead %.3g: error / bound %.3g" % (np.sort(x[r])[-1] - np.sort(x[r])[-2], worst))
+        assert worst <= 1.0
+
+
+LEADS = [0.0, 0.5, 4.0, 8.0, 12.0, 14.0, 16.0, 17.0, 18.0, 20.0, 22.0, 25.0, 40.0, 70.0]
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("E", [8, 100, 200, 300, 1000])
+def test_route_backward_of_a_leading_choice(kind, E):
+    """Softmax weights that are not renormalized, one of them close to one."""
+    say("route backward of a leading choice", kind, E)
+    rng = np.random.default_rng(E)
+    x = (0.5 * rng.standard_normal((len(LEADS), E))).astype(np.float32)
+    a = rng.integers(0, E, len(LEADS))
+    others = np.stack([rng.permutation(np.delete(np.arange(E), e)) for e in a])
+    for r, lead in enumerate(LEADS):
+        x[r, a[r]] = np.sort(x[r])[-1] + lead
+    for k in (1, 3, 7):
+        ids = np.concatenate([a[:, None], others[:, :k - 1]], 1).astype(np.int32)
+        for dw in (np.ones(ids.shape), rng.standard_normal(ids.shape)):
+            _check_dominated(x, ids, dw.astype(np.float32), False, kind, 2.5)
+        # a leading expert that is not among the chosen
+        _check_dominated(x, others[:, :k].astype(np.int32), np.ones((len(x), k), np.float32), False, kind)
+    # the same expert twice: whole numbers, whose sums are exact
+    ids = np.concatenate([a[:, None], others[:, :2], a[:, None], others[:, 1:2]], 1).astype(np.int32)
+    _check_dominated(x, ids, np.array([3, -2, 1, 4, 5], np.float32)[None].repeat(len(x), 0), False, kind)
+
+
+@pytest.mark.parametrize("E", [8, 130, 600])
+def test_route_backward_of_rows_with_nan(E):
+    """Weights that are not renormalized: a NaN logit makes its row's gradient NaN
+    wherever there is a score; masked experts have none, nor has a row without any."""
+    say("route backward of rows with NaN", E)
+    b = binding()
+    x = torch.randn((6, E), device=DEV)
+    x[:, ::3] = -float("inf")
+    ids = torch.tensor([[1, 2, 4]] * 6, dtype=torch.int32, device=DEV)
+    ids[4] = -1
+    x[1, 1], x[3, E - 1 if (E - 1) % 3 else E - 2] = float("nan"), float("nan")
+    x[4] = -float("inf")
+    got = b.expert_route_backward(x, ids, torch.randn((6, 3), device=DEV), renormalize=False)
+    assert (got[:, ::3] == 0).all() and (got[4] == 0).all()
+    there = torch.arange(E, device=DEV) % 3 != 0
+    for row in (1, 3):
+        assert torch.isnan(got[row, there]).all()
+    assert (torch.isfinite(got[[0, 2, 5]]) & ((got[[0, 2, 5]] != 0) == there)).all()
+
+
 def test_route_backward_against_differences():
     """The kernel's gradient against differences of the kernel's own weights.
     A step of 2^-6 costs h^2/6 times a third derivative below 2 per unit of dw
