@@ -331,7 +331,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
   const int e0 = lane * VPL;
   const bool softmax = a.score == kScoreSoftmax;
   int id[kRounds<L>];
-  float lc[kRounds<L>], mc = -__builtin_inff();
+  float lc[kRounds<L>], given[kRounds<L>], mc = -__builtin_inff();
   double dw[kRounds<L>], g[kRounds<L>];
 #pragma unroll
   for (int i = 0; i < kRounds<L>; i++) {
@@ -340,7 +340,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
     if (id[i] >= a.E) id[i] = -1;
     const bool mine = id[i] >= 0;
     lc[i] = mine ? R::get(row[id[i]]) : -__builtin_inff();
-    dw[i] = mine ? (double)a.scale * (double)d_w[t * a.k + j] : 0.0;
+    given[i] = mine ? d_w[t * a.k + j] : 0.0f;
+    dw[i] = (double)a.scale * (double)given[i];
     mc = fmaxf(mc, lc[i]);
   }
   float s[VPL];
@@ -386,10 +387,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
     }
     sum = lanes_sum<L>(sum);
 #pragma unroll
-    for (int i = 0; i < kRounds<L>; i++) {
-      const int j = lane + i * L;
-      g[i] = id[i] >= 0 ? (double)d_w[t * a.k + j] : 0.0;  // the scale comes last
-    }
+    for (int i = 0; i < kRounds<L>; i++) g[i] = (double)given[i];  // the scale comes last
   } else {
 #pragma unroll
     for (int i = 0; i < kRounds<L>; i++)
@@ -419,14 +417,14 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
     for (int v = 0; v < VPL; v++) top = s[v] == 1.0f ? fmaxf(top, acc[v]) : top;
     top = lanes_max<L>(top);
 #pragma unroll
-    for (int v = 0; v < VPL; v++) rest += s[v] > 0.0f ? s[v] * (acc[v] - top) : 0.0f;
-    rest = lanes_sum<L>(rest) / sum;
-    const float f = a.scale / sum;
-    // a NaN among the logits is one in every term (the sum is NaN); experts
+    for (int v = 0; v < VPL; v++) rest = fmaf(s[v], acc[v] - top, rest);
+    const float inv = 1.0f / sum, f = a.scale * inv;
+    rest = lanes_sum<L>(rest) * inv;
+    // a NaN among the logits is one in every term (the sum is NaN), but experts
     // without a score have no gradient
 #pragma unroll
     for (int v = 0; v < VPL; v++)
-      acc[v] = s[v] == 0.0f && acc[v] == 0.0f ? 0.0f : s[v] * f * ((acc[v] - top) - rest);
+      acc[v] = s[v] == 0.0f ? 0.0f : s[v] * f * ((acc[v] - top) - rest);
   }
   if (!live) return;
   auto* out = reinterpret_cast<typename R::type*>(d_logits) + t * a.E;
