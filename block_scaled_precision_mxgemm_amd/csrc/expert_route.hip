@@ -311,11 +311,12 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a, bo
 //   sigmoid:                dl_c = scale dw_c p_c (1 - p_c)
 // and zero elsewhere.  The softmax's own sum cancels in w, so that only the
 // third reads more than the chosen logits.  The few chosen terms are formed in
-// 64 bits, the third's row in 32: there all D are taken less that of the expert
-// of the largest logit, which changes nothing (the s add up to one).  Where that
-// expert has nearly all of the sum its D would cancel against the sum's, which
-// 32 bits do not hold; so its own difference is zero and the sum holds
-// what the other experts add.
+// 64 bits, the third's row in 32.  In the sums all dw (D) are taken less that of
+// the largest logit, which changes nothing, as the weights add up to one.  Where
+// that choice has nearly all of the sum its dw would cancel against the sum's,
+// and no type's digits hold the rest for every lead; so its own difference
+// is zero, and the sum holds what the other choices add (a single choice has a
+// constant weight: its gradient is exactly zero).
 template <int IN, int L, int VPL>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteArgs a, const float* __restrict__ d_w,
                                                                           void* __restrict__ d_logits, bool vec) {
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
   const bool softmax = a.score == kScoreSoftmax;
   int id[kRounds<L>];
   float lc[kRounds<L>], given[kRounds<L>], mc = -__builtin_inff();
-  double dw[kRounds<L>], g[kRounds<L>];
+  double g[kRounds<L>];
 #pragma unroll
   for (int i = 0; i < kRounds<L>; i++) {
     const int j = lane + i * L;
@@ -341,7 +342,6 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
     const bool mine = id[i] >= 0;
     lc[i] = mine ? R::get(row[id[i]]) : -__builtin_inff();
     given[i] = mine ? d_w[t * a.k + j] : 0.0f;
-    dw[i] = (double)a.scale * (double)given[i];
     mc = fmaxf(mc, lc[i]);
   }
   float s[VPL];
@@ -349,13 +349,18 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
   double dot = 0.0, total = 0.0;
   if (a.renormalize) {
     mc = lanes_max<L>(mc);
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < kRounds<L>; i++) top = id[i] >= 0 && lc[i] == mc ? fmaxf(top, given[i]) : top;
+    top = lanes_max<L>(top);
     if (!softmax) mc = fminf(mc, 0.0f);
-    double w[kRounds<L>];
+    double w[kRounds<L>], dw[kRounds<L>];
 #pragma unroll
     for (int i = 0; i < kRounds<L>; i++) {
       w[i] = 0.0;
       if (i * L < a.k && id[i] >= 0) {
         w[i] = chosen_score(a.score, (double)lc[i], (double)mc);
+        dw[i] = (double)a.scale * ((double)given[i] - (double)top);
         total += w[i];
         dot += w[i] * dw[i];
       }
@@ -368,8 +373,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
     for (int i = 0; i < kRounds<L>; i++) {
       g[i] = 0.0;
       if (i * L < a.k && id[i] >= 0) {
-        // one choice alone has a constant weight: no rounding is left of it
-        g[i] = w[i] * inv * (dw[i] - (w[i] == total ? dw[i] : dot));
+        g[i] = w[i] * inv * (dw[i] - dot);
         if (!softmax) g[i] *= 1.0 / (1.0 + exp((double)lc[i]));
       }
     }
@@ -391,7 +395,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_backward_kernel(RouteA
   } else {
 #pragma unroll
     for (int i = 0; i < kRounds<L>; i++)
-      g[i] = i * L < a.k && id[i] >= 0 ? dw[i] / ((1.0 + exp(-(double)lc[i])) * (1.0 + exp((double)lc[i]))) : 0.0;
+      g[i] = i * L < a.k && id[i] >= 0
+                 ? (double)a.scale * (double)given[i] / ((1.0 + exp(-(double)lc[i])) * (1.0 + exp((double)lc[i])))
+                 : 0.0;
   }
 #pragma unroll
   for (int i = 0; i < kRounds<L>; i++) {

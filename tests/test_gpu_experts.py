@@ -241,30 +241,31 @@ def test_route_backward_of_one_choice(score, kind):
         assert torch.isnan(got[0, ids[0, 1].long()]) and (got[1:] == 0).all()
 
 
-def _check_dominated(x, ids, dw, renormalize, kind, scale=1.0):
-    """The softmax's gradient where one logit, of expert a, leads: with D_e the
-    sum of expert e's dw (and s the softmax of the chosen alone where weights are
-    renormalized), dl_e = scale s_e sum_f s_f (D_e - D_f) has no terms that
-    cancel.  Allowed are the roundings of _check_backward, of the size of
+def _check_dominated(x, ids, dw, renormalize, kind, scale=1.0, score="softmax"):
+    """The gradient where one logit, of expert a, leads: with D_e the sum of
+    expert e's dw and s the softmax (where weights are renormalized: the chosen
+    scores p over their sum), dl_e = scale s_e sum_f s_f (D_e - D_f) has no terms
+    that cancel (sigmoid: times 1 - p_e).  Allowed are the roundings of _check_backward, of the size of
     s_e (|D_e - D_a| + sum_f s_f |D_f - D_a|): what is left of dl_a when a has
     nearly all of the sum, and not s_a |D_a|."""
     b = binding()
     t = dev(x).to(TYPES[kind])
     x = t.float().cpu().numpy().astype(np.float64)
     out = torch.full(x.shape, 99.0, dtype=TYPES[kind], device=DEV)
-    b.expert_route_backward(t, dev(ids), dev(dw), renormalize=renormalize, scale=scale, d_logits=out)
+    b.expert_route_backward(t, dev(ids), dev(dw), SCORES[score], renormalize=renormalize, scale=scale, d_logits=out)
     got = out.double().cpu().numpy()
     for r in range(len(x)):
-        D, p = np.zeros(x.shape[1]), np.exp(x[r] - x[r].max())
+        D, p = np.zeros(x.shape[1]), np.exp(x[r] - x[r].max()) if score == "softmax" else 1 / (1 + np.exp(-x[r]))
+        slope = 1 / (1 + np.exp(x[r])) if score == "sigmoid" else 1.0
         np.add.at(D, ids[r], dw[r].astype(np.float64) * scale)
         if renormalize:
             named = np.zeros(x.shape[1], bool)
             named[ids[r]] = True
-            p = np.where(named, np.exp(x[r] - x[r][named].max()), 0.0)
+            p = np.where(named, p / p[named].max(), 0.0)
         p = p / p.sum()
         a = int(np.argmax(p))
-        want = p * ((D[:, None] - D[None, :]) * p).sum(1)
-        mag = p * (np.abs(D - D[a]) + (p * np.abs(D - D[a])).sum())
+        want = slope * p * ((D[:, None] - D[None, :]) * p).sum(1)
+        mag = slope * p * (np.abs(D - D[a]) + (p * np.abs(D - D[a])).sum())
         tol = (6 * (x[r].max() - x[r].min()) + 6 * x.shape[1] ** 0.5 + 6 * ids.shape[1] + 24) * U * mag
         tol = tol + ref.half_step(TYPES[kind]) * (np.abs(want) + tol + torch.finfo(TYPES[kind]).smallest_normal) + 2.0 ** -126 * np.abs(D).max()
         worst = np.max(np.abs(got[r] - want) / np.maximum(tol, 1e-300))
@@ -295,6 +296,27 @@ def test_route_backward_of_a_leading_choice(kind, E):
     # the same expert twice: whole numbers, whose sums are exact
     ids = np.concatenate([a[:, None], others[:, :2], a[:, None], others[:, 1:2]], 1).astype(np.int32)
     _check_dominated(x, ids, np.array([3, -2, 1, 4, 5], np.float32)[None].repeat(len(x), 0), False, kind)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [8, 100, 300])
+def test_route_backward_of_a_leading_renormalized_choice(score, E):
+    """Renormalized weights, one of them so close to one that 64 bits do not hold the rest."""
+    say("route backward of a leading renormalized choice", score, E)
+    rng = np.random.default_rng(E)
+    x = (0.5 * rng.standard_normal((len(LEADS), E))).astype(np.float32)
+    ids = np.stack([rng.permutation(E)[:7] for _ in LEADS]).astype(np.int32)
+    for r, lead in enumerate(LEADS):
+        x[r, ids[r, r % 7]] = np.sort(x[r])[-1] + lead
+        if score == "sigmoid":
+            x[r] -= x[r].max()
+    for k in (2, 7):
+        for r in range(len(LEADS)):
+            # the leading choice among the k
+            mine = np.roll(ids[r:r + 1], -(r % 7), 1)[:, :k].copy()
+            mine = np.roll(mine, r % k, 1)
+            for dw in (np.arange(k)[None] + 1.0, rng.standard_normal((1, k))):
+                _check_dominated(x[r:r + 1], mine, dw.astype(np.float32), True, 0, 1.5, score)
 
 
 @pytest.mark.parametrize("E", [8, 130, 600])
