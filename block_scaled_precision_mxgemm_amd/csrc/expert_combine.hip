@@ -98,8 +98,11 @@ __global__ __launch_bounds__(kCThreads) void combine_kernel(CombineArgs a) {
 // workgroup per token, which reads the token's gradient once for all its
 // choices, takes 69 us there and twice as long for few tokens; the gradient
 // comes from the L2 for the second choice on anyway.
+// dY may be Y: a lane reads its columns of a row before it writes them, and no
+// other slot reads that row (dY is not __restrict__, which would let a store go
+// ahead of the load).
 template <int Y, int O, int L, bool NT>
-__global__ __launch_bounds__(kCThreads) void combine_backward_kernel(CombineArgs a, void* __restrict__ dY,
+__global__ __launch_bounds__(kCThreads) void combine_backward_kernel(CombineArgs a, void* dY,
                                                                      float* __restrict__ dW) {
   __shared__ float part[kCThreads / 64];
   const int lane = threadIdx.x % L;

@@ -521,7 +521,7 @@ def expert_combine_backward(d_out, y, position, weights, d_y: torch.Tensor | Non
                             d_weights: torch.Tensor | None = None, stream=None):
     """Gradients (d_y in y's type, d_weights T x k float32) of expert_combine from
     that of its result.  Rows of d_y that no position names are left as they
-    were; without `d_y` they are zero."""
+    were; without `d_y` they are zero.  `d_y` may be y itself."""
     y, position, weights, rows, N, T, k = _combine_args(y, position, weights)
     d_out = _arg(d_out, "d_out", _FLOATS, (T, N), like=y)
     if d_y is None:

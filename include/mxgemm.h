@@ -311,6 +311,9 @@ const char *mxgemm_status_string(int status);
 /*
  * ---- 8-bit integer products with a scale per token and per channel --------
  *
+ * In this section and the ones below, what a call writes overlaps neither what
+ * it reads nor its other outputs, unless said otherwise.
+ *
  * int8gemm_quantize - rows of fp32, bf16 or fp16 -> int8 codes plus one fp32
  * scale per row (activations: a scale per token; weights stored N x K: a scale
  * per output channel).  For every row r:
@@ -485,7 +488,7 @@ int expert_combine(const void *Y, int y_type, int64_t rows, int64_t N,
  * that no position names are left as they were.
  *
  *   dOut  device, T x N elements of out_type;  Y, dY  rows x N of y_type, each
- *         16-byte aligned;  dW  device, T x k fp32 (written)
+ *         16-byte aligned;  dW  device, T x k fp32 (written).  dY may be Y.
  */
 int expert_combine_backward(const void *dOut, int out_type, const void *Y,
                             int y_type, int64_t rows, int64_t N,

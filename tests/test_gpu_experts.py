@@ -557,6 +557,24 @@ def test_combine_backward_of_large_rows(kind, T, k, N):
     assert torch.equal(d_y, want_y)
 
 
+@pytest.mark.parametrize("y_kind,o_kind", [(0, 0), (1, 1), (2, 0), (0, 2)])
+@pytest.mark.parametrize("T,k,N", [(300, 4, 100), (3000, 2, 1041), (64, 8, 7168), (700, 3, 4096), (9000, 4, 3848)])
+def test_combine_backward_in_place(y_kind, o_kind, T, k, N):
+    """dY in Y's memory, for every number of lanes per row and for rows that pass the caches."""
+    say("combine backward in place", y_kind, o_kind, T, k, N)
+    b = binding()
+    rows = T * k + 3
+    pos = torch.randperm(rows, device=DEV)[:T * k].int().view(T, k)
+    pos[T // 2, 1] = -1
+    y = torch.randn((rows, N), device=DEV).to(TYPES[y_kind])
+    d = torch.randn((T, N), device=DEV).to(TYPES[o_kind])
+    w = torch.randn((T, k), device=DEV)
+    want_y, want_w = b.expert_combine_backward(d, y, pos, w, d_y=y.clone())
+    got_y, got_w = b.expert_combine_backward(d, y, pos, w, d_y=y)
+    assert got_y.data_ptr() == y.data_ptr()
+    assert torch.equal(got_y, want_y) and torch.equal(got_w, want_w)
+
+
 def test_combine_most_slots():
     """As many slots as a call can have: 2^20 tokens of 64 choices."""
     say("combine most slots")
