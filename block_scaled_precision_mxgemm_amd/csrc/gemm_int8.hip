@@ -419,6 +419,7 @@ struct RingKernel {
           for (int x = 0; x < 4; x++) v[x] = rounded_product((float)acc[u][h * 4 + j][x], sa[u]);
           *reinterpret_cast<v4f*>(cst + cc * 256 + (((j * 4 + rr) ^ cc) << 4)) = v;
         }
+        wave_sync();
 #pragma unroll FULL ? 4 : 1
         for (int q = 0; q < 4; q++) {
           const int br = q * 4 + rr;
@@ -434,6 +435,7 @@ struct RingKernel {
             store_columns<true>(e, a.N, t.row0 + orow, nc, v);
           }
         }
+        wave_sync();
       }
     }
   }

@@ -171,3 +171,28 @@ def test_decode_kernel_first_wait_counts_the_issued_loads():
             assert set(wks) == {kw}, (name, wks)
         seen += 1
     assert seen >= 80 and split >= 12 and formats == {0, 2, 3, 4, 8, 9}
+
+
+@pytest.mark.skipif(shutil.which(os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")) is None, reason="hipcc not found")
+def test_int8_output_step_keeps_its_lds_order():
+    """The output step of the large int8 tiles writes results to LDS in one lane
+    and reads them in another of the same wave: the compiler is told so by a wave
+    barrier between every run of writes and the reads behind it, and between
+    those and the next writes."""
+    import re
+    from block_scaled_precision_mxgemm_amd import build as B
+    asm = H.compile_to_asm(os.path.join(ROOT, "block_scaled_precision_mxgemm_amd", "csrc", "gemm_int8.hip"), B.FLAGS,
+                           B.HIPCC)
+    seen = 0
+    for m in re.finditer(r"^(_ZN\S*int8_ring_kernel\S*):", asm, re.M):
+        body = asm[m.end():asm.index(".Lfunc_end", m.end())]
+        last = ""
+        runs = 0
+        for op in re.findall(r"^\s*(?:(ds_write_b128|ds_read_b128|s_barrier)\b|(; wave barrier))", body, re.M):
+            op = op[0] or op[1]
+            assert not (last == "ds_write_b128" and op == "ds_read_b128"), m.group(1)
+            runs += last == "; wave barrier" and op == "ds_read_b128"
+            last = op
+        assert runs >= 8, (m.group(1), runs)
+        seen += 1
+    assert seen == 8
