@@ -338,6 +338,18 @@ def _out(t, name: str, dtype, shape, like: torch.Tensor, stream=None) -> torch.T
     return torch.empty(*shape, dtype=dtype, device=like.device)
 
 
+def _on16(t: torch.Tensor, stream) -> torch.Tensor:
+    """The values where the library takes them: at a multiple of 16 bytes.  Others
+    (one expert's row of E x N scales, with N not a multiple of 4) are copied on
+    the call's stream."""
+    if t.data_ptr() & 15 == 0:
+        return t
+    if stream is None:
+        return t.clone()
+    with torch.cuda.stream(stream):
+        return t.clone()
+
+
 _FLOATS = tuple(_DTYPE_IDS)
 
 
@@ -389,9 +401,9 @@ def int8gemm_run(a_q, a_s, b_q, b_s, bias: torch.Tensor | None = None, act: int 
     if b_q.shape[1] != K:
         raise ValueError("inner dimensions disagree: a_q %s, b_q %s" % (tuple(a_q.shape), tuple(b_q.shape)))
     a_s = _arg(a_s, "a_s", (torch.float32,), (M,), like=a_q)
-    b_s = _arg(b_s, "b_s", (torch.float32,), (N,), like=a_q)
+    b_s = _on16(_arg(b_s, "b_s", (torch.float32,), (N,), like=a_q), stream)
     if bias is not None:
-        bias = _arg(bias, "bias", (torch.float32,), (N,), like=a_q)
+        bias = _on16(_arg(bias, "bias", (torch.float32,), (N,), like=a_q), stream)
     out = _out(out, "out", _OUT_DTYPES[out_type], (M, N), a_q, stream)
     _call("int8gemm_run", a_q.device, stream, a_q.data_ptr(), a_s.data_ptr(), b_q.data_ptr(), b_s.data_ptr(),
           out.data_ptr(), M, N, K, _ptr(bias), act, out_type)
@@ -415,14 +427,14 @@ def int8gemm_run_grouped(a_q, a_s, b_q, b_s, offsets, index: torch.Tensor | None
     if b_q.shape[2] != K:
         raise ValueError("inner dimensions disagree: a_q %s, b_q %s" % (tuple(a_q.shape), tuple(b_q.shape)))
     a_s = _arg(a_s, "a_s", (torch.float32,), (rows_a,), like=a_q)
-    b_s = _arg(b_s, "b_s", (torch.float32,), (E, N), like=a_q)
+    b_s = _on16(_arg(b_s, "b_s", (torch.float32,), (E, N), like=a_q), stream)
     offsets = _arg(offsets, "offsets", (torch.int32,), (E + 1,), like=a_q)
     rows = rows_a
     if index is not None:
         index = _arg(index, "index", (torch.int32,), dim=1, like=a_q)
         rows = index.shape[0]
     if bias is not None:
-        bias = _arg(bias, "bias", (torch.float32,), (E, N), like=a_q)
+        bias = _on16(_arg(bias, "bias", (torch.float32,), (E, N), like=a_q), stream)
     out = _out(out, "out", _OUT_DTYPES[out_type], (rows, N), a_q, stream)
     _call("int8gemm_run_grouped", a_q.device, stream, a_q.data_ptr(), a_s.data_ptr(), rows_a, b_q.data_ptr(),
           b_s.data_ptr(), out.data_ptr(), rows, N, K, E, offsets.data_ptr(), _ptr(index), index_div, _ptr(bias), act,

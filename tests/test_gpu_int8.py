@@ -487,6 +487,44 @@ def test_two_calls_at_once():
             assert all(torch.equal(u, v) for u, v in zip(x, y))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 701, 272), (20, 1023, 528), (300, 517, 1040), (700, 4099, 2064), (2050, 4097, 1104)])
+def test_one_expert_of_many(M, N, K):
+    """Weights, scales and bias of one expert, and of a range of experts, as
+    slices that start at any element: the same as copies of them."""
+    say("one expert of many", M, N, K)
+    b = binding()
+    E = 5
+    x, x_s = b.int8gemm_quantize(torch.randn((M, K), device=DEV))
+    w = torch.empty((E, N, K), dtype=torch.int8, device=DEV).random_(-128, 128)
+    w_s, bias = torch.rand((E, N), device=DEV) / K, torch.randn((E, N), device=DEV)
+    side = torch.cuda.Stream()
+    for kind in (0, 1, 2):
+        kw = dict(act=b.ACT_GELU, out_type=kind)
+        for e in (1, 2, 3):
+            want = b.int8gemm_run(x, x_s, w[e], w_s[e].clone(), bias=bias[e].clone(), **kw)
+            assert torch.equal(b.int8gemm_run(x, x_s, w[e], w_s[e], bias=bias[e], **kw), want)
+        torch.cuda.synchronize()
+        got = b.int8gemm_run(x, x_s, w[3], w_s[3], bias=bias[3], stream=side, **kw)
+        side.synchronize()
+        assert torch.equal(got, want)
+        off = torch.tensor([0, M // 3, M // 3, M], dtype=torch.int32, device=DEV)
+        want = b.int8gemm_run_grouped(x, x_s, w[1:4], w_s[1:4].clone(), off, bias=bias[1:4].clone(), **kw)
+        assert torch.equal(b.int8gemm_run_grouped(x, x_s, w[1:4], w_s[1:4], off, bias=bias[1:4], **kw), want)
+    # captured, with other values at each replay
+    out = torch.empty((M, N), device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.int8gemm_run(x, x_s, w[1], w_s[1], bias=bias[1], out=out)
+    for _ in range(3):
+        bias.normal_()
+        want = b.int8gemm_run(x, x_s, w[1], w_s[1], bias=bias[1])
+        torch.cuda.synchronize()
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 # ---- streams, graphs, refusals ----------------------------------------------
 
 
