@@ -160,7 +160,7 @@ const char* mxgemm_status_string(int status) {
     case MXG_EINVAL:
       return "invalid argument (null pointer, dimension out of range, K not a multiple of 32 (int8: 16), or unknown format)";
     case MXG_EALIGN:
-      return "data pointer not 16-byte aligned";
+      return "pointer not aligned (data: 16 bytes; the int8 and expert calls' other arrays: their element)";
     case MXG_EUNSUPPORTED:
       return "device is not gfx950 (MI355X)";
     case MXG_EHIP:

@@ -50,7 +50,7 @@ extern "C" {
 /* Status codes. */
 #define MXG_OK 0
 #define MXG_EINVAL 1         /* null pointer, non-positive or oversized dim, K % 32 != 0, bad enum */
-#define MXG_EALIGN 2         /* a data pointer is not 16-byte aligned */
+#define MXG_EALIGN 2         /* a pointer is not aligned as its call asks (data: 16 bytes) */
 #define MXG_EUNSUPPORTED 3   /* current device is not gfx950 */
 #define MXG_EHIP 4           /* the HIP runtime reported an error at launch */
 

@@ -28,6 +28,12 @@ def test_exports(lib):
         assert name + "(" in open(os.path.join(ROOT, "include", "mxgemm.h")).read()
 
 
+def test_alignment_status_names_both_kinds(lib):
+    """Data is aligned to 16 bytes, but a scale or an index to its element: the text does not call that data."""
+    text = lib.mxgemm_status_string(EALIGN)
+    assert b"16 bytes" in text and b"element" in text
+
+
 def test_package_names():
     import block_scaled_precision_mxgemm_amd as pkg
 
