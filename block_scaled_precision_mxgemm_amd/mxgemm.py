@@ -448,8 +448,10 @@ def expert_route(logits, k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor 
     """The k experts of each token (T x E logits) and their weights: (ids T x k
     int32, weights T x k float32).  bias (E float32) counts for the choice
     alone; with groups > 1 only the top_groups groups with the largest sum of
-    their group_top largest scores are chosen from.  Experts with a logit of
-    -inf are not chosen; missing choices are -1 with weight 0."""
+    their group_top largest scores (of experts that can be chosen) are chosen
+    from.  Experts with a logit of -inf are not chosen; missing choices are -1
+    with weight 0.  No autograd graph is recorded (as in all calls here): the
+    gradient of the weights is expert_route_backward."""
     logits = _arg(logits, "logits", _FLOATS, dim=2)
     T, E = logits.shape
     if bias is not None:
@@ -518,7 +520,8 @@ def _combine_args(y, position, weights):
 def expert_combine(y, position, weights, out_type: int | None = None, out: torch.Tensor | None = None, stream=None):
     """out[t] = sum_j weights[t][j] y[position[t][j]] (y: rows x N; position: T x k
     int32, values outside the rows add nothing; weights: T x k float32), summed
-    in fp32, in out_type (y's type unless given)."""
+    in fp32, in out_type (y's type unless given).  No autograd graph is recorded:
+    the gradient is expert_combine_backward."""
     y, position, weights, rows, N, T, k = _combine_args(y, position, weights)
     out_type = _DTYPE_IDS[y.dtype] if out_type is None else out_type
     if out_type not in _OUT_DTYPES:

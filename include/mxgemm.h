@@ -404,8 +404,9 @@ int int8gemm_run_grouped(const int8_t *A, const float *scaleA, int64_t rowsA,
  * expert_route - choice of k of E experts for each token, and their weights.
  *   s = softmax(logits[t]) or sigmoid(logits[t]);   c = s + bias
  *   groups > 1: the experts form `groups` runs of E / groups; a run's score
- *     is the sum of its group_top (1 or 2) largest c, and the top_groups runs
- *     of largest score stay (ties: the lower run);
+ *     is the sum of its group_top (1 or 2) largest c, of experts that are not
+ *     out (a run with one left: that c alone; with none: it ranks last), and
+ *     the top_groups runs of largest score stay (ties: the lower run);
  *   ids[t]     = the k experts of largest c that stay, in falling order of c
  *                (ties: the lower expert);
  *   weights[t] = scale * s[ids], divided by the sum of s[ids] when renormalize.

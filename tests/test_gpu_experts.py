@@ -100,6 +100,21 @@ def test_route_groups(score, E, groups, top_groups, k, group_top, with_bias):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups_with_one_expert_left(score):
+    """The score of a group whose other experts are all out is that of the one
+    left, against groups with two and with none."""
+    say("route groups with one expert left", score)
+    x = np.full((4, 16), -np.inf, np.float32)
+    x[0, [1, 5, 6, 9]] = [3.0, 1.0, 0.5, 0.0]        # 3 against 1 + 0.5, by its score: s(3) or the pair
+    x[1, [0, 4, 5, 8, 9, 12]] = [0.2, 0.1, 0.0, 0.1, 0.1, 9.0]
+    x[2, [7, 15]] = [-4.0, -5.0]
+    x[3, :4] = 0.0
+    for top_groups in (1, 2, 3):
+        _check_route(x, 3, score, groups=4, top_groups=top_groups, group_top=2)
+        _check_route(x, 3, score, groups=4, top_groups=top_groups, group_top=2, bias=np.linspace(0, 0.3, 16).astype(np.float32))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_route_extreme_logits(score, renormalize):
     say("route extremes", score, renormalize)
