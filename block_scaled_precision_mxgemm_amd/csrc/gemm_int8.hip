@@ -8,6 +8,7 @@
 // bias of expert e, and row p of C takes row index[p] / index_div of A (row p
 // without an index).  The workgroups find their tile from the offsets on the
 // device: no host copy of the row counts, and no work but a scan of them.
+#include "int8_choice.h"
 #include "mxg_int8.h"
 #include "mxg_internal.h"
 
@@ -625,33 +626,8 @@ hipError_t launch_few(const I8Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// ---- choice -----------------------------------------------------------------
-//
-// Each variant's time is estimated as rounds x (slices x us + extra): tiles over
-// the workgroups that run at once, us per slice of 128 k with the chip full
-// (seven tenths of it where a variant that fits twice on a CU has it for
-// itself), and what a tile costs besides; and as no less than the weights'
-// time from memory.  The smallest estimate is taken, the first of equal ones.
-// The constants are measured; what the choice is worth, in us (bf16 output,
-// weights from memory; dense M x N x K, or tokens x choices of experts of N x K):
-//                                  16x16  16x32  32x32  32x64  deep  128x128 256x128 256x256
-//   16 x 4096 x 4096                 6.3    6.8    8.0    11.6  20     20      25      42
-//   16 x 28672 x 8192                46     44     49     46.7  52     60      66      90
-//   32 x 28672 x 8192                73     61     54     46.7  53     60      66      90
-//   64 x 4096 x 14336                34     26     21     31    54     80      83      137
-//   256 x 4096 x 4096                39     27     26     16.6  17     21      25      42
-//   1024 x 4096 x 4096               -      -      -      59    20.5   22.8    27      43
-//   512 x 14336 x 4096               -      -      -      -     -      41      33      49
-//   8192 x 14336 x 4096              -      -      -      1300  636    490     427     375
-//   16 x 4 of 64 of 2048 x 4096      93     68     87     77    98     98      105     118
-//   256 x 4 of 64 of 2048 x 4096     186    132    152    117   134    141     157     161
-//   1024 x 8 of 64 of 2048 x 4096    -      -      -      297   175    165     202     220
-//   2048 x 4 of 16 of 4096 x 2048    -      -      -      282   136    118     118     112
-struct Variant {
-  int bm, bn, per_cu;
-  double us, extra;
-  hipError_t (*launch)(const I8Args&, hipStream_t);
-};
+// ---- launch -----------------------------------------------------------------
+
 using Tile16x16 = I8Few<1, 1, 4, 5>;
 using Tile16x32 = I8Few<1, 2, 4, 3>;
 using Tile32x32 = I8Few<2, 2, 4, 4>;
@@ -663,34 +639,14 @@ using Tile128x128Deep = I8Cfg<128, 128, 4, 2, 3>;
 using Tile256x128 = I8Cfg<256, 128, 4, 2>;
 using Tile256x256 = I8Cfg<256, 256, 4, 2>;
 
-const Variant kVariants[] = {
-    {16, 16, 2, 0.18, 1.8, launch_few<Tile16x16>},
-    {16, 32, 2, 0.22, 1.8, launch_few<Tile16x32>},
-    {32, 32, 1, 0.19, 2.4, launch_few<Tile32x32>},
-    {32, 64, 2, 0.52, 1.5, launch_few<Tile32x64>},
-    {128, 128, 1, 0.55, 3.0, launch_ring<Tile128x128Deep>},
-    {128, 128, 2, 1.00, 2.0, launch_ring<Tile128x128>},
-    {256, 128, 1, 0.87, 3.0, launch_ring<Tile256x128>},
-    {256, 256, 1, 1.45, 8.0, launch_ring<Tile256x256>}};
-
-constexpr int kCus = 256;
-constexpr double kBytesPerUs = 5.2e6;
-
-double estimate(const Variant& v, const I8Args& a) {
-  // by expert the rows' split is not known here: half a tile more for each
-  // expert that can have rows
-  const double experts = a.offsets == nullptr ? 0.0 : (double)(a.E < a.M ? a.E : a.M);
-  const double tiles_m =
-      a.offsets == nullptr ? (double)((a.M + v.bm - 1) / v.bm) : (double)a.M / v.bm + 0.5 * experts;
-  const double tiles = tiles_m * (double)((a.N + v.bn - 1) / v.bn);
-  const double full = tiles / (kCus * v.per_cu);
-  const double rounds = full > 4.0 ? full + 0.5 : __builtin_ceil(full);
-  const double us = v.per_cu == 2 && tiles <= kCus ? 0.7 * v.us : v.us;
-  const double t = rounds * ((a.K + 127) / 128 * us + v.extra);
-  // experts that get rows when m rows fall on E of them evenly: E m / (m + 0.6 E)
-  const double used = a.offsets == nullptr ? 1.0 : (double)a.E * a.M / (a.M + 0.6 * a.E);
-  const double floor = used * a.N * a.K / kBytesPerUs;
-  return t > floor ? t : floor;
+// variant V of kI8Variants
+template <int V, class T>
+hipError_t launch_variant(const I8Args& a, hipStream_t stream) {
+  static_assert(T::BM == kI8Variants[V].bm && T::BN == kI8Variants[V].bn, "the variant's tile");
+  if constexpr (V < 4)
+    return launch_few<T>(a, stream);
+  else
+    return launch_ring<T>(a, stream);
 }
 
 hipError_t launch_gathered_far(const I8Args& a, hipStream_t stream) {
@@ -710,16 +666,24 @@ hipError_t launch_int8(const I8Args& args, hipStream_t stream) {
   set_division(a);
   // gathered rows are addressed by 32-bit offsets from A's start
   if (a.index != nullptr && a.rows_a * a.K >= ((int64_t)1 << 32)) return launch_gathered_far(a, stream);
-  const Variant* best = nullptr;
-  double least = 0.0;
-  for (const Variant& v : kVariants) {
-    const double t = estimate(v, a);
-    if (best == nullptr || t < least) {
-      best = &v;
-      least = t;
-    }
+  switch (i8_choice(a.M, a.N, a.K, a.offsets == nullptr ? 0 : a.E)) {
+    case 0:
+      return launch_variant<0, Tile16x16>(a, stream);
+    case 1:
+      return launch_variant<1, Tile16x32>(a, stream);
+    case 2:
+      return launch_variant<2, Tile32x32>(a, stream);
+    case 3:
+      return launch_variant<3, Tile32x64>(a, stream);
+    case 4:
+      return launch_variant<4, Tile128x128Deep>(a, stream);
+    case 5:
+      return launch_variant<5, Tile128x128>(a, stream);
+    case 6:
+      return launch_variant<6, Tile256x128>(a, stream);
+    default:
+      return launch_variant<7, Tile256x256>(a, stream);
   }
-  return best->launch(a, stream);
 }
 
 }  // namespace mxg

@@ -150,6 +150,21 @@ def test_binding_refuses_host_tensors():
             call()
 
 
+def test_large_tile_cases_take_their_tiles():
+    """The GPU tests of the large tiles are at sizes that take them."""
+    import test_gpu_int8_large as large
+
+    chosen = large.load_choice()
+    for tile, M, N, K in large.DENSE:
+        assert chosen(M, N, K) == tile
+    for tile, E, tokens, div, N, K in large.EXPERTS:
+        assert chosen(tokens * div, N, K, E) == tile
+    for tile, M, N in large.LARGEST:
+        assert chosen(M, N, 131056) == tile
+    for tile, rows, N, K in large.OFFSETS:
+        assert chosen(rows, N, K, 3) == tile
+
+
 # ---- the 64-bit forms that the GPU tests compare with -----------------------
 
 
