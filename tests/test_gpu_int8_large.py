@@ -183,6 +183,30 @@ def test_largest_sums(tile, M, N, x, y):
     assert (out == float(np.float32(x * y * K))).all()
 
 
+@pytest.mark.parametrize("tile,M,N,K", DENSE)
+def test_every_tile_gives_the_same(tile, M, N, K):
+    """The sums are exact, so whatever tiles two calls take, they agree bit for
+    bit: the product at once, in few-row pieces, as one expert's, and over
+    experts some of which have no rows."""
+    say("every tile the same", tile, M, N, K)
+    b = binding()
+    g = torch.Generator(device=DEV).manual_seed(N)
+    a, w = _codes(g, M, K), _codes(g, N, K)
+    a_s, w_s, bias = _scales(g, M, by=128), _scales(g, N, by=64 * math.sqrt(K)), torch.randn(N, device=DEV, generator=g)
+    E = 6
+    many = [t.expand(E, *t.shape).contiguous() for t in (w, w_s, bias)]
+    off = torch.tensor([0, 0, M // 3, M // 3, M - 1, M - 1, M], dtype=torch.int32, device=DEV)
+    for kind in (0, 1, 2):
+        kw = dict(act=b.ACT_GELU, out_type=kind)
+        want = b.int8gemm_run(a, a_s, w, w_s, bias=bias, **kw)
+        rows = slice(M // 2, M // 2 + 23)
+        few = b.int8gemm_run(a[rows], a_s[rows], w, w_s, bias=bias, **kw)
+        assert torch.equal(few, want[rows])
+        one = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+        assert torch.equal(b.int8gemm_run_grouped(a, a_s, w[None], w_s[None], one, bias=bias[None], **kw), want)
+        assert torch.equal(b.int8gemm_run_grouped(a, a_s, many[0], many[1], off, bias=many[2], **kw), want)
+
+
 @pytest.mark.parametrize("tile,rows,N,K", OFFSETS)
 @pytest.mark.parametrize("shape", ["front and behind", "falling", "outside", "all in the last"])
 def test_offsets(tile, rows, N, K, shape):
