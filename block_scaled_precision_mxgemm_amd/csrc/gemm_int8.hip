@@ -433,6 +433,13 @@ struct RingKernel {
 #pragma unroll
               for (int x = 0; x < 4; x++) v[x] = gelu(v[x]);
             }
+            if constexpr (OUT == kOutF16) {
+              // fp32 values first, as where the type is not known: else the
+              // compiler makes one instruction of GELU's last product and the
+              // conversion (v_fma_mixlo_f16, one rounding instead of two)
+#pragma unroll
+              for (int x = 0; x < 4; x++) asm("" : "+v"(v[x]));
+            }
             store_columns<true>(e, a.N, t.row0 + orow, nc, v);
           }
         }

@@ -157,15 +157,6 @@ __device__ __forceinline__ float rounded_product(float x, float y) {
   return x * y;
 }
 
-// fp32 -> fp16 bits of a value that is an fp32 value first: left to itself the
-// compiler makes one instruction of the conversion and the product before it
-// (v_fma_mixlo_f16, one rounding instead of two) in some kernels and not in
-// others.
-__device__ __forceinline__ uint32_t f16_bits_of_f32(float f) {
-  asm("" : "+v"(f));
-  return f16_bits(f);
-}
-
 // Vectors at any element's address: rows of C, of the scales and of the bias
 // start there when N is not a multiple of 4 (global memory takes such accesses
 // in one instruction).
@@ -200,7 +191,7 @@ __device__ __forceinline__ void store_columns(Epi e, int64_t N, int64_t m, int n
   }
   uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; i++) h[i] = e.out == kOutBF16 ? bf16_bits(v[i]) : f16_bits_of_f32(v[i]);
+  for (int i = 0; i < 4; i++) h[i] = e.out == kOutBF16 ? bf16_bits(v[i]) : f16_bits(v[i]);
   uint16_t* p = reinterpret_cast<uint16_t*>(e.C) + m * N + n;
   if (n + 3 < N) {
     const v2i_any w = {(int)(h[0] | (h[1] << 16)), (int)(h[2] | (h[3] << 16))};

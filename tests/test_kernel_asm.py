@@ -196,3 +196,14 @@ def test_int8_output_step_keeps_its_lds_order():
         assert runs >= 8, (m.group(1), runs)
         seen += 1
     assert seen == 8
+
+
+@pytest.mark.skipif(shutil.which(os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")) is None, reason="hipcc not found")
+def test_int8_results_are_rounded_to_fp32_first():
+    """No int8 product kernel joins the last product of GELU with the conversion to
+    fp16 (one rounding instead of two): all of them give the same bits."""
+    from block_scaled_precision_mxgemm_amd import build as B
+    asm = H.compile_to_asm(os.path.join(ROOT, "block_scaled_precision_mxgemm_amd", "csrc", "gemm_int8.hip"), B.FLAGS,
+                           B.HIPCC)
+    assert "int8_ring_kernel" in asm and "v_cvt_f16_f32" in asm
+    assert "v_fma_mix" not in asm and "v_mad_mix" not in asm
