@@ -93,7 +93,7 @@ __global__ __launch_bounds__(kCThreads) void combine_kernel(CombineArgs a) {
 }
 
 // L lanes per slot, two pieces of a row at a time.  2047 tokens of 8 choices
-// and 4096 columns (bf16), a wave for each slot: 64 us from memory, 4.4 TB/s of
+// and 4096 columns (bf16), a wave for each slot: 64 us from memory, 4.5 TB/s of
 // reads and writes in equal parts, of which a large copy reaches 5.0.  A
 // workgroup per token, which reads the token's gradient once for all its
 // choices, takes 69 us there and twice as long for few tokens; the gradient

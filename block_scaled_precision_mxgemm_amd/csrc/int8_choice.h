@@ -12,20 +12,22 @@ namespace mxg {
 // itself), and what a tile costs besides; and as no less than the weights'
 // time from memory.  The smallest estimate is taken, the first of equal ones.
 // The constants are measured; what the choice is worth, in us (bf16 output,
-// weights from memory; dense M x N x K, or tokens x choices of experts of N x K):
-//                                  16x16  16x32  32x32  32x64  deep  128x128 256x128 256x256
-//   16 x 4096 x 4096                 6.3    6.8    8.0    11.6  20     20      25      42
-//   16 x 28672 x 8192                46     44     49     46.7  52     60      66      90
-//   32 x 28672 x 8192                73     61     54     46.7  53     60      66      90
-//   64 x 4096 x 14336                34     26     21     31    54     80      83      137
-//   256 x 4096 x 4096                39     27     26     16.6  17     21      25      42
-//   1024 x 4096 x 4096               -      -      -      59    20.5   22.8    27      43
-//   512 x 14336 x 4096               -      -      -      -     -      41      33      49
-//   8192 x 14336 x 4096              -      -      -      1300  636    490     427     375
-//   16 x 4 of 64 of 2048 x 4096      93     68     87     77    98     98      105     118
-//   256 x 4 of 64 of 2048 x 4096     186    132    152    117   134    141     157     161
-//   1024 x 8 of 64 of 2048 x 4096    -      -      -      297   175    165     202     220
-//   2048 x 4 of 16 of 4096 x 2048    -      -      -      282   136    118     118     112
+// operands from memory, calls of one captured graph; dense M x N x K, or tokens
+// x choices of experts of N x K; * what is taken, at most 7 % behind the fastest).
+// The time of A's and C's bytes is left out.
+//                                  16x16  16x32  32x32  32x64   deep 128x128 256x128 256x256
+//   16 x 4096 x 4096                 7.1*   8.3    8.5   11.6   18.7    28.1    28.8    43.7
+//   16 x 28672 x 8192               49.5   46.3*  53.8   46.1   53.5    59.8    64.7    88.2
+//   32 x 28672 x 8192               71.8   59.7   55.4   46.8*  51.9    59.5    63.4    91.1
+//   64 x 4096 x 14336               34.9   27.7   22.9*  31.6   58.4    87.3    88.7     142
+//   256 x 4096 x 4096               41.8   29.3   27.2   17.4*  22.9    28.9    32.6    49.2
+//   1024 x 4096 x 4096               155    105   98.8   54.2   23.9*   29.4    32.2    47.9
+//   512 x 14336 x 4096               267    183    171   92.3   46.5    43.0    35.1*   50.9
+//   8192 x 14336 x 4096             3824   2528   2588   1301    576     520     454     398*
+//   16 x 4 of 64 of 2048 x 4096     92.9   73.2*  93.5   82.3   96.8     104     115     124
+//   256 x 4 of 64 of 2048 x 4096     188    134    150    114*   139     148     153     148
+//   1024 x 8 of 64 of 2048 x 4096    864    546    544    281    182     168*    164     158
+//   2048 x 4 of 16 of 4096 x 2048   1166    651    665    282    139     118*    124     112
 struct I8Variant {
   int bm, bn, per_cu;
   double us, extra;
