@@ -165,6 +165,18 @@ def test_large_tile_cases_take_their_tiles():
         assert chosen(rows, N, K, 3) == tile
 
 
+def test_many_tiles_cases_take_every_tile():
+    """The GPU tests of more tiles than run at once reach all of them."""
+    import test_gpu_int8 as gpu
+    import test_gpu_int8_large as large
+
+    chosen = large.load_choice()
+    cases = [m.args[1] for f in (gpu.test_product_many_tiles, gpu.test_experts_many_tiles) for m in f.pytestmark
+             if m.name == "parametrize"]
+    taken = {chosen(*c) for c in cases[0]} | {chosen(c[1] * c[2], c[3], c[4], c[0]) for c in cases[1]}
+    assert taken == set(large.TILES)
+
+
 # ---- the 64-bit forms that the GPU tests compare with -----------------------
 
 
