@@ -5,7 +5,9 @@ The computation is C = (A * 2^sA)(B * 2^sB)^T over operands stored as FP8
 with one UE8M0 scale per 32 contiguous K elements, fp32 output; a dense fp16
 GEMM is the comparison path.  Beside it are int8 products with one scale per
 token and output channel, dense and by expert, and the router, plan and
-combination of a layer of experts.  All arithmetic runs in the
+combination of a layer of experts; E4M3 products with one scale per block of 128,
+dense and by expert, with their weights' gradients; and the root-mean-square norm
+with an 8-bit output.  All arithmetic runs in the
 HIP kernels of ``libmxgemm.so`` behind a C ABI (``include/mxgemm.h``); the
 Python binding in :mod:`block_scaled_precision_mxgemm_amd.mxgemm` only
 marshals torch device tensors to it.
@@ -30,6 +32,13 @@ _BINDING_NAMES = (
     "expert_plan",
     "expert_combine",
     "expert_combine_backward",
+    "fp8gemm_quantize",
+    "fp8gemm_run",
+    "fp8gemm_run_grouped",
+    "fp8gemm_weight_grad",
+    "fp8gemm_weight_grad_grouped",
+    "rmsnorm_quantize",
+    "rmsnorm_backward",
     "mxgemm_mfma_ceiling",
     "mxgemm_device_supported",
     "MXGemmError",
@@ -59,6 +68,11 @@ _BINDING_NAMES = (
     "SCORE_SOFTMAX",
     "SCORE_SIGMOID",
     "INT8_MAX_K",
+    "QUANT_NONE",
+    "QUANT_INT8",
+    "QUANT_FP8",
+    "QUANT_FP8_POW2",
+    "QUANT_MXFP8",
     "library_path",
 )
 

@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include "../../include/mxgemm.h"
+#include "mxg_fp8.h"
 #include "mxg_int8.h"
 #include "mxg_internal.h"
 
@@ -139,6 +140,44 @@ int validate_combine(const mxg::CombineArgs& a, int y_type, int out_type) {
   return MXG_OK;
 }
 
+int blocks_of(int64_t d) { return (int)((d + 127) / 128); }
+
+// sizes and operands of the E4M3 products and of their weights' gradients
+bool fp8_dims_ok(int64_t N, int64_t K) { return dim_ok(N) && dim_ok(K) && K % 16 == 0; }
+bool experts_ok(const int32_t* offsets, const int32_t* index, int index_div, int64_t rows, int64_t rowsA, int64_t E) {
+  if (!offsets || rows < 1 || rows > MXG_MAX_SLOTS || rowsA < 1 || rowsA > MXG_MAX_SLOTS) return false;
+  return E >= 1 && E <= MXG_MAX_EXPERTS && index_div >= 1 && (index != nullptr || rowsA >= rows);
+}
+
+int run_fp8(const mxg::F8Args& a, const float* bias, int act, int out_type, hipStream_t st) {
+  if (!a.A || !a.SA || !a.B || !a.SB || !a.e.C) return MXG_EINVAL;
+  if (!aligned16(a.A) || !aligned16(a.B) || !aligned16(a.e.C)) return MXG_EALIGN;
+  if (!aligned4(a.SA) || !aligned4(a.SB) || !aligned4(a.offsets) || !aligned4(a.index)) return MXG_EALIGN;
+  int s = validate_epi(bias, act, out_type);
+  if (s != MXG_OK) return s;
+  s = check_device();
+  if (s != MXG_OK) return s;
+  return to_status(mxg::launch_fp8(a, st));
+}
+
+int run_fp8_grad(const mxg::F8GradArgs& a, int c_type, hipStream_t st) {
+  if (!a.dY || !a.A || !a.SA || !a.dW || !type_ok(c_type) || !type_ok(a.out_type)) return MXG_EINVAL;
+  if (mxg::fp8_weight_grad_bytes(a.M, a.N, a.K, a.E) > 0 && !a.workspace) return MXG_EINVAL;
+  if (!aligned16(a.dY) || !aligned16(a.A) || !aligned16(a.dW) || !aligned16(a.workspace)) return MXG_EALIGN;
+  if (!aligned4(a.SA) || !aligned4(a.offsets) || !aligned4(a.index)) return MXG_EALIGN;
+  const int s = check_device();
+  if (s != MXG_OK) return s;
+  return to_status(mxg::launch_fp8_weight_grad(a, c_type, st));
+}
+
+bool norm_dims_ok(int64_t rows, int64_t K) {
+  return rows >= 1 && rows <= MXG_MAX_SLOTS && dim_ok(K) && K % 16 == 0;
+}
+
+static_assert(MXG_QUANT_NONE == mxg::kQuantNone && MXG_QUANT_INT8 == mxg::kQuantInt8 &&
+                  MXG_QUANT_FP8 == mxg::kQuantFp8 && MXG_QUANT_FP8_POW2 == mxg::kQuantFp8Pow2 &&
+                  MXG_QUANT_MXFP8 == mxg::kQuantMx,
+              "code ids of the norm");
 static_assert(MXG_OUT_F32 == mxg::kOutF32 && MXG_OUT_BF16 == mxg::kOutBF16 && MXG_OUT_F16 == mxg::kOutF16,
               "output type ids");
 static_assert(MXG_SCORE_SOFTMAX == mxg::kScoreSoftmax && MXG_SCORE_SIGMOID == mxg::kScoreSigmoid, "score ids");
@@ -158,9 +197,9 @@ const char* mxgemm_status_string(int status) {
     case MXG_OK:
       return "ok";
     case MXG_EINVAL:
-      return "invalid argument (null pointer, dimension out of range, K not a multiple of 32 (int8: 16), or unknown format)";
+      return "invalid argument (null pointer, dimension out of range, K not a multiple of 32 (int8, fp8 and norm: 16), or unknown format)";
     case MXG_EALIGN:
-      return "pointer not aligned (data: 16 bytes; the int8 and expert calls' other arrays: their element)";
+      return "pointer not aligned (data: 16 bytes; the int8, fp8, norm and expert calls' other arrays: their element)";
     case MXG_EUNSUPPORTED:
       return "device is not gfx950 (MI355X)";
     case MXG_EHIP:
@@ -344,6 +383,93 @@ int expert_combine_backward(const void* dOut, int out_type, const void* Y, int y
   const int d = check_device();
   if (d != MXG_OK) return d;
   return to_status(mxg::launch_combine_backward(a, y_type, out_type, dY, dW, (hipStream_t)stream));
+}
+
+int fp8gemm_quantize(const void* X, int in_type, int64_t E, int64_t rows, int64_t K, int block_rows, int pow2, uint8_t* Q,
+                     float* S, void* stream) {
+  if (!X || !Q || !S || !type_ok(in_type) || (pow2 != 0 && pow2 != 1)) return MXG_EINVAL;
+  if (E < 1 || E > MXG_MAX_EXPERTS || !dim_ok(K) || (K % 16) != 0) return MXG_EINVAL;
+  if (block_rows == 1) {
+    if (rows < 1 || rows > MXG_MAX_SLOTS || E * rows > MXG_MAX_SLOTS) return MXG_EINVAL;
+  } else if (block_rows != 128 || !dim_ok(rows)) {
+    return MXG_EINVAL;
+  }
+  if (!aligned16(X) || !aligned16(Q) || !aligned4(S)) return MXG_EALIGN;
+  const int d = check_device();
+  if (d != MXG_OK) return d;
+  return to_status(
+      mxg::launch_quantize_fp8(X, in_type, E, rows, K, block_rows, pow2 != 0, Q, S, (hipStream_t)stream));
+}
+
+int fp8gemm_run(const uint8_t* A, const float* scaleA, const uint8_t* B, const float* scaleB, void* C, int64_t M, int64_t N,
+                int64_t K, const float* bias, int act, int out_type, void* stream) {
+  if (!dim_ok(M) || !fp8_dims_ok(N, K)) return MXG_EINVAL;
+  return run_fp8(mxg::F8Args{A, scaleA, M, B, scaleB, mxg::Epi{C, bias, out_type, act}, M, (int)N, (int)K, 1, nullptr,
+                             nullptr, 1, 0, 0, blocks_of(K), blocks_of(N)},
+                 bias, act, out_type, (hipStream_t)stream);
+}
+
+int fp8gemm_run_grouped(const uint8_t* A, const float* scaleA, int64_t rowsA, const uint8_t* B, const float* scaleB,
+                        void* C, int64_t rows, int64_t N, int64_t K, int64_t E, const int32_t* offsets,
+                        const int32_t* index, int index_div, const float* bias, int act, int out_type, void* stream) {
+  if (!fp8_dims_ok(N, K) || !experts_ok(offsets, index, index_div, rows, rowsA, E)) return MXG_EINVAL;
+  return run_fp8(mxg::F8Args{A, scaleA, rowsA, B, scaleB, mxg::Epi{C, bias, out_type, act}, rows, (int)N, (int)K, (int)E,
+                             offsets, index, index_div, 0, 0, blocks_of(K), blocks_of(N)},
+                 bias, act, out_type, (hipStream_t)stream);
+}
+
+int64_t fp8gemm_weight_grad_workspace(int64_t M, int64_t N, int64_t K, int64_t E) {
+  if (M < 1 || M > MXG_MAX_SLOTS || !fp8_dims_ok(N, K) || E < 1 || E > MXG_MAX_EXPERTS) return -1;
+  return mxg::fp8_weight_grad_bytes(M, N, K, E);
+}
+
+int fp8gemm_weight_grad(const void* dC, int c_type, int64_t M, int64_t N, const uint8_t* A, const float* scaleA, int64_t K,
+                        void* dW, int out_type, void* workspace, void* stream) {
+  if (M < 1 || M > MXG_MAX_SLOTS || !fp8_dims_ok(N, K)) return MXG_EINVAL;
+  return run_fp8_grad(mxg::F8GradArgs{dC, M, A, scaleA, M, (int)N, (int)K, blocks_of(K), 1, nullptr, nullptr, 1, 0, 0, dW,
+                                      out_type, workspace},
+                      c_type, (hipStream_t)stream);
+}
+
+int fp8gemm_weight_grad_grouped(const void* dC, int c_type, int64_t rows, int64_t N, const uint8_t* A,
+                                const float* scaleA, int64_t rowsA, int64_t K, int64_t E, const int32_t* offsets,
+                                const int32_t* index, int index_div, void* dW, int out_type, void* workspace,
+                                void* stream) {
+  if (!fp8_dims_ok(N, K) || !experts_ok(offsets, index, index_div, rows, rowsA, E)) return MXG_EINVAL;
+  return run_fp8_grad(mxg::F8GradArgs{dC, rows, A, scaleA, rowsA, (int)N, (int)K, blocks_of(K), (int)E, offsets, index,
+                                      index_div, 0, 0, dW, out_type, workspace},
+                      c_type, (hipStream_t)stream);
+}
+
+int rmsnorm_quantize(const void* X, const void* R, int type, const void* W, int w_type, int64_t rows, int64_t K, float eps,
+                     void* H, void* Y, int quant, uint8_t* Q, void* S, float* rstd, void* stream) {
+  if (!X || !W || !type_ok(type) || !type_ok(w_type) || !norm_dims_ok(rows, K)) return MXG_EINVAL;
+  if (!(eps >= 0.0f) || eps > 3.0e38f || (R == nullptr) != (H == nullptr)) return MXG_EINVAL;
+  if (quant < MXG_QUANT_NONE || quant > MXG_QUANT_MXFP8 || (quant == MXG_QUANT_MXFP8 && K % 32 != 0)) return MXG_EINVAL;
+  if (quant == MXG_QUANT_NONE ? (!Y || Q || S) : (!Q || !S)) return MXG_EINVAL;
+  if (!aligned16(X) || !aligned16(R) || !aligned16(W) || !aligned16(H) || !aligned16(Y) || !aligned16(Q)) return MXG_EALIGN;
+  if (!aligned4(rstd) || (quant != MXG_QUANT_MXFP8 && !aligned4(S))) return MXG_EALIGN;
+  const int d = check_device();
+  if (d != MXG_OK) return d;
+  return to_status(mxg::launch_rmsnorm(mxg::NormArgs{X, R, W, w_type, rows, (int)K, eps, H, Y, quant, Q, S, rstd}, type,
+                                       (hipStream_t)stream));
+}
+
+int64_t rmsnorm_backward_workspace(int64_t rows, int64_t K) {
+  return norm_dims_ok(rows, K) ? mxg::rmsnorm_backward_bytes(rows, K) : -1;
+}
+
+int rmsnorm_backward(const void* dY, const void* H, const void* dH, int type, const void* W, int w_type, const float* rstd,
+                     int64_t rows, int64_t K, void* dX, float* dW, void* workspace, void* stream) {
+  if (!dY || !H || !W || !rstd || !dX || !dW || !workspace) return MXG_EINVAL;
+  if (!type_ok(type) || !type_ok(w_type) || !norm_dims_ok(rows, K)) return MXG_EINVAL;
+  if (!aligned16(dY) || !aligned16(H) || !aligned16(dH) || !aligned16(W) || !aligned16(dX) || !aligned16(dW) ||
+      !aligned16(workspace) || !aligned4(rstd))
+    return MXG_EALIGN;
+  const int d = check_device();
+  if (d != MXG_OK) return d;
+  return to_status(mxg::launch_rmsnorm_backward(
+      mxg::NormGradArgs{dY, H, dH, W, w_type, rstd, rows, (int)K, dX, dW, workspace}, type, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -469,7 +469,7 @@ __global__ __launch_bounds__(T::NW * 64) __attribute__((amdgpu_waves_per_eu(2)))
 template <class T>
 hipError_t launch_ring(const I8Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
-  const int64_t tiles = tiles_n * i8_tiles_m(a, T::BM);
+  const int64_t tiles = tiles_n * expert_tiles_m(a, T::BM);
   if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
   int dev = 0, cus = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -623,7 +623,7 @@ __global__ __launch_bounds__(T::NW * 64) void int8_few_kernel(I8Args a, int tile
 template <class T>
 hipError_t launch_few(const I8Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
-  const int64_t tiles = tiles_n * i8_tiles_m(a, T::BM);
+  const int64_t tiles = tiles_n * expert_tiles_m(a, T::BM);
   if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)tiles), block(T::NW * 64);
   if (a.index != nullptr)
@@ -658,7 +658,7 @@ hipError_t launch_variant(const I8Args& a, hipStream_t stream) {
 
 hipError_t launch_gathered_far(const I8Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + kBN - 1) / kBN;
-  const int64_t tiles = tiles_n * i8_tiles_m(a, kBM);
+  const int64_t tiles = tiles_n * expert_tiles_m(a, kBM);
   if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
   const int64_t most = (int64_t)kCus * 8;  // what runs at once takes tile after tile
   hipLaunchKernelGGL(int8_tile_kernel, dim3((unsigned)(tiles < most ? tiles : most)), dim3(256), 0, stream, a,

@@ -69,6 +69,74 @@ hipError_t launch_quantize_int8(const void* X, int in_type, int64_t rows, int64_
 struct I8Args;
 hipError_t launch_int8(const I8Args& a, hipStream_t stream);
 
+// Rows of `in_type` to E4M3 codes with one fp32 scale per row and 128 columns
+// (block_rows 1) or per 128 x 128 block (block_rows 128; E matrices of rows x K).
+hipError_t launch_quantize_fp8(const void* X, int in_type, int64_t E, int64_t rows, int64_t K, int block_rows, bool pow2,
+                               uint8_t* Q, float* S, hipStream_t stream);
+// E4M3 product with a scale per block of 128, dense or by expert (F8Args in mxg_fp8.h).
+struct F8Args;
+hipError_t launch_fp8(const F8Args& a, hipStream_t stream);
+
+// Gradient of an E4M3 product's weights from its activations' codes.
+struct F8GradArgs {
+  const void* dY;      // M x N
+  int64_t M;
+  const uint8_t* A;    // rows_a x K
+  const float* SA;     // rows_a x KB
+  int64_t rows_a;
+  int N, K, KB;
+  int E;               // experts; offsets == nullptr: one, all rows
+  const int32_t* offsets;
+  const int32_t* index;
+  int index_div;
+  uint32_t div_mul;    // as in I8Args
+  int div_shift;
+  void* dW;            // E x N x K of out_type
+  int out_type;
+  void* workspace;
+};
+int64_t fp8_weight_grad_bytes(int64_t M, int64_t N, int64_t K, int64_t E);
+hipError_t launch_fp8_weight_grad(const F8GradArgs& a, int y_type, hipStream_t stream);
+
+constexpr int kQuantNone = 0;
+constexpr int kQuantInt8 = 1;
+constexpr int kQuantFp8 = 2;
+constexpr int kQuantFp8Pow2 = 3;
+constexpr int kQuantMx = 4;
+
+// Norm of rows of K elements of a kOut* type; R, H, Y, Q, S and rstd may be nullptr.
+struct NormArgs {
+  const void* X;
+  const void* R;
+  const void* W;
+  int w_type;
+  int64_t rows;
+  int K;
+  float eps;
+  void* H;
+  void* Y;
+  int quant;
+  uint8_t* Q;
+  void* S;
+  float* rstd;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, int type, hipStream_t stream);
+struct NormGradArgs {
+  const void* dY;
+  const void* H;
+  const void* dH;  // or nullptr
+  const void* W;
+  int w_type;
+  const float* rstd;
+  int64_t rows;
+  int K;
+  void* dX;
+  float* dW;
+  void* workspace;
+};
+int64_t rmsnorm_backward_bytes(int64_t rows, int64_t K);
+hipError_t launch_rmsnorm_backward(const NormGradArgs& a, int type, hipStream_t stream);
+
 constexpr int kScoreSoftmax = 0;
 constexpr int kScoreSigmoid = 1;
 

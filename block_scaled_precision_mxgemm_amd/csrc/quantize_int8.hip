@@ -19,50 +19,21 @@
 // its last byte, so that a value takes about 7 instructions; with 20 (a
 // rounding instruction, tests on each value) the arithmetic, not the memory,
 // bound the kernel: 8192 x 14336 bf16 took 80 us.
+#include "mxg_codes.h"
 #include "mxg_internal.h"
-#include "mxg_rows.h"
 
 namespace mxg {
 namespace {
-
-constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-
-// t = x / s + kMagic with the last bit corrected
-__device__ __forceinline__ float corrected(float t, float x, float s, float half) {
-  const float r = t - kMagic;
-  const float d = fmaf(-r, s, x);
-  const bool odd = (__float_as_int(t) & 1) != 0;
-  if (d > half || (d == half && odd)) t += 1.0f;
-  if (d < -half || (d == -half && odd)) t -= 1.0f;
-  return t;
-}
 
 // The codes of 16 bytes of a row.
 template <int IN>
 __device__ __forceinline__ void put_codes(int8_t* q, const v4i& w, float s, float inv, float half) {
   constexpr int VEC = RowElem<IN>::VEC;
-  float f[VEC], t[VEC], far = 0.0f;
-  unpack16<IN>(w, f);
-#pragma unroll
-  for (int i = 0; i < VEC; i++) {
-    t[i] = fmaf(f[i], inv, kMagic);
-    far = fmaxf(far, fabsf(fmaf(kMagic - t[i], s, f[i])));
-  }
-  if (__any(far >= half)) {
-#pragma unroll
-    for (int i = 0; i < VEC; i++) t[i] = corrected(t[i], f[i], s, half);
-  }
+  float f[VEC];
   uint32_t c[VEC / 4];
-#pragma unroll
-  for (int i = 0; i < VEC / 4; i++) {
-    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(t[4 * i + 1]), __float_as_uint(t[4 * i]), 0x0c0c0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(t[4 * i + 3]), __float_as_uint(t[4 * i + 2]), 0x04000c0cu);
-    c[i] = lo | hi;
-  }
-  if constexpr (VEC == 8)
-    *reinterpret_cast<v2i*>(q) = v2i{(int)c[0], (int)c[1]};
-  else
-    *reinterpret_cast<uint32_t*>(q) = c[0];
+  unpack16<IN>(w, f);
+  int8_codes<VEC>(f, s, inv, half, c);
+  store_codes<VEC>((uint8_t*)q, c);
 }
 
 // Largest magnitude bits of the elements of 16 bytes, in the element type;

@@ -1,0 +1,412 @@
+// rmsnorm.hip - root-mean-square norm of rows, with the addition of a residual
+// before it and an output in 8-bit codes with scales, and its gradients.
+//
+//   h = x + r, rounded to the rows' type (what the backward pass is given is
+//       what was normed);
+//   rstd = 1 / sqrt(sum_k h_k^2 / K + eps);   y_k = (h_k rstd) w_k in fp32;
+//   codes of y: int8 with a scale per row, E4M3 with one per 128 columns, or
+//   E4M3 with a UE8M0 scale per 32 (the rules of the three quantizers, applied
+//   to the fp32 values: y is not rounded to 16 bits in between).
+//
+// One pass over memory: a row is held in registers between its sum and its
+// codes.  Sums are in fp32: a lane's own, then over the lanes, then over the
+// waves of a row.
+#include "mxg_codes.h"
+#include "mxg_internal.h"
+
+namespace mxg {
+namespace {
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
+  return x;
+}
+
+// Sum / largest over the L lanes of a row (all lanes of the workgroup that
+// belong to it call these); `part` is 16 words of LDS.
+template <int L>
+__device__ __forceinline__ float row_sum(float x, float* part) {
+  x = wave_sum(x);
+  if constexpr (L > 64) {
+    __syncthreads();  // what `part` held has been read
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < L / 64; w++) x += part[w];
+  }
+  return x;
+}
+template <int L>
+__device__ __forceinline__ uint32_t row_max(uint32_t x, float* part) {
+  x = lanes_max<64>(x);
+  if constexpr (L > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = __uint_as_float(x);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < L / 64; w++) x = max(x, __float_as_uint(part[w]));
+  }
+  return x;
+}
+
+// Weights k .. k + N - 1 in fp32.
+template <int N>
+__device__ __forceinline__ void load_weights(const void* W, int type, int k, float (&w)[N]) {
+  if (type == kOutF32) {
+#pragma unroll
+    for (int i = 0; i < N / 4; i++) {
+      const v4f v = *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(W) + k + 4 * i);
+#pragma unroll
+      for (int j = 0; j < 4; j++) w[4 * i + j] = v[j];
+    }
+    return;
+  }
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(W) + k;
+  uint32_t v[N / 2];
+  if constexpr (N == 8) {
+    const v4i u = *reinterpret_cast<const v4i*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = (uint32_t)u[i];
+  } else {
+    const v2i u = *reinterpret_cast<const v2i*>(p);
+    v[0] = (uint32_t)u[0];
+    v[1] = (uint32_t)u[1];
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; i++) {
+    const uint16_t lo = (uint16_t)(v[i] & 0xffffu), hi = (uint16_t)(v[i] >> 16);
+    w[2 * i] = type == kOutBF16 ? RowElem<kOutBF16>::get(lo) : RowElem<kOutF16>::get(lo);
+    w[2 * i + 1] = type == kOutBF16 ? RowElem<kOutBF16>::get(hi) : RowElem<kOutF16>::get(hi);
+  }
+}
+
+constexpr int norm_threads(int L) { return L > 256 ? L : 256; }
+
+// Row of this thread; -1: none.
+template <int L>
+__device__ __forceinline__ int64_t norm_row(int64_t rows) {
+  const int64_t group = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t row = group * (norm_threads(L) / L) + threadIdx.x / L;
+  return row < rows ? row : -1;
+}
+
+// L lanes per row.  HELD > 0: its 16-byte pieces, at most HELD of them a lane,
+// stay in registers; HELD = 0: longer rows are read twice (three times for
+// int8), after the first time from the caches.
+template <int IN, int HELD, int L>
+__global__ __launch_bounds__(norm_threads(L)) void rmsnorm_kernel(NormArgs a) {
+  constexpr int VEC = RowElem<IN>::VEC;
+  using T = typename RowElem<IN>::type;
+  __shared__ float part[16];
+  const int64_t row = norm_row<L>(a.rows);
+  if (row < 0) return;
+  const int tid = threadIdx.x % L;
+  const int nv = a.K / VEC;
+  const int64_t base = row * a.K;
+  const v4i* x = reinterpret_cast<const v4i*>((const T*)a.X + base);
+  const v4i* res = reinterpret_cast<const v4i*>((const T*)a.R + base);
+  v4i* h = reinterpret_cast<v4i*>((T*)a.H + base);
+  const v4i zero = {0, 0, 0, 0};
+  const int steps = HELD > 0 ? HELD : (nv + L - 1) / L;
+
+  // the rounded sum's piece i, with the sum of its squares
+  float sum = 0.0f;
+  auto add = [&](int i, v4i w) {
+    float f[VEC];
+    unpack16<IN>(w, f);
+    if (a.R != nullptr) {
+      float g[VEC];
+      unpack16<IN>(res[i], g);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) f[j] += g[j];
+      w = pack16<IN>(f);
+      h[i] = w;
+      unpack16<IN>(w, f);
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; j++) sum = fmaf(f[j], f[j], sum);
+    return w;
+  };
+  v4i held[HELD > 0 ? HELD : 1];
+  if constexpr (HELD > 0) {
+#pragma unroll
+    for (int u = 0; u < HELD; u++) {
+      const int i = tid + u * L;
+      held[u] = i < nv ? x[i] : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < HELD; u++) {
+      const int i = tid + u * L;
+      if (i < nv) held[u] = add(i, held[u]);
+    }
+  } else {
+    for (int i = tid; i < nv; i += L) add(i, x[i]);
+  }
+  sum = row_sum<L>(sum, part);
+  const float rstd = 1.0f / sqrtf(sum / (float)a.K + a.eps);
+  if (a.rstd != nullptr && tid == 0) a.rstd[row] = rstd;
+
+  // y of step u (zeros past the row's end)
+  const v4i* from = a.R != nullptr ? h : x;
+  auto value = [&](int u, float (&y)[VEC]) {
+    const int i = tid + u * L;
+    if (i < nv) {
+      float w[VEC];
+      if constexpr (HELD > 0)
+        unpack16<IN>(held[u], y);
+      else
+        unpack16<IN>(from[i], y);
+      load_weights<VEC>(a.W, a.w_type, i * VEC, w);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) y[j] = y[j] * rstd * w[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; j++) y[j] = 0.0f;
+    }
+    return i;
+  };
+  float s = 0.0f, inv = 0.0f;
+  if (a.quant == kQuantInt8) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int u = 0; u < steps; u++) {
+      float y[VEC];
+      value(u, y);
+      most = max(most, magnitude_bits<VEC>(y));
+    }
+    most = row_max<L>(most, part);
+    if (most >= 0x7f800000u) {
+      s = __builtin_nanf("");
+    } else if (most > 0u) {
+      s = fmaxf(__uint_as_float(most) / 127.0f, 0x1p-126f);
+      inv = 1.0f / s;
+    }
+    if (tid == 0) reinterpret_cast<float*>(a.S)[row] = s;
+  }
+  const int KB = (a.K + kBlock - 1) / kBlock;
+  uint8_t* q = a.Q + base;
+#pragma unroll
+  for (int u = 0; u < steps; u++) {
+    float y[VEC];
+    const int i = value(u, y);
+    const bool valid = i < nv;
+    if (a.Y != nullptr && valid) reinterpret_cast<v4i*>((T*)a.Y + base)[i] = pack16<IN>(y);
+    uint32_t c[VEC / 4];
+    if (a.quant == kQuantInt8) {
+      if (inv > 0.0f) {
+        int8_codes<VEC>(y, s, inv, 0.5f * s, c);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC / 4; j++) c[j] = 0;
+      }
+    } else if (a.quant == kQuantMx) {
+      constexpr int LB = 32 / VEC;
+      const uint32_t amax = lanes_max<LB>(magnitude_bits<VEC>(y));
+      const bool bad = amax >= 0x7f800000u;
+      const int exponent = amax == 0u ? -127 : min(max(__builtin_amdgcn_frexp_expf(__uint_as_float(amax)) - 9, -127), 127);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) y[j] = ldexpf(y[j], -exponent);
+      e4m3_codes<VEC>(y, 1.0f, !bad, c);
+      if (valid && i % LB == 0)
+        reinterpret_cast<uint8_t*>(a.S)[row * (a.K / 32) + i / LB] = bad ? (uint8_t)255 : (uint8_t)(exponent + 127);
+    } else if (a.quant != kQuantNone) {
+      constexpr int LB = kBlock / VEC;
+      const float sb = block_scale(lanes_max<LB>(magnitude_bits<VEC>(y)), a.quant == kQuantFp8Pow2);
+      const float ib = block_inverse(sb);
+      e4m3_codes<VEC>(y, ib, sb == sb, c);
+      if (valid && i % LB == 0) reinterpret_cast<float*>(a.S)[row * KB + i / LB] = sb;
+    }
+    if (a.quant != kQuantNone && valid) store_codes<VEC>(q + (int64_t)i * VEC, c);
+  }
+}
+
+template <int IN, int HELD, int L>
+void norm_rows(const NormArgs& a, hipStream_t stream) {
+  constexpr int threads = norm_threads(L), per = threads / L;
+  // in two dimensions: a launch has less than 2^32 threads in one
+  const int64_t groups = (a.rows + per - 1) / per, most = 1 << 20;
+  const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)((groups + most - 1) / most));
+  hipLaunchKernelGGL((rmsnorm_kernel<IN, HELD, L>), grid, dim3(threads), 0, stream, a);
+}
+
+template <int IN>
+void norm_in(const NormArgs& a, hipStream_t stream) {
+  const int64_t pieces = a.K / RowElem<IN>::VEC;
+  if (pieces <= 64)
+    norm_rows<IN, 1, 64>(a, stream);
+  else if (pieces <= 2 * 64)
+    norm_rows<IN, 2, 64>(a, stream);
+  else if (pieces <= 2 * 256)
+    norm_rows<IN, 2, 256>(a, stream);
+  else if (pieces <= 4 * 256)
+    norm_rows<IN, 4, 256>(a, stream);
+  else if (pieces <= 4 * 1024)
+    norm_rows<IN, 4, 1024>(a, stream);
+  else
+    norm_rows<IN, 0, 1024>(a, stream);
+}
+
+// ---- gradients ----------------------------------------------------------------
+//
+//   hat = h rstd, g = dy w:   dx = rstd (g - hat sum_k(g hat) / K) + dh,
+//   dw = sum over rows of dy hat.
+template <int IN, int HELD, int L>
+__global__ __launch_bounds__(norm_threads(L)) void rmsnorm_backward_kernel(NormGradArgs a) {
+  constexpr int VEC = RowElem<IN>::VEC;
+  using T = typename RowElem<IN>::type;
+  __shared__ float part[16];
+  const int64_t row = norm_row<L>(a.rows);
+  if (row < 0) return;
+  const int tid = threadIdx.x % L;
+  const int nv = a.K / VEC;
+  const int64_t base = row * a.K;
+  const v4i* dy = reinterpret_cast<const v4i*>((const T*)a.dY + base);
+  const v4i* h = reinterpret_cast<const v4i*>((const T*)a.H + base);
+  const v4i* dh = reinterpret_cast<const v4i*>((const T*)a.dH + base);
+  v4i* dx = reinterpret_cast<v4i*>((T*)a.dX + base);
+  const v4i zero = {0, 0, 0, 0};
+  const float rstd = a.rstd[row];
+  v4i hy[HELD > 0 ? HELD : 1], hh[HELD > 0 ? HELD : 1];
+  float sum = 0.0f;
+  auto dot = [&](int i, const v4i& y, const v4i& x) {
+    float f[VEC], g[VEC], w[VEC];
+    unpack16<IN>(y, g);
+    unpack16<IN>(x, f);
+    load_weights<VEC>(a.W, a.w_type, i * VEC, w);
+#pragma unroll
+    for (int j = 0; j < VEC; j++) sum = fmaf(g[j] * w[j], f[j] * rstd, sum);
+  };
+  if constexpr (HELD > 0) {
+#pragma unroll
+    for (int u = 0; u < HELD; u++) {
+      const int i = tid + u * L;
+      hy[u] = i < nv ? dy[i] : zero;
+      hh[u] = i < nv ? h[i] : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < HELD; u++)
+      if (tid + u * L < nv) dot(tid + u * L, hy[u], hh[u]);
+  } else {
+    for (int i = tid; i < nv; i += L) dot(i, dy[i], h[i]);
+  }
+  const float c = row_sum<L>(sum, part) / (float)a.K;
+  auto put = [&](int i, const v4i& y, const v4i& x) {
+    float f[VEC], g[VEC], w[VEC];
+    unpack16<IN>(y, g);
+    unpack16<IN>(x, f);
+    load_weights<VEC>(a.W, a.w_type, i * VEC, w);
+#pragma unroll
+    for (int j = 0; j < VEC; j++) f[j] = rstd * (g[j] * w[j] - f[j] * rstd * c);
+    if (a.dH != nullptr) {
+      unpack16<IN>(dh[i], g);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) f[j] += g[j];
+    }
+    dx[i] = pack16<IN>(f);
+  };
+  if constexpr (HELD > 0) {
+#pragma unroll
+    for (int u = 0; u < HELD; u++)
+      if (tid + u * L < nv) put(tid + u * L, hy[u], hh[u]);
+  } else {
+    for (int i = tid; i < nv; i += L) put(i, dy[i], h[i]);
+  }
+}
+
+// Sums of dy hat over strips of rows, then over the strips: no atomics, so that
+// every run gives the same bits.
+template <int IN>
+__global__ __launch_bounds__(256) void rmsnorm_dweight_kernel(NormGradArgs a, int64_t strip, float* part) {
+  constexpr int VEC = RowElem<IN>::VEC;
+  using T = typename RowElem<IN>::type;
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.K / VEC) return;
+  const int64_t r0 = blockIdx.y * strip, r1 = min(r0 + strip, a.rows);
+  float acc[VEC] = {};
+  for (int64_t r = r0; r < r1; r++) {
+    float f[VEC], g[VEC];
+    unpack16<IN>(reinterpret_cast<const v4i*>((const T*)a.dY + r * a.K)[i], g);
+    unpack16<IN>(reinterpret_cast<const v4i*>((const T*)a.H + r * a.K)[i], f);
+    const float rstd = a.rstd[r];
+#pragma unroll
+    for (int j = 0; j < VEC; j++) acc[j] = fmaf(g[j], f[j] * rstd, acc[j]);
+  }
+  float* p = part + (int64_t)blockIdx.y * a.K + i * VEC;
+#pragma unroll
+  for (int j = 0; j < VEC / 4; j++)
+    *reinterpret_cast<v4f*>(p + 4 * j) = v4f{acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]};
+}
+__global__ __launch_bounds__(256) void rmsnorm_dweight_sum_kernel(const float* part, int strips, int K, float* dW) {
+  const int k = blockIdx.x * 256 + threadIdx.x;
+  if (k >= K) return;
+  float s = 0.0f;
+  for (int i = 0; i < strips; i++) s += part[(int64_t)i * K + k];
+  dW[k] = s;
+}
+
+// Strips of rows that the weight's gradient is summed over.
+int strips_of(int64_t rows) { return (int)(rows < 256 ? rows : 256); }
+
+template <int IN, int HELD, int L>
+void backward_rows(const NormGradArgs& a, hipStream_t stream) {
+  constexpr int threads = norm_threads(L), per = threads / L;
+  const int64_t groups = (a.rows + per - 1) / per, most = 1 << 20;
+  const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)((groups + most - 1) / most));
+  hipLaunchKernelGGL((rmsnorm_backward_kernel<IN, HELD, L>), grid, dim3(threads), 0, stream, a);
+}
+
+template <int IN>
+void backward_in(const NormGradArgs& a, hipStream_t stream) {
+  const int64_t pieces = a.K / RowElem<IN>::VEC;
+  const int strips = strips_of(a.rows);
+  float* part = reinterpret_cast<float*>(a.workspace);
+  // the sums first: dX may be dY
+  hipLaunchKernelGGL((rmsnorm_dweight_kernel<IN>), dim3((unsigned)((pieces + 255) / 256), (unsigned)strips), dim3(256), 0,
+                     stream, a, (a.rows + strips - 1) / strips, part);
+  hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel, dim3((unsigned)((a.K + 255) / 256)), dim3(256), 0, stream, part, strips,
+                     a.K, a.dW);
+  if (pieces <= 64)
+    backward_rows<IN, 1, 64>(a, stream);
+  else if (pieces <= 2 * 256)
+    backward_rows<IN, 2, 256>(a, stream);
+  else if (pieces <= 4 * 1024)
+    backward_rows<IN, 4, 1024>(a, stream);
+  else
+    backward_rows<IN, 0, 1024>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormArgs& a, int type, hipStream_t stream) {
+  switch (type) {
+    case kOutF32:
+      norm_in<kOutF32>(a, stream);
+      break;
+    case kOutBF16:
+      norm_in<kOutBF16>(a, stream);
+      break;
+    default:
+      norm_in<kOutF16>(a, stream);
+  }
+  return hipGetLastError();
+}
+
+int64_t rmsnorm_backward_bytes(int64_t rows, int64_t K) { return (int64_t)strips_of(rows) * K * 4; }
+
+hipError_t launch_rmsnorm_backward(const NormGradArgs& a, int type, hipStream_t stream) {
+  switch (type) {
+    case kOutF32:
+      backward_in<kOutF32>(a, stream);
+      break;
+    case kOutBF16:
+      backward_in<kOutBF16>(a, stream);
+      break;
+    default:
+      backward_in<kOutF16>(a, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mxg

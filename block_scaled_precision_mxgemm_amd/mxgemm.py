@@ -48,6 +48,12 @@ CEIL_FP16 = 16
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
 INT8_MAX_K = 131056
+# codes that rmsnorm_quantize writes (MXG_QUANT_*)
+QUANT_NONE = 0
+QUANT_INT8 = 1
+QUANT_FP8 = 2
+QUANT_FP8_POW2 = 3
+QUANT_MXFP8 = 4
 _OUT_DTYPES = {OUT_F32: torch.float32, OUT_BF16: torch.bfloat16, OUT_F16: torch.float16}
 _DTYPE_IDS = {t: i for i, t in _OUT_DTYPES.items()}
 
@@ -95,6 +101,20 @@ def _load():
     lib.expert_plan.argtypes = [p, i64, ci, i64, p, p, p, p, p]
     lib.expert_combine.argtypes = [p, ci, i64, i64, p, p, i64, ci, p, ci, p]
     lib.expert_combine_backward.argtypes = [p, ci, p, ci, i64, i64, p, p, i64, ci, p, p, p]
+    lib.fp8gemm_quantize.argtypes = [p, ci, i64, i64, i64, ci, ci, p, p, p]
+    lib.fp8gemm_run.argtypes = [p, p, p, p, p, i64, i64, i64, p, ci, ci, p]
+    lib.fp8gemm_run_grouped.argtypes = [p, p, i64, p, p, p, i64, i64, i64, i64, p, p, ci, p, ci, ci, p]
+    lib.fp8gemm_weight_grad.argtypes = [p, ci, i64, i64, p, p, i64, p, ci, p, p]
+    lib.fp8gemm_weight_grad_grouped.argtypes = [p, ci, i64, i64, p, p, i64, i64, i64, p, p, ci, p, ci, p, p]
+    lib.rmsnorm_quantize.argtypes = [p, p, ci, p, ci, i64, i64, cf, p, p, ci, p, p, p, p]
+    lib.rmsnorm_backward.argtypes = [p, p, p, ci, p, ci, p, i64, i64, p, p, p, p]
+    lib.fp8gemm_weight_grad_workspace.argtypes = [i64, i64, i64, i64]
+    lib.rmsnorm_backward_workspace.argtypes = [i64, i64]
+    for name in ("fp8gemm_quantize", "fp8gemm_run", "fp8gemm_run_grouped", "fp8gemm_weight_grad",
+                 "fp8gemm_weight_grad_grouped", "rmsnorm_quantize", "rmsnorm_backward"):
+        getattr(lib, name).restype = ci
+    for name in ("fp8gemm_weight_grad_workspace", "rmsnorm_backward_workspace"):
+        getattr(lib, name).restype = i64
     for name in ("int8gemm_quantize", "int8gemm_run", "int8gemm_run_grouped", "expert_route", "expert_route_backward",
                  "expert_plan", "expert_combine", "expert_combine_backward"):
         getattr(lib, name).restype = ci
@@ -547,6 +567,218 @@ def expert_combine_backward(d_out, y, position, weights, d_y: torch.Tensor | Non
           _DTYPE_IDS[y.dtype], rows, N, position.data_ptr(), weights.data_ptr(), T, k, d_y.data_ptr(),
           d_weights.data_ptr())
     return d_y, d_weights
+
+
+# ---- E4M3 products with a scale per block of 128 -------------------------------
+
+
+def _blocks(d: int) -> int:
+    return (d + 127) // 128
+
+
+def _codes_arg(t, name: str, dim: int, like: torch.Tensor | None = None, shape=None) -> torch.Tensor:
+    """E4M3 codes: uint8, or float8_e4m3fn taken as its bytes."""
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
+        t = t.view(torch.uint8)
+    return _arg(t, name, (torch.uint8,), shape, dim, like)
+
+
+def fp8gemm_quantize(x: torch.Tensor, block_rows: int = 1, pow2: bool = False, q: torch.Tensor | None = None,
+                     s: torch.Tensor | None = None, stream=None):
+    """Quantize rows (rows x K or E x rows x K of float32, bfloat16 or float16, K a
+    multiple of 16) to (E4M3 codes as uint8, fp32 scales): one per row and 128
+    columns (block_rows 1: activations) or per 128 x 128 block (block_rows 128:
+    weights).  pow2: scales that are powers of two, as fp8gemm_weight_grad takes
+    them without another rounding."""
+    x = _arg(x, "x", _FLOATS)
+    if x.dim() not in (2, 3):
+        raise ValueError("x must have 2 or 3 dimensions")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    rows, K = x.shape[-2:]
+    E = x.shape[0] if x.dim() == 3 else 1
+    lead = tuple(x.shape[:-2])
+    q = _out(q, "q", torch.uint8, lead + (rows, K), x, stream)
+    s = _out(s, "s", torch.float32, lead + (-(-rows // block_rows), _blocks(K)), x, stream)
+    _call("fp8gemm_quantize", x.device, stream, x.data_ptr(), _DTYPE_IDS[x.dtype], E, rows, K, block_rows, int(pow2),
+          q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def fp8gemm_run(a_q, a_s, b_q, b_s, bias: torch.Tensor | None = None, act: int = ACT_NONE, out_type: int = OUT_F32,
+                out: torch.Tensor | None = None, stream=None):
+    """C = out_type(act(sum_b a_s[i][b] b_s[j // 128][b] sum_{k in block b} a_q[i][k] b_q[j][k]
+    + bias[j])), blocks of 128 columns; a_q: M x K, b_q: N x K E4M3 codes; a_s: M x KB,
+    b_s: NB x KB float32 (KB, NB the blocks of K and N)."""
+    if out_type not in _OUT_DTYPES:
+        raise ValueError("unknown out_type %r" % (out_type,))
+    a_q = _codes_arg(a_q, "a_q", 2)
+    M, K = a_q.shape
+    b_q = _codes_arg(b_q, "b_q", 2, a_q)
+    N = b_q.shape[0]
+    if b_q.shape[1] != K:
+        raise ValueError("inner dimensions disagree: a_q %s, b_q %s" % (tuple(a_q.shape), tuple(b_q.shape)))
+    a_s = _arg(a_s, "a_s", (torch.float32,), (M, _blocks(K)), like=a_q)
+    b_s = _arg(b_s, "b_s", (torch.float32,), (_blocks(N), _blocks(K)), like=a_q)
+    if bias is not None:
+        bias = _on16(_arg(bias, "bias", (torch.float32,), (N,), like=a_q), stream)
+    out = _out(out, "out", _OUT_DTYPES[out_type], (M, N), a_q, stream)
+    _call("fp8gemm_run", a_q.device, stream, a_q.data_ptr(), a_s.data_ptr(), b_q.data_ptr(), b_s.data_ptr(),
+          out.data_ptr(), M, N, K, _ptr(bias), act, out_type)
+    return out
+
+
+def fp8gemm_run_grouped(a_q, a_s, b_q, b_s, offsets, index: torch.Tensor | None = None, index_div: int = 1,
+                        bias: torch.Tensor | None = None, act: int = ACT_NONE, out_type: int = OUT_F32,
+                        out: torch.Tensor | None = None, stream=None):
+    """The products of E experts: rows offsets[e] .. offsets[e+1]-1 of the result
+    with b_q[e] (E x N x K), b_s[e] (E x NB x KB) and bias[e] (E x N).  offsets, index,
+    index_div and rows outside the offsets as for int8gemm_run_grouped."""
+    if out_type not in _OUT_DTYPES:
+        raise ValueError("unknown out_type %r" % (out_type,))
+    a_q = _codes_arg(a_q, "a_q", 2)
+    rows_a, K = a_q.shape
+    b_q = _codes_arg(b_q, "b_q", 3, a_q)
+    E, N = b_q.shape[:2]
+    if b_q.shape[2] != K:
+        raise ValueError("inner dimensions disagree: a_q %s, b_q %s" % (tuple(a_q.shape), tuple(b_q.shape)))
+    a_s = _arg(a_s, "a_s", (torch.float32,), (rows_a, _blocks(K)), like=a_q)
+    b_s = _arg(b_s, "b_s", (torch.float32,), (E, _blocks(N), _blocks(K)), like=a_q)
+    offsets = _arg(offsets, "offsets", (torch.int32,), (E + 1,), like=a_q)
+    rows = rows_a
+    if index is not None:
+        index = _arg(index, "index", (torch.int32,), dim=1, like=a_q)
+        rows = index.shape[0]
+    if bias is not None:
+        bias = _on16(_arg(bias, "bias", (torch.float32,), (E, N), like=a_q), stream)
+    out = _out(out, "out", _OUT_DTYPES[out_type], (rows, N), a_q, stream)
+    _call("fp8gemm_run_grouped", a_q.device, stream, a_q.data_ptr(), a_s.data_ptr(), rows_a, b_q.data_ptr(),
+          b_s.data_ptr(), out.data_ptr(), rows, N, K, E, offsets.data_ptr(), _ptr(index), index_div, _ptr(bias), act,
+          out_type)
+    return out
+
+
+def _grad_workspace(rows: int, N: int, K: int, E: int, device: torch.device, stream):
+    need = (_lib or _load()).fp8gemm_weight_grad_workspace(rows, N, K, E)
+    if need < 0:
+        _check(1, "fp8gemm_weight_grad")
+    return _new((need,), torch.uint8, device, stream) if need else None
+
+
+def fp8gemm_weight_grad(d_c, a_q, a_s, out_type: int = OUT_F32, out: torch.Tensor | None = None, stream=None):
+    """Gradient of fp8gemm_run's weights (N x K) from that of its result (d_c: M x N
+    of float32, bfloat16 or float16) and the activations' codes (a_q: M x K, a_s: M x
+    KB): sum_m d_c[m][n] a_s[m][k // 128] a_q[m][k], in fp32.  The products a_s a_q are
+    rounded to bfloat16, which leaves them as they are when the scales are powers
+    of two.  (The gradient of the activations is fp8gemm_run of the quantized d_c with
+    the transposed weights and scales.)"""
+    if out_type not in _OUT_DTYPES:
+        raise ValueError("unknown out_type %r" % (out_type,))
+    d_c = _arg(d_c, "d_c", _FLOATS, dim=2)
+    M, N = d_c.shape
+    a_q = _codes_arg(a_q, "a_q", 2, d_c)
+    K = a_q.shape[1]
+    if a_q.shape[0] != M:
+        raise ValueError("rows disagree: d_c %s, a_q %s" % (tuple(d_c.shape), tuple(a_q.shape)))
+    a_s = _arg(a_s, "a_s", (torch.float32,), (M, _blocks(K)), like=d_c)
+    out = _out(out, "out", _OUT_DTYPES[out_type], (N, K), d_c, stream)
+    workspace = _grad_workspace(M, N, K, 1, d_c.device, stream)
+    _call("fp8gemm_weight_grad", d_c.device, stream, d_c.data_ptr(), _DTYPE_IDS[d_c.dtype], M, N, a_q.data_ptr(),
+          a_s.data_ptr(), K, out.data_ptr(), out_type, _ptr(workspace))
+    return out
+
+
+def fp8gemm_weight_grad_grouped(d_c, a_q, a_s, offsets, index: torch.Tensor | None = None, index_div: int = 1,
+                                out_type: int = OUT_F32, out: torch.Tensor | None = None, stream=None):
+    """Gradients of the weights of E experts (E x N x K): that of expert e from rows
+    offsets[e] .. offsets[e+1]-1 of d_c (rows x N), row p against row index[p] //
+    index_div of a_q and a_s, or row p without an index.  Zeros for an expert without
+    rows; a row whose index is outside a_q makes its expert's gradient NaN."""
+    if out_type not in _OUT_DTYPES:
+        raise ValueError("unknown out_type %r" % (out_type,))
+    d_c = _arg(d_c, "d_c", _FLOATS, dim=2)
+    rows, N = d_c.shape
+    a_q = _codes_arg(a_q, "a_q", 2, d_c)
+    rows_a, K = a_q.shape
+    a_s = _arg(a_s, "a_s", (torch.float32,), (rows_a, _blocks(K)), like=d_c)
+    offsets = _arg(offsets, "offsets", (torch.int32,), dim=1, like=d_c)
+    E = offsets.shape[0] - 1
+    if index is not None:
+        index = _arg(index, "index", (torch.int32,), (rows,), like=d_c)
+    elif rows_a < rows:
+        raise ValueError("a_q has %d rows, d_c %d" % (rows_a, rows))
+    out = _out(out, "out", _OUT_DTYPES[out_type], (E, N, K), d_c, stream)
+    workspace = _grad_workspace(rows, N, K, E, d_c.device, stream)
+    _call("fp8gemm_weight_grad_grouped", d_c.device, stream, d_c.data_ptr(), _DTYPE_IDS[d_c.dtype], rows, N,
+          a_q.data_ptr(), a_s.data_ptr(), rows_a, K, E, offsets.data_ptr(), _ptr(index), index_div, out.data_ptr(),
+          out_type, _ptr(workspace))
+    return out
+
+
+# ---- root-mean-square norm with an 8-bit output ----------------------------------
+
+
+def rmsnorm_quantize(x, weight, residual: torch.Tensor | None = None, quant: int = QUANT_FP8, eps: float = 1e-6,
+                     with_y: bool = False, q: torch.Tensor | None = None, s: torch.Tensor | None = None,
+                     h: torch.Tensor | None = None, y: torch.Tensor | None = None, rstd: torch.Tensor | None = None,
+                     stream=None):
+    """h = x + residual (x without one); y = h / sqrt(mean(h^2) + eps) * weight; codes
+    and scales of y: (q, s, h, y, rstd).  x, residual: rows x K of float32, bfloat16
+    or float16, weight: K of any of them.  quant: QUANT_INT8 (q int8, s per row),
+    QUANT_FP8 / QUANT_FP8_POW2 (q uint8, s rows x KB: fp8gemm_run), QUANT_MXFP8 (q, s
+    uint8, s rows x K / 32: mxgemm_run) or QUANT_NONE (q and s are None, y is given).
+    y, in x's type, only with_y (or when passed); h may be x or residual; rstd (rows
+    float32) is what rmsnorm_backward takes."""
+    x = _arg(x, "x", _FLOATS, dim=2)
+    rows, K = x.shape
+    weight = _arg(weight, "weight", _FLOATS, (K,), like=x)
+    if quant not in (QUANT_NONE, QUANT_INT8, QUANT_FP8, QUANT_FP8_POW2, QUANT_MXFP8):
+        raise ValueError("unknown quant %r" % (quant,))
+    if residual is not None:
+        residual = _arg(residual, "residual", (x.dtype,), (rows, K), like=x)
+        h = _out(h, "h", x.dtype, (rows, K), x, stream)
+    elif h is not None:
+        raise ValueError("h is written only with a residual")
+    if quant == QUANT_NONE:
+        if q is not None or s is not None:
+            raise ValueError("q and s are written only with a quant")
+    else:
+        q = _out(q, "q", torch.int8 if quant == QUANT_INT8 else torch.uint8, (rows, K), x, stream)
+        if quant == QUANT_MXFP8:
+            s = _out(s, "s", torch.uint8, (rows, K // 32), x, stream)
+        else:
+            s = _out(s, "s", torch.float32, (rows,) if quant == QUANT_INT8 else (rows, _blocks(K)), x, stream)
+    if y is not None or with_y or quant == QUANT_NONE:
+        y = _out(y, "y", x.dtype, (rows, K), x, stream)
+    rstd = _out(rstd, "rstd", torch.float32, (rows,), x, stream)
+    _call("rmsnorm_quantize", x.device, stream, x.data_ptr(), _ptr(residual), _DTYPE_IDS[x.dtype], weight.data_ptr(),
+          _DTYPE_IDS[weight.dtype], rows, K, eps, _ptr(h), _ptr(y), quant, _ptr(q), _ptr(s), rstd.data_ptr())
+    return q, s, x if h is None else h, y, rstd
+
+
+def rmsnorm_backward(d_y, h, weight, rstd, d_h: torch.Tensor | None = None, d_x: torch.Tensor | None = None,
+                     d_weight: torch.Tensor | None = None, stream=None):
+    """Gradients (d_x in h's type, of x and of the residual alike; d_weight K float32)
+    of rmsnorm_quantize's y from d_y, with h and rstd as it gave them.  d_h: the
+    gradient that h gets besides, added to d_x.  d_x may be d_y or d_h.  The rounding
+    to codes counts as the identity."""
+    h = _arg(h, "h", _FLOATS, dim=2)
+    rows, K = h.shape
+    d_y = _arg(d_y, "d_y", (h.dtype,), (rows, K), like=h)
+    weight = _arg(weight, "weight", _FLOATS, (K,), like=h)
+    rstd = _arg(rstd, "rstd", (torch.float32,), (rows,), like=h)
+    if d_h is not None:
+        d_h = _arg(d_h, "d_h", (h.dtype,), (rows, K), like=h)
+    need = (_lib or _load()).rmsnorm_backward_workspace(rows, K)
+    if need < 0:
+        _check(1, "rmsnorm_backward")
+    d_x = _out(d_x, "d_x", h.dtype, (rows, K), h, stream)
+    d_weight = _out(d_weight, "d_weight", torch.float32, (K,), h, stream)
+    workspace = _new((need,), torch.uint8, h.device, stream) if need else None
+    _call("rmsnorm_backward", h.device, stream, d_y.data_ptr(), h.data_ptr(), _ptr(d_h), _DTYPE_IDS[h.dtype],
+          weight.data_ptr(), _DTYPE_IDS[weight.dtype], rstd.data_ptr(), rows, K, d_x.data_ptr(), d_weight.data_ptr(),
+          _ptr(workspace))
+    return d_x, d_weight
 
 
 def raw_library():

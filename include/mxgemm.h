@@ -49,7 +49,7 @@ extern "C" {
 
 /* Status codes. */
 #define MXG_OK 0
-#define MXG_EINVAL 1         /* null pointer, non-positive or oversized dim, K % 32 != 0, bad enum */
+#define MXG_EINVAL 1         /* null pointer, non-positive or oversized dim, K % 32 != 0 (int8 and fp8 calls: K % 16), bad enum */
 #define MXG_EALIGN 2         /* a pointer is not aligned as its call asks (data: 16 bytes) */
 #define MXG_EUNSUPPORTED 3   /* current device is not gfx950 */
 #define MXG_EHIP 4           /* the HIP runtime reported an error at launch */
@@ -496,6 +496,182 @@ int expert_combine_backward(const void *dOut, int out_type, const void *Y,
                             const int32_t *position, const float *weights,
                             int64_t T, int k, void *dY, float *dW,
                             void *stream);
+
+/*
+ * ---- E4M3 products with a scale per block of 128 ----------------------------
+ *
+ * Codes are E4M3 bytes; scales are fp32, any values.  KB = ceil(K / 128), NB =
+ * ceil(N / 128); the last block of a row or of the rows may be shorter.
+ *
+ * fp8gemm_quantize - E matrices of rows x K (fp32, bf16 or fp16) -> E4M3 codes plus
+ * one fp32 scale per row and 128 columns (block_rows 1: activations) or per 128 x
+ * 128 block (block_rows 128: weights).  For every block:
+ *   s    = amax / 448 in fp32 (amax: its largest magnitude), at least 2^-126 when
+ *          amax > 0; with pow2 the next power of two that is not smaller; 0 when
+ *          amax = 0;
+ *   code = x * (1 / s), each in fp32, rounded to the nearest E4M3 value, ties to
+ *          even, saturated to +-448; the sign is kept (-0 -> 0x80).
+ * A block holding a NaN or an infinity gets s = NaN and zero codes.  Values with
+ * pow2 scales are bf16 values (fp8gemm_weight_grad).
+ *
+ *   X           device, E x rows x K elements of in_type, 16-byte aligned (read only)
+ *   E           1 .. MXG_MAX_EXPERTS;  rows 1 .. MXG_MAX_SLOTS (block_rows 128:
+ *               MXG_MAX_DIM), E * rows <= MXG_MAX_SLOTS with block_rows 1
+ *   K           16 .. MXG_MAX_DIM, K % 16 == 0
+ *   block_rows  1 or 128;  pow2 0 or 1
+ *   Q           device, E x rows x K bytes, 16-byte aligned (written)
+ *   S           device, E x ceil(rows / block_rows) x KB fp32, 4-byte aligned (written)
+ * Returns MXG_OK or an error status.  The output is bit-for-bit deterministic.
+ */
+int fp8gemm_quantize(const void *X, int in_type, int64_t E, int64_t rows, int64_t K,
+                     int block_rows, int pow2, uint8_t *Q, float *S, void *stream);
+
+/*
+ * fp8gemm_run - C[i][j] = out_type(act(sum_b (scaleA[i][b] * scaleB[j / 128][b])
+ * * p_b + bias[j])), p_b = sum of a[i][k] * b[j][k] over the k of block b (128
+ * columns).  The two scales are multiplied in fp32; p_b times that is added in
+ * fp32, rounded once a block; then the output step of mxgemm_run_fused.
+ *
+ * Accuracy: p_b is formed by the fp8 MFMA, which adds 128 products in one
+ * operation and drops bits far below the largest of them (mxgemm_run): at most
+ * 2^-7 of the largest product of the block (2^-16 of p_b, root mean square, on
+ * normal data); the sum over blocks adds 2 KB * 2^-24 * sum |terms|.
+ *
+ *   A        device, M x K E4M3 codes, 16-byte aligned
+ *   scaleA   device, M x KB fp32, 4-byte aligned
+ *   B        device, N x K codes, 16-byte aligned
+ *   scaleB   device, NB x KB fp32, 4-byte aligned
+ *   C        device, M x N elements of out_type, 16-byte aligned; overwritten
+ *   M, N     1 .. MXG_MAX_DIM;  K 16 .. MXG_MAX_DIM, K % 16 == 0
+ *   bias, act, out_type  as for mxgemm_run_fused
+ * The gradient of A is the same product with dC (quantized) and the weights'
+ * transpose, whose blocks are those of the weights; that of B is
+ * fp8gemm_weight_grad.
+ * Returns MXG_OK or an error status.  Deterministic; the order of the sum over
+ * blocks goes by the sizes.
+ */
+int fp8gemm_run(const uint8_t *A, const float *scaleA, const uint8_t *B,
+                const float *scaleB, void *C, int64_t M, int64_t N, int64_t K,
+                const float *bias, int act, int out_type, void *stream);
+
+/*
+ * fp8gemm_run_grouped - the products of E experts in one call, as
+ * int8gemm_run_grouped has them: rows offsets[e] .. offsets[e+1]-1 of C with B,
+ * scaleB and bias of expert e; row p of C takes row index[p] / index_div of A and
+ * scaleA (index == NULL: row p).
+ *
+ *   A, scaleA  rowsA rows (1 .. MXG_MAX_SLOTS)
+ *   B          E x N x K codes;  scaleB E x NB x KB fp32;  bias E x N fp32 or NULL
+ *   C          rows x N elements of out_type (rows 1 .. MXG_MAX_SLOTS; with
+ *              index == NULL at most rowsA)
+ *   E          1 .. MXG_MAX_EXPERTS
+ *   offsets, index, index_div  as for int8gemm_run_grouped (offsets outside 0 ..
+ *              rows and falling ones too)
+ * Rows of C outside offsets[0] .. offsets[E]-1 are left as they were.  A row whose
+ * index is negative or outside A is NaN.
+ * Returns MXG_OK or an error status.  Deterministic.
+ */
+int fp8gemm_run_grouped(const uint8_t *A, const float *scaleA, int64_t rowsA,
+                        const uint8_t *B, const float *scaleB, void *C,
+                        int64_t rows, int64_t N, int64_t K, int64_t E,
+                        const int32_t *offsets, const int32_t *index,
+                        int index_div, const float *bias, int act,
+                        int out_type, void *stream);
+
+/*
+ * fp8gemm_weight_grad - gradient of the weights of a product whose activations were
+ * kept as codes: dW[n][k] = sum_m dC[m][n] * x[m][k], x[m][k] = scaleA[m][k / 128]
+ * * A[m][k] rounded to bf16 (exact for scales that are powers of two, as
+ * fp8gemm_quantize and rmsnorm_quantize give with pow2).  Sums in fp32 on the
+ * bf16 MFMA, rounded once to out_type; dC in fp16 or fp32 goes in as the sum of two
+ * bf16 values (exact for fp16 of at least 2^-10, else within 2^-17 of a value).
+ * The gradient is that of the dequantized activations.
+ *
+ *   dC         device, M x N elements of c_type, 16-byte aligned
+ *   A, scaleA  as for fp8gemm_run
+ *   dW         device, N x K elements of out_type, 16-byte aligned; overwritten
+ *   M          1 .. MXG_MAX_SLOTS;  N, K as for fp8gemm_run
+ *   workspace  device, fp8gemm_weight_grad_workspace(M, N, K, 1) bytes, 16-byte
+ *              aligned; NULL when that is 0.  Holds nothing between calls.
+ * Returns MXG_OK or an error status.  Deterministic.  The workspace's size is -1
+ * for arguments that the call refuses.
+ */
+int64_t fp8gemm_weight_grad_workspace(int64_t M, int64_t N, int64_t K, int64_t E);
+int fp8gemm_weight_grad(const void *dC, int c_type, int64_t M, int64_t N,
+                        const uint8_t *A, const float *scaleA, int64_t K,
+                        void *dW, int out_type, void *workspace, void *stream);
+
+/*
+ * fp8gemm_weight_grad_grouped - the same for the weights of E experts: dW[e] is the
+ * sum over rows offsets[e] .. offsets[e+1]-1 of dC (zeros where there are none),
+ * row p of dC against row index[p] / index_div of A (index == NULL: row p).  A row
+ * whose index is negative or outside A counts as a row of NaNs, as its result is.
+ *
+ *   dC         rows x N;  A, scaleA  rowsA rows;  dW  E x N x K
+ *   rows, rowsA, E, offsets, index, index_div  as for fp8gemm_run_grouped
+ *   workspace  fp8gemm_weight_grad_workspace(rows, N, K, E) bytes
+ */
+int fp8gemm_weight_grad_grouped(const void *dC, int c_type, int64_t rows,
+                                int64_t N, const uint8_t *A,
+                                const float *scaleA, int64_t rowsA, int64_t K,
+                                int64_t E, const int32_t *offsets,
+                                const int32_t *index, int index_div, void *dW,
+                                int out_type, void *workspace, void *stream);
+
+/* Codes that rmsnorm_quantize writes. */
+#define MXG_QUANT_NONE 0      /* none */
+#define MXG_QUANT_INT8 1      /* int8, S: rows fp32 (int8gemm_quantize) */
+#define MXG_QUANT_FP8 2       /* E4M3, S: rows x KB fp32 (fp8gemm_quantize) */
+#define MXG_QUANT_FP8_POW2 3  /* the same with pow2 */
+#define MXG_QUANT_MXFP8 4     /* E4M3, S: rows x K/32 bytes (mxgemm_quantize) */
+
+/*
+ * rmsnorm_quantize - root-mean-square norm of rows, with a residual added before
+ * it and codes for the products as its output:
+ *   H    = X + R in fp32, rounded to their type (R == NULL: H is X);
+ *   rstd = 1 / sqrt(sum_k H[r][k]^2 / K + eps);
+ *   y    = (H * rstd) * W in fp32;
+ *   Q, S = codes of y by the rule of the quantizer that `quant` names, from the fp32
+ *          values; Y = y rounded to the rows' type.
+ *
+ *   X, R   device, rows x K elements of `type`, 16-byte aligned; R may be NULL
+ *   W      device, K elements of w_type, 16-byte aligned
+ *   rows   1 .. MXG_MAX_SLOTS;  K 16 .. MXG_MAX_DIM, K % 16 == 0 (MXG_QUANT_MXFP8:
+ *          K % 32 == 0);  eps >= 0, finite
+ *   H      device, rows x K of `type`, 16-byte aligned (written; may be X or R);
+ *          NULL if and only if R is
+ *   Y      device, rows x K of `type`, 16-byte aligned (written), or NULL
+ *   Q, S   device, Q rows x K bytes, 16-byte aligned, S 4-byte aligned (MXFP8:
+ *          any); NULL for MXG_QUANT_NONE, which takes a Y
+ *   rstd   device, rows fp32, 4-byte aligned (written), or NULL
+ * Returns MXG_OK or an error status.  Deterministic.
+ */
+int rmsnorm_quantize(const void *X, const void *R, int type, const void *W,
+                     int w_type, int64_t rows, int64_t K, float eps, void *H,
+                     void *Y, int quant, uint8_t *Q, void *S, float *rstd,
+                     void *stream);
+
+/*
+ * rmsnorm_backward - gradients of rmsnorm_quantize's y: with hat = H * rstd, g = dY *
+ * W, c = sum_k(g * hat) / K,
+ *   dX = rstd * (g - hat * c) + dH,   dW = sum over rows of dY * hat,
+ * in fp32, dX rounded to `type`.  dX is the gradient of X and of R.  The rounding to
+ * codes counts as the identity.
+ *
+ *   dY, H, dH  device, rows x K of `type`, 16-byte aligned; dH (the gradient that H
+ *              gets besides) may be NULL
+ *   W, w_type, rows, K  as for rmsnorm_quantize;  rstd  device, rows fp32
+ *   dX         device, rows x K of `type`, 16-byte aligned (written; may be dY or dH)
+ *   dW         device, K fp32, 16-byte aligned (written)
+ *   workspace  device, rmsnorm_backward_workspace(rows, K) bytes, 16-byte aligned.
+ *              Holds nothing between calls.
+ * Returns MXG_OK or an error status.  Deterministic.
+ */
+int64_t rmsnorm_backward_workspace(int64_t rows, int64_t K);
+int rmsnorm_backward(const void *dY, const void *H, const void *dH, int type,
+                     const void *W, int w_type, const float *rstd, int64_t rows,
+                     int64_t K, void *dX, float *dW, void *workspace,
+                     void *stream);
 
 #ifdef __cplusplus
 }
