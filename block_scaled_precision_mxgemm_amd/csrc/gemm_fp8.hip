@@ -6,16 +6,19 @@
 // is added to the fp32 accumulator by an fma, block after block.
 //
 // By expert, rows and offsets are as in gemm_int8.hip.
+#include "fp8_choice.h"
 #include "mxg_fp8.h"
 #include "mxg_internal.h"
 
 namespace mxg {
 namespace {
 
-// 64 x 64 tiles, 4 waves of 32 x 32, a block of 128 k at a time through
-// registers.
+// ---- gathered rows of an A of 4 GiB and more --------------------------------
+//
+// The one case that the kernels below, whose gathered rows are 32-bit offsets,
+// do not take.  64 x 64 tiles, 4 waves of 32 x 32, a block of 128 k at a time
+// through registers.
 constexpr int kBM = 64, kBN = 64, kBK = 128;
-constexpr int kCus = 256;
 
 __global__ __launch_bounds__(256) void fp8_tile_kernel(F8Args a, int tiles_n) {
   __shared__ __attribute__((aligned(16))) uint8_t sa[kBM * kBK], sb[kBN * kBK];
@@ -81,7 +84,601 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(F8Args a, int tiles_n) {
   }
 }
 
-hipError_t launch_tile(const F8Args& a, hipStream_t stream) {
+// scales that a whole wave shares, by scalar loads
+typedef __attribute__((address_space(4))) float float_const;
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ring_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// A block's partial sum, kept in program order; whoever reads it places the
+// wait states.
+__device__ __forceinline__ void mfma_start(v4f& p, const v8i& x, const v8i& y) {
+  asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, 0" : "=&v"(p) : "v"(x), "v"(y));
+}
+
+// A lane's number or address, in a form that the compiler cannot see through:
+// what is derived from it is formed where it is used instead of ahead of the tile loop
+// and held in registers across it.
+__device__ __forceinline__ int opaque(int lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+__device__ __forceinline__ v8i fragment(const uint8_t* p, int sw) {
+  return join(*reinterpret_cast<const v4i*>(p + sw), *reinterpret_cast<const v4i*>(p + (sw ^ 64)));
+}
+
+// ---- large tiles ------------------------------------------------------------
+//
+// WM x WN waves, two per SIMD, each with a TM x TN part of the tile in 16 x 16
+// fragments.  LDS holds two blocks of 128 k of A and B (whole 128-byte lines of
+// each row) and of A's scales, filled by direct global -> LDS copies; B's scale
+// of a wave's columns, one of 128 x 128, is a scalar.
+//
+// A wave goes through a block column by column of fragments: FM MFMAs, each
+// behind the 4 fmas that add the sum which its registers still hold (that of 4
+// MFMAs before), times its row's scale, to the accumulators.  With the s_nop 18
+// wait states lie between an MFMA and the fmas on its result.  The fmas take
+// half of the MFMAs' time on the vector unit, beside them.  The fragments of B are read two columns
+// ahead, those of A for the next block behind the last column's MFMAs.  One
+// barrier per block, behind the column before the last: by then the block has
+// been read by all, and the next one has arrived; the copies of the block after
+// that go into the buffer that is left.
+//
+// A workgroup takes tile after tile; the first block of the next tile is copied
+// while the last one of the present tile is multiplied, and the output goes
+// through the last block's buffer.
+template <int BM_, int BN_, int WM_, int WN_>
+struct F8Cfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int NW = WM * WN;                // waves
+  static constexpr int TM = BM / WM, TN = BN / WN;  // a wave's part of the tile
+  static constexpr int FM = TM / 16, FN = TN / 16;  // and its fragments
+  static constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KiB copies of a wave and block
+  static constexpr int COPIES = CA + CB + 1;
+  static constexpr int LAG = FM >= 4 ? 1 : 4 / FM;  // columns between an MFMA and its fmas
+  static constexpr int OFF_B = BM * 128, STAGE = (BM + BN) * 128;
+  static constexpr int OFF_S = 2 * STAGE, SZS = BM * 4;  // A's scales of a block
+  static constexpr int LDS = OFF_S + 2 * SZS;
+  static constexpr int PER_CU = LDS > 80 * 1024 ? 1 : 2;  // workgroups
+  static_assert(LDS <= 160 * 1024, "fits the 160 KiB LDS of a gfx950 CU");
+  static_assert(CA * NW * 8 == BM && CB * NW * 8 == BN && NW % 2 == 0 && NW * 64 >= BM, "copies split evenly over the waves");
+  static_assert(TN == 64 || TN == 128, "output staging; one scale of B for a wave");
+  static_assert(STAGE >= NW * 4096, "output staging");
+};
+
+template <class T, bool GATHER>
+struct F8Ring {
+  static constexpr int FM = T::FM, FN = T::FN;
+
+  static __device__ __forceinline__ void run(const F8Args& a, int tiles_n) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / T::WN, wn = wave % T::WN;
+    const int g = lane >> 4, r = lane & 15;
+    const int K = a.K, S = a.KB, tail = K & 127;
+
+    // A copy moves 8 rows of 128 bytes: lane l fetches row l / 8, and of its
+    // chunks the one that the swizzle puts at place l % 8 (the row's swizzle
+    // depends on the parity of the copy's number, which is the wave's).
+    constexpr int kRsrcWord3 = 0x00020000;
+    // All of an offset is the lane's, so that the bounds check of the buffers (which
+    // end with the tile's rows) sees it: rows past the tile's end read as zeros.
+    const int c16 = ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
+    const uint32_t off0 = (uint32_t)((lane >> 3) * K + c16);
+    const float_const* sb_at = nullptr;  // B's scales of this wave's columns
+    __amdgpu_buffer_rsrc_t rs_a, rs_b, rs_s;
+    const ExpertScan scan = scan_experts(a, T::BM, lane);
+    auto find = [&](int64_t tile, ExpertTile& t) {
+      if (!pick_tile(a, scan, T::BM, tiles_n, tile, opaque(threadIdx.x & 63), t)) return false;
+      // as scalars
+      t.row0 = __builtin_amdgcn_readfirstlane((int)t.row0);
+      t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+      t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+      t.tn = __builtin_amdgcn_readfirstlane(t.tn);
+      return true;
+    };
+    // what the copies of a tile read
+    auto open = [&](const ExpertTile& t) {
+      const int n0 = t.tn * T::BN, cols = min(T::BN, a.N - n0);
+      if constexpr (GATHER) {
+        rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)a.A, 0, (int)(uint32_t)(a.rows_a * K), kRsrcWord3);
+        rs_s = __builtin_amdgcn_make_buffer_rsrc((void*)a.SA, 0, (int)(uint32_t)(a.rows_a * S * 4), kRsrcWord3);
+      } else {
+        rs_a = __builtin_amdgcn_make_buffer_rsrc((void*)(a.A + t.row0 * K), 0, t.rows * K, kRsrcWord3);
+        rs_s = __builtin_amdgcn_make_buffer_rsrc((void*)(a.SA + t.row0 * S), 0, t.rows * S * 4, kRsrcWord3);
+      }
+      rs_b = __builtin_amdgcn_make_buffer_rsrc((void*)(a.B + ((int64_t)t.expert * a.N + n0) * K), 0, cols * K,
+                                               kRsrcWord3);
+      // columns past N (a wave may have no others) take the last block's scales
+      sb_at = (const float_const*)(a.SB + ((int64_t)t.expert * a.NB + min((n0 + wn * T::TN) >> 7, a.NB - 1)) * S);
+    };
+    // Places in A and in its scales of the rows that this lane copies.  By index
+    // they are looked up in two steps: the indices are loaded long before they
+    // are needed.
+    struct Rows {
+      uint32_t a[GATHER ? T::CA : 1], s;
+    };
+    auto load_rows = [&](const ExpertTile& t) {
+      Rows w;
+      if constexpr (GATHER) {
+        const int lane = opaque(threadIdx.x & 63);
+        const int32_t* index = a.index + t.row0;
+#pragma unroll
+        for (int u = 0; u < T::CA; u++) w.a[u] = (uint32_t)index[min((wave + T::NW * u) * 8 + (lane >> 3), t.rows - 1)];
+        w.s = (uint32_t)index[min((wave * 64 + lane) % T::BM, t.rows - 1)];
+      }
+      return w;
+    };
+    auto places = [&](Rows w) {
+      if constexpr (GATHER) {
+        const int lane = opaque(threadIdx.x & 63);
+        const int c16 = ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
+        // a row outside A is read as row 0 (its results are NaN)
+#pragma unroll
+        for (int u = 0; u < T::CA; u++) w.a[u] = (uint32_t)(max(row_of_index(a, (int)w.a[u]), (int64_t)0) * K) + c16;
+        w.s = (uint32_t)(max(row_of_index(a, (int)w.s), (int64_t)0) * S * 4);
+      } else {
+        w.a[0] = off0;
+        w.s = (uint32_t)((wave * 64 + lane) % T::BM * S * 4);
+      }
+      return w;
+    };
+    // copy u of COPIES of a block into buffer `buf`
+    auto copy = [&](const Rows& w, int slice, int buf, int u) {
+      uint8_t* to = smem + buf * T::STAGE;
+      if (u < T::CA) {
+        const int rows = (wave + T::NW * u) * 8;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, (lds_void*)(to + rows * 128), 16,
+                                                 w.a[GATHER ? u : 0] + (GATHER ? 0 : rows * K) + slice * 128, 0, 0, 0);
+      } else if (u < T::CA + T::CB) {
+        const int rows = (wave + T::NW * (u - T::CA)) * 8;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, (lds_void*)(to + T::OFF_B + rows * 128), 16,
+                                                 off0 + rows * K + slice * 128, 0, 0, 0);
+      } else {
+        // the scales of 64 rows (several waves bring the same ones)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rs_s, (lds_void*)(smem + T::OFF_S + buf * T::SZS + (wave * 64 % T::BM) * 4), 4, w.s + slice * 4, 0, 0, 0);
+      }
+    };
+    auto copy_all = [&](const Rows& w, int slice, int buf) {
+#pragma unroll
+      for (int u = 0; u < T::COPIES; u++) copy(w, slice, buf, u);
+    };
+    // In a partial last block the chunks past K that this lane fetched are other
+    // rows' codes: zeros over A's and B's.
+    auto zero_tail = [&](int buf) {
+      const int lane = opaque(threadIdx.x & 63);
+      const int c16 = ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
+      if (c16 >= tail) {
+        uint8_t* to = smem + buf * T::STAGE + wave * 1024 + lane * 16;
+#pragma unroll
+        for (int u = 0; u < T::CA; u++) *reinterpret_cast<v4i*>(to + T::NW * u * 1024) = v4i{0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < T::CB; u++) *reinterpret_cast<v4i*>(to + T::OFF_B + T::NW * u * 1024) = v4i{0, 0, 0, 0};
+      }
+    };
+
+    int64_t tile = blockIdx.x;
+    ExpertTile t;
+    if (!find(tile, t)) return;
+    open(t);
+    Rows w = places(load_rows(t));
+    int buf = 0;  // of the block at hand
+    copy_all(w, 0, 0);
+    wait_vm<0>();
+    if (tail != 0 && S == 1) zero_tail(0);
+    // lane address of a fragment's first half; the second half's is that with
+    // bit 6 flipped, by the swizzle
+    const int sw = r * 128 + ((g ^ ((r >> 1) & 7)) << 4);
+    const int la = wm * T::TM * 128, lb = T::OFF_B + wn * T::TN * 128, ls = T::OFF_S + (wm * T::TM + r) * 4;
+
+    for (;;) {
+      // this wave's copies of block 0 are there; the last tile's output is read back
+      ring_barrier();
+      if (S > 1) copy_all(w, 1, buf ^ 1);
+      // the next tile, found here where few registers are in use
+      ExpertTile following;
+      Rows w_next;
+      tile += gridDim.x;
+      const bool next = find(tile, following);
+      if (next) w_next = load_rows(following);
+      v4f acc[FM][FN];
+#pragma unroll
+      for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++) acc[i][j] = v4f{0, 0, 0, 0};
+      v8i fa[FM], fb[2];
+      v4f p[T::LAG][FM];
+      float sc[FM], sa[FM];  // scales of the sums at hand; A's of the block at hand
+      float sb = sb_at[0];
+      {
+        const uint8_t* from = smem + buf * T::STAGE;
+#pragma unroll
+        for (int f = 0; f < FM; f++) fa[f] = fragment(from + la + f * 2048, sw);
+        fb[0] = fragment(from + lb, sw);
+        fb[1] = fragment(from + lb + 2048, sw);
+#pragma unroll
+        for (int f = 0; f < FM; f++) {
+          sa[f] = *reinterpret_cast<const float*>(smem + ls + buf * T::SZS + f * 64);
+          sc[f] = 0.0f;
+          // added with scale 0 ahead of the first columns
+#pragma unroll
+          for (int l = 0; l < T::LAG; l++) p[l][f] = v4f{0, 0, 0, 0};
+        }
+      }
+      for (int s = 0; s < S; s++) {
+        // (what is read for a block past the last one is not used)
+        const uint8_t* here = smem + buf * T::STAGE + lb;
+        float sb_next = sb_at[min(s + 1, S - 1)];
+#pragma unroll
+        for (int j = 0; j < FN; j++) {
+          const bool last = j == FN - 1;
+          if (j == T::LAG) {
+#pragma unroll
+            for (int u = 0; u < FM; u++) sc[u] = sa[u] * sb;
+          }
+#pragma unroll
+          for (int u = 0; u < FM; u++) {
+            // the sums of the column LAG before; ahead of column LAG those of the block before
+            v4f& c = acc[u][(j + FN - T::LAG) % FN];
+            v4f& q = p[j % T::LAG][u];
+            asm volatile("s_nop 2" : "+v"(q));
+#pragma unroll
+            for (int x = 0; x < 4; x++) c[x] = fmaf(q[x], sc[u], c[x]);
+            asm volatile("" : "+v"(c));  // here, not behind the next branch
+            __builtin_amdgcn_sched_barrier(0);
+            mfma_start(q, fb[j & 1], fa[u]);
+            if (last) fa[u] = fragment(smem + (buf ^ 1) * T::STAGE + la + u * 2048, sw);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (j + 2 < FN) fb[j & 1] = fragment(here + (j + 2) * 2048, sw);
+          if (j == FN - 2) {
+            wait_vm<0>();
+            if (tail != 0 && s + 2 == S) zero_tail(buf ^ 1);
+            ring_barrier();
+            asm volatile("" : "+s"(sb_next));  // loaded by now
+            if (s + 2 < S) {
+              copy_all(w, s + 2, buf);
+            } else if ((s + 2 == S || S == 1) && next) {
+              open(following);
+              if (GATHER) w = places(w_next);
+              copy_all(w, 0, S == 1 ? buf ^ 1 : buf);
+            }
+            fb[0] = fragment(smem + (buf ^ 1) * T::STAGE + lb, sw);
+          }
+          if (last) fb[1] = fragment(smem + (buf ^ 1) * T::STAGE + lb + 2048, sw);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int u = 0; u < FM; u++) sa[u] = *reinterpret_cast<const float*>(smem + ls + (buf ^ 1) * T::SZS + u * 64);
+        sb = sb_next;
+        buf ^= 1;
+      }
+      asm volatile("s_nop 15\n\ts_nop 2" ::: "memory");
+#pragma unroll
+      for (int u = 0; u < FM; u++) {
+#pragma unroll
+        for (int l = 0; l < T::LAG; l++) {
+          asm volatile("" : "+v"(p[l][u]));
+          v4f& c = acc[u][FN - T::LAG + l];
+#pragma unroll
+          for (int x = 0; x < 4; x++) c[x] = fmaf(p[l][u][x], sc[u], c[x]);
+        }
+      }
+      // the buffer of the last block, which all have read
+      uint8_t* cst = smem + (buf ^ 1) * T::STAGE + wave * 4096;
+      if (t.rows != T::BM || (t.tn + 1) * T::BN > a.N)
+        store<-1, 0>(a, t, acc, cst, wm, wn);
+      else if (a.e.act == kActGelu)
+        store_typed<kActGelu>(a, t, acc, cst, wm, wn);
+      else
+        store_typed<kActNone>(a, t, acc, cst, wm, wn);
+      if (!next) return;
+      t = following;
+      if (tail != 0 && S == 1) zero_tail(buf);
+    }
+  }
+
+  // Output: a lane holds 4 columns of row r of each fragment.  16 rows x 64
+  // columns at a time go through 4 KiB of LDS and come back with consecutive
+  // lanes on consecutive columns, so that the stores fill whole lines.
+  // OUT >= 0: all rows and columns of the tile exist, and type and activation
+  // are known here; OUT < 0: the general form.
+  template <int OUT, int ACT>
+  static __device__ __forceinline__ void store(const F8Args& a, const ExpertTile& t, v4f (&acc)[FM][FN], uint8_t* cst,
+                                               int wm, int wn) {
+    constexpr bool FULL = OUT >= 0;
+    Epi e = a.e;
+    if (FULL) {
+      e.out = OUT;
+      e.act = ACT;
+    }
+    const int lane = opaque(threadIdx.x & 63);
+    const int rr = lane >> 4, cc = lane & 15;  // in a fragment: columns 4 rr, row cc; read back: row of 4, chunk
+    const int64_t eb = (int64_t)t.expert * a.N;
+    constexpr int NH = T::TN / 64;
+    const int n0 = t.tn * T::BN + wn * T::TN + cc * 4;
+    v4f bias[NH];
+#pragma unroll
+    for (int h = 0; h < NH; h++) {
+      const int nc = n0 + h * 64;
+      // -0 leaves every sum as it is
+      bias[h] = v4f{-0.f, -0.f, -0.f, -0.f};
+      if (a.e.bias != nullptr) {
+        if (FULL)
+          bias[h] = *reinterpret_cast<const v4f_any*>(a.e.bias + eb + nc);
+        else
+          bias[h] = load_columns(a.e.bias + eb, nc, a.N, 0.0f);
+      }
+    }
+    bool out[FM];  // rows of A that do not exist
+#pragma unroll
+    for (int u = 0; u < FM; u++) {
+      const int row = wm * T::TM + 16 * u + cc;
+      out[u] = GATHER && (FULL || row < t.rows) && a_row(a, t.row0 + row) < 0;
+    }
+    // the next tile's first copies are older than these loads: none of them
+    // is in flight behind this, and the stores are not waited for with them
+    wait_vm<0>();
+#pragma unroll
+    for (int u = 0; u < FM; u++) {
+#pragma unroll
+      for (int h = 0; h < NH; h++) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          v4f v = acc[u][h * 4 + j];
+          if (GATHER) {
+#pragma unroll
+            for (int x = 0; x < 4; x++) v[x] = out[u] ? __builtin_nanf("") : v[x];
+          }
+          *reinterpret_cast<v4f*>(cst + cc * 256 + (((j * 4 + rr) ^ cc) << 4)) = v;
+        }
+        wave_sync();
+#pragma unroll FULL ? 4 : 1
+        for (int q = 0; q < 4; q++) {
+          const int br = q * 4 + rr;
+          v4f v = *reinterpret_cast<const v4f*>(cst + br * 256 + ((cc ^ br) << 4));
+          const int orow = wm * T::TM + 16 * u + br, nc = n0 + h * 64;
+          if (FULL || (orow < t.rows && nc < a.N)) {
+            v += bias[h];
+            if (e.act == kActGelu) {
+#pragma unroll
+              for (int x = 0; x < 4; x++) v[x] = gelu(v[x]);
+            }
+            store_columns<true>(e, a.N, t.row0 + orow, nc, v);
+          }
+        }
+        wave_sync();
+      }
+    }
+  }
+
+  template <int ACT>
+  static __device__ __forceinline__ void store_typed(const F8Args& a, const ExpertTile& t, v4f (&acc)[FM][FN], uint8_t* cst,
+                                                     int wm, int wn) {
+    if (a.e.out == kOutF32)
+      store<kOutF32, ACT>(a, t, acc, cst, wm, wn);
+    else if (a.e.out == kOutBF16)
+      store<kOutBF16, ACT>(a, t, acc, cst, wm, wn);
+    else
+      store<kOutF16, ACT>(a, t, acc, cst, wm, wn);
+  }
+};
+
+template <class T, bool GATHER>
+__global__ __launch_bounds__(T::NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void fp8_ring_kernel(F8Args a,
+                                                                                                     int tiles_n) {
+  F8Ring<T, GATHER>::run(a, tiles_n);
+}
+
+template <class T>
+hipError_t launch_ring(const F8Args& a, hipStream_t stream) {
+  const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
+  const int64_t tiles = tiles_n * expert_tiles_m(a, T::BM);
+  if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e != hipSuccess) return e;
+  const int64_t most = (int64_t)cus * T::PER_CU;
+  const dim3 grid((unsigned)(tiles < most ? tiles : most)), block(T::NW * 64);
+  if (a.index != nullptr)
+    hipLaunchKernelGGL((fp8_ring_kernel<T, true>), grid, block, 0, stream, a, (int)tiles_n);
+  else
+    hipLaunchKernelGGL((fp8_ring_kernel<T, false>), grid, block, 0, stream, a, (int)tiles_n);
+  return hipGetLastError();
+}
+
+// ---- few rows ---------------------------------------------------------------
+//
+// CW x KW waves on a tile of 16 MB rows x 16 CW columns: each wave has 16 of the
+// columns and every KW-th block of 128 k (a line of each row).  A stage of LDS
+// holds KW blocks, one for each group of waves, and each wave's copy of the
+// scales of A for its block; D stages are in flight or in use, so that a CU
+// keeps most of its LDS of memory requests going, which is what bounds such
+// products.  The groups' sums are added through LDS at the end.
+template <int MB_, int CW_, int KW_, int D_>
+struct F8Few {
+  static constexpr int MB = MB_, CW = CW_, KW = KW_, D = D_;
+  static constexpr int BM = 16 * MB, BN = 16 * CW, NW = CW * KW;
+  static constexpr int PART = (BM + BN) * 128, OFF_S = KW * PART, STAGE = OFF_S + NW * 256, LDS = D * STAGE;
+  // copies of 8 rows: RG for a block, NC for a stage, of which a wave issues
+  // MIN or (the first REM waves) one more; and one of scales
+  static constexpr int RG = (BM + BN) / 8, NC = RG * KW, MIN = NC / NW, REM = NC % NW, MAX = MIN + (REM ? 1 : 0);
+  static_assert(LDS <= 160 * 1024 && LDS >= NW * MB * 1024 && D >= 3, "stages, and the sums of all waves");
+  static_assert(BM <= 64 && 128 % BN == 0, "a wave's scales; one scale of B for a tile");
+};
+
+template <class T, bool GATHER>
+__global__ __launch_bounds__(T::NW * 64) void fp8_few_kernel(F8Args a, int tiles_n) {
+  constexpr int MB = T::MB, CW = T::CW, KW = T::KW, NW = T::NW, D = T::D;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cw = wave % CW, kw = wave / CW;
+  const int g = lane >> 4, r = lane & 15;
+  ExpertTile t;
+  if (!find_tile(a, T::BM, tiles_n, blockIdx.x, lane, t)) return;
+  const int K = a.K, n0 = t.tn * T::BN, cols = min(T::BN, a.N - n0);
+  const int S = a.KB, tail = K & 127;  // blocks
+  const int I = (S + KW - 1) / KW;     // stages
+
+  constexpr int kRsrcWord3 = 0x00020000;
+  const auto rs_a = GATHER
+                        ? __builtin_amdgcn_make_buffer_rsrc((void*)a.A, 0, (int)(uint32_t)(a.rows_a * K), kRsrcWord3)
+                        : __builtin_amdgcn_make_buffer_rsrc((void*)(a.A + t.row0 * K), 0, t.rows * K, kRsrcWord3);
+  const auto rs_s = GATHER
+                        ? __builtin_amdgcn_make_buffer_rsrc((void*)a.SA, 0, (int)(uint32_t)(a.rows_a * S * 4), kRsrcWord3)
+                        : __builtin_amdgcn_make_buffer_rsrc((void*)(a.SA + t.row0 * S), 0, t.rows * S * 4, kRsrcWord3);
+  const auto rs_b = __builtin_amdgcn_make_buffer_rsrc((void*)(a.B + ((int64_t)t.expert * a.N + n0) * K), 0, cols * K,
+                                                      kRsrcWord3);
+  const float_const* sb_at = (const float_const*)(a.SB + ((int64_t)t.expert * a.NB + (n0 >> 7)) * S);
+  // Copy u of this wave: rows 8 rg .. of block kp of the stage, A's rows first.
+  // Rows past the end are fetched as the last one, rows outside A as row 0.
+  auto source = [&](int row) -> int64_t {
+    const int at = min(row, t.rows - 1);
+    return GATHER ? max(a_row(a, t.row0 + at), (int64_t)0) : at;
+  };
+  uint32_t off[T::MAX];
+#pragma unroll
+  for (int u = 0; u < T::MAX; u++) {
+    const int rg = (wave + NW * u) % T::RG;
+    const int c16 = ((lane & 7) ^ (4 * (rg & 1) + (lane >> 4))) * 16;
+    const int64_t row = rg < T::BM / 8 ? source(rg * 8 + (lane >> 3)) : min(rg * 8 - T::BM + (lane >> 3), cols - 1);
+    off[u] = (uint32_t)(row * K) + c16;
+  }
+  const uint32_t off_s = (uint32_t)(source(lane % T::BM) * S * 4);
+  auto issue = [&](int i, int stage) {
+#pragma unroll
+    for (int u = 0; u < T::MAX; u++) {
+      const int q = wave + NW * u;
+      if (u < T::MIN || wave < T::REM) {
+        const int kp = q / T::RG, rg = q % T::RG;
+        const int slice = min(i * KW + kp, S - 1);  // past K: not used
+        uint32_t o = off[u];
+        if (tail != 0 && slice == S - 1) {
+          // chunks past K are fetched as the block's first one
+          const int c16 = ((lane & 7) ^ (4 * (rg & 1) + (lane >> 4))) * 16;
+          if (c16 >= tail) o -= c16;
+        }
+        lds_void* to = (lds_void*)(smem + stage * T::STAGE + kp * T::PART + rg * 1024);
+        if (rg < T::BM / 8)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, to, 16, o, slice * 128, 0, 0);
+        else
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, to, 16, o, slice * 128, 0, 0);
+      }
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_s, (lds_void*)(smem + stage * T::STAGE + T::OFF_S + wave * 256), 4, off_s,
+                                             min(i * KW + kw, S - 1) * 4, 0, 0);
+  };
+  v4f acc[MB];
+#pragma unroll
+  for (int i = 0; i < MB; i++) acc[i] = v4f{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < D - 1; i++)
+    if (i < I) issue(i, i);
+  const int sw = r * 128 + ((g ^ ((r >> 1) & 7)) << 4);
+  int stage = 0;
+  float sb = sb_at[min(kw, S - 1)];
+  for (int i = 0; i < I; i++) {
+    // this wave's copies of stage i are there, then everybody's; the stage
+    // before has been read by all
+    if (i + D - 2 >= I)
+      wait_vm<0>();
+    else if (wave < T::REM)
+      wait_vm<(D - 2) * (T::MAX + 1)>();
+    else
+      wait_vm<(D - 2) * (T::MIN + 1)>();
+    ring_barrier();
+    if (i + D - 1 < I) issue(i + D - 1, stage == 0 ? D - 1 : stage - 1);
+    const int slice = i * KW + kw;
+    const float sb_next = sb_at[min(slice + KW, S - 1)];
+    if (slice < S) {
+      const uint8_t* pa = smem + stage * T::STAGE + kw * T::PART;
+      const uint8_t* ps = smem + stage * T::STAGE + T::OFF_S + wave * 256 + r * 4;
+      const v8i fb = fragment(pa + T::BM * 128 + cw * 2048, sw);
+      // codes past K count as zeros
+      const bool lo = tail == 0 || slice != S - 1 || g * 16 < tail, hi = tail == 0 || slice != S - 1 || 64 + g * 16 < tail;
+#pragma unroll
+      for (int u = 0; u < MB; u++) {
+        v8i fa = fragment(pa + u * 2048, sw);
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          fa[x] = lo ? fa[x] : 0;
+          fa[4 + x] = hi ? fa[4 + x] : 0;
+        }
+        const float s = *reinterpret_cast<const float*>(ps + u * 64) * sb;
+        const v4f p = mfma_block(fb, fa);
+#pragma unroll
+        for (int x = 0; x < 4; x++) acc[u][x] = fmaf(p[x], s, acc[u][x]);
+      }
+    }
+    sb = sb_next;
+    stage = stage == D - 1 ? 0 : stage + 1;
+  }
+  // sums of the KW groups, a fragment per wave at a time
+  constexpr int NF = MB * CW;
+  v4f* part = reinterpret_cast<v4f*>(smem);  // [KW][NF][64]
+  ring_barrier();
+#pragma unroll
+  for (int u = 0; u < MB; u++) part[(kw * NF + cw * MB + u) * 64 + lane] = acc[u];
+  __syncthreads();
+  for (int f = wave; f < NF; f += NW) {
+    v4f sum = part[f * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < KW; w++) sum += part[(w * NF + f) * 64 + lane];
+    const int row = 16 * (f % MB) + r, n = n0 + 16 * (f / MB) + 4 * g;
+    if (row < t.rows && n < a.N) {
+      const int64_t m = t.row0 + row;
+      if (GATHER && a_row(a, m) < 0) {
+        const float nan = __builtin_nanf("");
+        sum = v4f{nan, nan, nan, nan};
+      }
+      f8_store4<false>(a, t.expert, m, n, sum);
+    }
+  }
+}
+
+template <class T>
+hipError_t launch_few(const F8Args& a, hipStream_t stream) {
+  const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
+  const int64_t tiles = tiles_n * expert_tiles_m(a, T::BM);
+  if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)tiles), block(T::NW * 64);
+  if (a.index != nullptr)
+    hipLaunchKernelGGL((fp8_few_kernel<T, true>), grid, block, 0, stream, a, (int)tiles_n);
+  else
+    hipLaunchKernelGGL((fp8_few_kernel<T, false>), grid, block, 0, stream, a, (int)tiles_n);
+  return hipGetLastError();
+}
+
+// ---- launch -----------------------------------------------------------------
+
+using Tile16x16 = F8Few<1, 1, 4, 5>;
+using Tile16x32 = F8Few<1, 2, 4, 3>;
+using Tile32x32 = F8Few<2, 2, 4, 4>;
+using Tile32x64 = F8Few<2, 4, 2, 3>;
+using Tile128x128 = F8Cfg<128, 128, 2, 2>;
+using Tile128x128Eight = F8Cfg<128, 128, 4, 2>;
+using Tile256x128 = F8Cfg<256, 128, 4, 2>;
+using Tile256x256 = F8Cfg<256, 256, 4, 2>;
+
+// variant V of kF8Variants
+template <int V, class T>
+hipError_t launch_variant(const F8Args& a, hipStream_t stream) {
+  static_assert(T::BM == kF8Variants[V].bm && T::BN == kF8Variants[V].bn, "the variant's tile");
+  if constexpr (V < 4)
+    return launch_few<T>(a, stream);
+  else
+    return launch_ring<T>(a, stream);
+}
+
+hipError_t launch_gathered_far(const F8Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + kBN - 1) / kBN;
   const int64_t tiles = tiles_n * expert_tiles_m(a, kBM);
   if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
@@ -96,7 +693,27 @@ hipError_t launch_tile(const F8Args& a, hipStream_t stream) {
 hipError_t launch_fp8(const F8Args& args, hipStream_t stream) {
   F8Args a = args;
   set_division(a);
-  return launch_tile(a, stream);
+  // gathered rows are addressed by 32-bit offsets from A's start
+  if (a.index != nullptr && a.rows_a * a.K >= ((int64_t)1 << 32)) return launch_gathered_far(a, stream);
+  int v = f8_choice(a.M, a.N, a.K, a.offsets == nullptr ? 0 : a.E);
+  switch (v) {
+    case 0:
+      return launch_variant<0, Tile16x16>(a, stream);
+    case 1:
+      return launch_variant<1, Tile16x32>(a, stream);
+    case 2:
+      return launch_variant<2, Tile32x32>(a, stream);
+    case 3:
+      return launch_variant<3, Tile32x64>(a, stream);
+    case 4:
+      return launch_variant<4, Tile128x128Eight>(a, stream);
+    case 5:
+      return launch_variant<5, Tile128x128>(a, stream);
+    case 6:
+      return launch_variant<6, Tile256x128>(a, stream);
+    default:
+      return launch_variant<7, Tile256x256>(a, stream);
+  }
 }
 
 }  // namespace mxg

@@ -53,13 +53,49 @@ __device__ __forceinline__ void tile_order(int bid, int tiles_m, int tiles_n, in
   tn = in / rows;
 }
 
-// Tile `bid` in that order, found by a wave (every lane gets it); false if
-// there is none.  By expert, each lane takes a run of experts and the lane
-// whose run holds the tile passes it on.  The offsets count as kept inside
-// 0 .. M and never falling (each at least the largest before it), so that
-// whatever they hold, no row has two experts.
+// The experts' rows as the lanes of a wave hold them: each lane has a run of
+// `per` experts.  The offsets count as kept inside 0 .. M and never falling (each
+// at least the largest before it), so that whatever they hold, no row has two
+// experts.
+struct ExpertScan {
+  int first;   // first row of the run
+  int last;    // and the row behind the last one
+  int before;  // tiles of the experts before the run
+  int mine;    // and of the run
+  int total;   // of all
+};
+
 template <class Args>
-__device__ __forceinline__ bool find_tile(const Args& a, int bm, int tiles_n, int64_t bid, int lane, ExpertTile& t) {
+__device__ __forceinline__ ExpertScan scan_experts(const Args& a, int bm, int lane) {
+  ExpertScan s = {0, 0, 0, 0, 0};
+  if (a.offsets == nullptr) return s;
+  const int M = (int)a.M;
+  const int per = (a.E + 63) / 64;
+  const int e0 = lane * per, e1 = min(e0 + per, a.E);
+  // first row of the run: the largest offset up to e0
+  int top = 0;
+  for (int e = e0; e < e1; e++) top = max(top, min(a.offsets[e + 1], M));
+  if (lane == 0) top = max(top, min(a.offsets[0], M));
+  top = wave_scan<true>(top);
+  s.first = __shfl_up(top, 1);
+  if (lane == 0) s.first = max(0, min(a.offsets[0], M));
+  s.last = s.first;
+  for (int e = e0; e < e1; e++) {
+    const int hi = max(s.last, min(a.offsets[e + 1], M));
+    s.mine += (hi - s.last + bm - 1) / bm;
+    s.last = hi;
+  }
+  s.before = wave_scan<false>(s.mine);
+  s.total = __builtin_amdgcn_readlane(s.before, 63);
+  s.before -= s.mine;
+  return s;
+}
+
+// Tile `bid` in the order above (every lane gets it); false if there is none.
+// By expert, the lane whose run holds the tile passes it on.
+template <class Args>
+__device__ __forceinline__ bool pick_tile(const Args& a, const ExpertScan& s, int bm, int tiles_n, int64_t bid, int lane,
+                                          ExpertTile& t) {
   const int M = (int)a.M;
   int tm;
   if (a.offsets == nullptr) {
@@ -71,42 +107,31 @@ __device__ __forceinline__ bool find_tile(const Args& a, int bm, int tiles_n, in
     t.expert = 0;
     return true;
   }
+  if (bid >= (int64_t)s.total * tiles_n) return false;
+  tile_order((int)bid, s.total, tiles_n, tm, t.tn);
   const int per = (a.E + 63) / 64;
-  const int e0 = lane * per, e1 = min(e0 + per, a.E);
-  // first row of the run: the largest offset up to e0
-  int top = 0;
-  for (int e = e0; e < e1; e++) top = max(top, min(a.offsets[e + 1], M));
-  if (lane == 0) top = max(top, min(a.offsets[0], M));
-  top = wave_scan<true>(top);
-  int first = __shfl_up(top, 1);
-  if (lane == 0) first = max(0, min(a.offsets[0], M));
-  int mine = 0;
-  int lo = first;
-  for (int e = e0; e < e1; e++) {
-    const int hi = max(lo, min(a.offsets[e + 1], M));
-    mine += (hi - lo + bm - 1) / bm;
-    lo = hi;
-  }
-  int before = wave_scan<false>(mine);
-  const int total = __builtin_amdgcn_readlane(before, 63);
-  if (bid >= (int64_t)total * tiles_n) return false;
-  tile_order((int)bid, total, tiles_n, tm, t.tn);
-  before -= mine;
   int row0 = 0, rows = 0, expert = 0;
-  const bool holds = tm >= before && tm < before + mine;
+  const bool holds = tm >= s.before && tm < s.before + s.mine;
   if (holds) {
-    lo = first;
-    for (int e = e0; e < e1; e++) {
-      const int hi = max(lo, min(a.offsets[e + 1], M));
-      const int n = (hi - lo + bm - 1) / bm;
-      if (tm < before + n) {
-        row0 = lo + (tm - before) * bm;
-        rows = min(hi - row0, bm);
-        expert = e;
-        break;
+    int lo = s.first, before = s.before;
+    if (per == 1) {
+      row0 = lo + (tm - before) * bm;
+      rows = min(s.last - row0, bm);
+      expert = lane;
+    } else {
+      const int e0 = lane * per, e1 = min(e0 + per, a.E);
+      for (int e = e0; e < e1; e++) {
+        const int hi = max(lo, min(a.offsets[e + 1], M));
+        const int n = (hi - lo + bm - 1) / bm;
+        if (tm < before + n) {
+          row0 = lo + (tm - before) * bm;
+          rows = min(hi - row0, bm);
+          expert = e;
+          break;
+        }
+        before += n;
+        lo = hi;
       }
-      before += n;
-      lo = hi;
     }
   }
   const int src = __builtin_ctzll(__ballot(holds));
@@ -116,13 +141,21 @@ __device__ __forceinline__ bool find_tile(const Args& a, int bm, int tiles_n, in
   return true;
 }
 
-// Row of A that row p of C takes; -1 for an index outside A.
 template <class Args>
-__device__ __forceinline__ int64_t a_row(const Args& a, int64_t p) {
-  if (a.index == nullptr) return p;
-  const int i = a.index[p];
+__device__ __forceinline__ bool find_tile(const Args& a, int bm, int tiles_n, int64_t bid, int lane, ExpertTile& t) {
+  return pick_tile(a, scan_experts(a, bm, lane), bm, tiles_n, bid, lane, t);
+}
+
+// Row of A that an index stands for; -1 for one outside A.
+template <class Args>
+__device__ __forceinline__ int64_t row_of_index(const Args& a, int i) {
   const int64_t row = i < 0 ? -1 : (int64_t)(((uint64_t)(uint32_t)i * a.div_mul) >> a.div_shift);
   return row < a.rows_a ? row : -1;
+}
+// Row of A that row p of C takes.
+template <class Args>
+__device__ __forceinline__ int64_t a_row(const Args& a, int64_t p) {
+  return a.index == nullptr ? p : row_of_index(a, a.index[p]);
 }
 
 // A product that is rounded before a sum takes it up (no fma), so that every
