@@ -114,40 +114,59 @@ __device__ __forceinline__ v8i fragment(const uint8_t* p, int sw) {
 // ---- large tiles ------------------------------------------------------------
 //
 // WM x WN waves, two per SIMD, each with a TM x TN part of the tile in 16 x 16
-// fragments.  LDS holds two blocks of 128 k of A and B (whole 128-byte lines of
+// fragments.  LDS holds D blocks of 128 k of A and B (whole 128-byte lines of
 // each row) and of A's scales, filled by direct global -> LDS copies; B's scale
 // of a wave's columns, one of 128 x 128, is a scalar.
 //
 // A wave goes through a block column by column of fragments: FM MFMAs, each
 // behind the 4 fmas that add the sum which its registers still hold (that of 4
 // MFMAs before), times its row's scale, to the accumulators.  With the s_nop 18
-// wait states lie between an MFMA and the fmas on its result.  The fmas take
-// half of the MFMAs' time on the vector unit, beside them.  The fragments of B are read two columns
-// ahead, those of A for the next block behind the last column's MFMAs.  One
-// barrier per block, behind the column before the last: by then the block has
-// been read by all, and the next one has arrived; the copies of the block after
-// that go into the buffer that is left.
+// wait states lie between an MFMA and the fmas on its result.  The fmas run
+// beside the MFMAs: a loop of both on registers reaches 3600 TFLOP/s on random
+// codes, without the fmas 4200.  The fragments of B are read two columns ahead,
+// those of A for the next block behind the last column's MFMAs.
 //
-// A workgroup takes tile after tile; the first block of the next tile is copied
-// while the last one of the present tile is multiplied, and the output goes
-// through the last block's buffer.
-template <int BM_, int BN_, int WM_, int WN_>
+// What bounds the loop is the time from a copy's issue to its arrival (about
+// 1.5 us with the chip full).  A barrier behind the column before the last says
+// that the next block has arrived.  Where D > 2 blocks fit, it also says that the
+// block at hand has been read, and copies of D blocks later take its place.
+// SPLIT (256 x 256, where D = 2): A's fragments are in registers from the
+// start of a block on, and the first half of a wave's columns has been read in its
+// middle.  A barrier there lets the copies of the block after the next go
+// out: A and the first halves into the buffers that are left, the second halves
+// into a third buffer (8192 x 14336 x 4096: 470 us with the copies behind the one
+// barrier).
+//
+// A workgroup takes tile after tile; the first blocks of the next tile are
+// copied while the last ones of the present tile are multiplied, and the output
+// goes through the last block's buffer.
+template <int BM_, int BN_, int WM_, int WN_, int D_, bool SPLIT_ = false>
 struct F8Cfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, D = D_;
+  static constexpr bool SPLIT = SPLIT_;
   static constexpr int NW = WM * WN;                // waves
   static constexpr int TM = BM / WM, TN = BN / WN;  // a wave's part of the tile
   static constexpr int FM = TM / 16, FN = TN / 16;  // and its fragments
   static constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KiB copies of a wave and block
   static constexpr int COPIES = CA + CB + 1;
   static constexpr int LAG = FM >= 4 ? 1 : 4 / FM;  // columns between an MFMA and its fmas
-  static constexpr int OFF_B = BM * 128, STAGE = (BM + BN) * 128;
-  static constexpr int OFF_S = 2 * STAGE, SZS = BM * 4;  // A's scales of a block
-  static constexpr int LDS = OFF_S + 2 * SZS;
+  static constexpr int SZA = BM * 128, SZB = BN * 128, SZH = SZB / 2, SZS = BM * 4;
+  // slot i of A (and in it the output's staging), of B, of B's second halves (SPLIT), of A's scales
+  static constexpr int STEP_A = SPLIT ? SZA : SZA + SZB;
+  static constexpr int OFF_B = SPLIT ? 2 * SZA : SZA, STEP_B = SPLIT ? SZH : SZA + SZB;
+  static constexpr int OFF_H = 2 * SZA + 2 * SZH;
+  static constexpr int OFF_S = SPLIT ? OFF_H + 3 * SZH : D * (SZA + SZB);
+  static constexpr int LDS = OFF_S + D * SZS;
   static constexpr int PER_CU = LDS > 80 * 1024 ? 1 : 2;  // workgroups
+  // column behind which copies are issued, over ISSUE columns; blocks in flight
+  // behind the next one at the barrier before the last column
+  static constexpr int FROM = SPLIT ? FN / 2 - 1 : FN - 2, ISSUE = SPLIT ? 3 : D > 2 ? 2 : 1;
+  static constexpr int NEWER = SPLIT ? 1 : D - 2;
   static_assert(LDS <= 160 * 1024, "fits the 160 KiB LDS of a gfx950 CU");
   static_assert(CA * NW * 8 == BM && CB * NW * 8 == BN && NW % 2 == 0 && NW * 64 >= BM, "copies split evenly over the waves");
   static_assert(TN == 64 || TN == 128, "output staging; one scale of B for a wave");
-  static_assert(STAGE >= NW * 4096, "output staging");
+  static_assert((SPLIT ? SZA : SZA + SZB) >= NW * 4096, "output staging");
+  static_assert(!SPLIT || (D == 2 && NW == 8 && WN == 2 && TN == 128), "halves of B");
 };
 
 template <class T, bool GATHER>
@@ -170,7 +189,6 @@ struct F8Ring {
     // end with the tile's rows) sees it: rows past the tile's end read as zeros.
     const int c16 = ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
     const uint32_t off0 = (uint32_t)((lane >> 3) * K + c16);
-    const float_const* sb_at = nullptr;  // B's scales of this wave's columns
     __amdgpu_buffer_rsrc_t rs_a, rs_b, rs_s;
     const ExpertScan scan = scan_experts(a, T::BM, lane);
     auto find = [&](int64_t tile, ExpertTile& t) {
@@ -194,8 +212,6 @@ struct F8Ring {
       }
       rs_b = __builtin_amdgcn_make_buffer_rsrc((void*)(a.B + ((int64_t)t.expert * a.N + n0) * K), 0, cols * K,
                                                kRsrcWord3);
-      // columns past N (a wave may have no others) take the last block's scales
-      sb_at = (const float_const*)(a.SB + ((int64_t)t.expert * a.NB + min((n0 + wn * T::TN) >> 7, a.NB - 1)) * S);
     };
     // Places in A and in its scales of the rows that this lane copies.  By index
     // they are looked up in two steps: the indices are loaded long before they
@@ -228,59 +244,103 @@ struct F8Ring {
       }
       return w;
     };
-    // copy u of COPIES of a block into buffer `buf`
-    auto copy = [&](const Rows& w, int slice, int buf, int u) {
-      uint8_t* to = smem + buf * T::STAGE;
+    // Slots of a block: `a` of D, and (SPLIT) `h` of 3 for the second halves of B.
+    struct Slot {
+      int a, h;
+    };
+    auto after = [&](Slot x) { return Slot{x.a + 1 == T::D ? 0 : x.a + 1, x.h == 2 ? 0 : x.h + 1}; };
+    // the block D later
+    auto later = [&](Slot x) { return Slot{x.a, x.h == 0 ? 2 : x.h - 1}; };
+    // LDS place of this wave's copy v of B: rows 8 (wave + NW v)
+    auto b_place = [&](Slot x, int v) {
+      if (T::SPLIT) return ((v & 1) ? T::OFF_H + x.h * T::SZH : T::OFF_B + x.a * T::STEP_B) + ((v >> 1) * 8 + wave) * 1024;
+      return T::OFF_B + x.a * T::STEP_B + (wave + T::NW * v) * 1024;
+    };
+    // and of column j of its fragments
+    auto b_column = [&](Slot x, int j) {
+      if (T::SPLIT)
+        return (j >= FN / 2 ? T::OFF_H + x.h * T::SZH : T::OFF_B + x.a * T::STEP_B) + wn * (T::SZH / 2) +
+               j % (FN / 2) * 2048;
+      return T::OFF_B + x.a * T::STEP_B + wn * T::TN * 128 + j * 2048;
+    };
+    // copy u of COPIES of a block
+    auto copy = [&](const Rows& w, int slice, Slot x, int u) {
       if (u < T::CA) {
         const int rows = (wave + T::NW * u) * 8;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, (lds_void*)(to + rows * 128), 16,
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, (lds_void*)(smem + x.a * T::STEP_A + rows * 128), 16,
                                                  w.a[GATHER ? u : 0] + (GATHER ? 0 : rows * K) + slice * 128, 0, 0, 0);
       } else if (u < T::CA + T::CB) {
         const int rows = (wave + T::NW * (u - T::CA)) * 8;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, (lds_void*)(to + T::OFF_B + rows * 128), 16,
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, (lds_void*)(smem + b_place(x, u - T::CA)), 16,
                                                  off0 + rows * K + slice * 128, 0, 0, 0);
       } else {
         // the scales of 64 rows (several waves bring the same ones)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs_s, (lds_void*)(smem + T::OFF_S + buf * T::SZS + (wave * 64 % T::BM) * 4), 4, w.s + slice * 4, 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_s, (lds_void*)(smem + T::OFF_S + x.a * T::SZS + (wave * 64 % T::BM) * 4),
+                                                 4, w.s + slice * 4, 0, 0, 0);
       }
     };
-    auto copy_all = [&](const Rows& w, int slice, int buf) {
+    auto copy_all = [&](const Rows& w, int slice, Slot x) {
 #pragma unroll
-      for (int u = 0; u < T::COPIES; u++) copy(w, slice, buf, u);
+      for (int u = 0; u < T::COPIES; u++) copy(w, slice, x, u);
     };
     // In a partial last block the chunks past K that this lane fetched are other
     // rows' codes: zeros over A's and B's.
-    auto zero_tail = [&](int buf) {
+    auto zero_tail = [&](Slot x) {
       const int lane = opaque(threadIdx.x & 63);
       const int c16 = ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
       if (c16 >= tail) {
-        uint8_t* to = smem + buf * T::STAGE + wave * 1024 + lane * 16;
 #pragma unroll
-        for (int u = 0; u < T::CA; u++) *reinterpret_cast<v4i*>(to + T::NW * u * 1024) = v4i{0, 0, 0, 0};
+        for (int u = 0; u < T::CA; u++)
+          *reinterpret_cast<v4i*>(smem + x.a * T::STEP_A + (wave + T::NW * u) * 1024 + lane * 16) = v4i{0, 0, 0, 0};
 #pragma unroll
-        for (int u = 0; u < T::CB; u++) *reinterpret_cast<v4i*>(to + T::OFF_B + T::NW * u * 1024) = v4i{0, 0, 0, 0};
+        for (int u = 0; u < T::CB; u++) *reinterpret_cast<v4i*>(smem + b_place(x, u) + lane * 16) = v4i{0, 0, 0, 0};
       }
     };
 
     int64_t tile = blockIdx.x;
     ExpertTile t;
     if (!find(tile, t)) return;
-    open(t);
+    // Copies cross from one tile to the next: block v of the present tile is
+    // number v, block v of the next one number S + v.  (Not where a tile has fewer
+    // blocks than LDS holds.)
+    const bool cross = S >= T::D;
+    bool first = true;
     Rows w = places(load_rows(t));
-    int buf = 0;  // of the block at hand
-    copy_all(w, 0, 0);
-    wait_vm<0>();
-    if (tail != 0 && S == 1) zero_tail(0);
+    Slot at = {0, 0};  // of the block at hand
+    int ahead = 0;     // number of the last block whose copies are issued
     // lane address of a fragment's first half; the second half's is that with
     // bit 6 flipped, by the swizzle
     const int sw = r * 128 + ((g ^ ((r >> 1) & 7)) << 4);
-    const int la = wm * T::TM * 128, lb = T::OFF_B + wn * T::TN * 128, ls = T::OFF_S + (wm * T::TM + r) * 4;
+    const int la = wm * T::TM * 128, ls = T::OFF_S + (wm * T::TM + r) * 4;
 
     for (;;) {
-      // this wave's copies of block 0 are there; the last tile's output is read back
-      ring_barrier();
-      if (S > 1) copy_all(w, 1, buf ^ 1);
+      if (!first) ring_barrier();  // the last tile's output is read back
+      if (first || !cross) {
+        open(t);
+        if (!first) w = places(load_rows(t));
+        Slot x = at;
+        ahead = min(T::D, S) - 1;
+        for (int i = 0; i <= ahead; i++) {
+          copy_all(w, i, x);
+          x = after(x);
+        }
+        if (S >= T::D)
+          wait_vm<(T::D - 1) * T::COPIES>();
+        else
+          wait_vm<0>();
+        if (tail != 0 && S == 1) zero_tail(at);
+        ring_barrier();
+      } else {
+        // blocks 0 .. D - 2 are there since the last tile's output
+        Slot x = at;
+#pragma unroll
+        for (int i = 1; i < T::D; i++) x = after(x);
+        copy_all(w, T::D - 1, x);
+        ahead = T::D - 1;
+      }
+      // columns past N (a wave may have no others) take the last block's scales
+      const float_const* sb_at =
+          (const float_const*)(a.SB + ((int64_t)t.expert * a.NB + min((t.tn * T::BN + wn * T::TN) >> 7, a.NB - 1)) * S);
       // the next tile, found here where few registers are in use
       ExpertTile following;
       Rows w_next;
@@ -296,25 +356,23 @@ struct F8Ring {
       v4f p[T::LAG][FM];
       float sc[FM], sa[FM];  // scales of the sums at hand; A's of the block at hand
       float sb = sb_at[0];
-      {
-        const uint8_t* from = smem + buf * T::STAGE;
 #pragma unroll
-        for (int f = 0; f < FM; f++) fa[f] = fragment(from + la + f * 2048, sw);
-        fb[0] = fragment(from + lb, sw);
-        fb[1] = fragment(from + lb + 2048, sw);
+      for (int f = 0; f < FM; f++) fa[f] = fragment(smem + at.a * T::STEP_A + la + f * 2048, sw);
+      fb[0] = fragment(smem + b_column(at, 0), sw);
+      fb[1] = fragment(smem + b_column(at, 1), sw);
 #pragma unroll
-        for (int f = 0; f < FM; f++) {
-          sa[f] = *reinterpret_cast<const float*>(smem + ls + buf * T::SZS + f * 64);
-          sc[f] = 0.0f;
-          // added with scale 0 ahead of the first columns
+      for (int f = 0; f < FM; f++) {
+        sa[f] = *reinterpret_cast<const float*>(smem + ls + at.a * T::SZS + f * 64);
+        sc[f] = 0.0f;
+        // added with scale 0 ahead of the first columns
 #pragma unroll
-          for (int l = 0; l < T::LAG; l++) p[l][f] = v4f{0, 0, 0, 0};
-        }
+        for (int l = 0; l < T::LAG; l++) p[l][f] = v4f{0, 0, 0, 0};
       }
       for (int s = 0; s < S; s++) {
         // (what is read for a block past the last one is not used)
-        const uint8_t* here = smem + buf * T::STAGE + lb;
+        const Slot then = after(at);
         float sb_next = sb_at[min(s + 1, S - 1)];
+        int to_copy = -1;
 #pragma unroll
         for (int j = 0; j < FN; j++) {
           const bool last = j == FN - 1;
@@ -333,31 +391,54 @@ struct F8Ring {
             asm volatile("" : "+v"(c));  // here, not behind the next branch
             __builtin_amdgcn_sched_barrier(0);
             mfma_start(q, fb[j & 1], fa[u]);
-            if (last) fa[u] = fragment(smem + (buf ^ 1) * T::STAGE + la + u * 2048, sw);
+            if (last) fa[u] = fragment(smem + then.a * T::STEP_A + la + u * 2048, sw);
             __builtin_amdgcn_sched_barrier(0);
           }
-          if (j + 2 < FN) fb[j & 1] = fragment(here + (j + 2) * 2048, sw);
           if (j == FN - 2) {
-            wait_vm<0>();
-            if (tail != 0 && s + 2 == S) zero_tail(buf ^ 1);
+            // the next block is there (those that the tile starts with are since
+            // the last tile's output; its stores are waited for with the copies
+            // behind them)
+            if (first || !cross || s + 2 >= T::D) {
+              if (ahead - (s + 1) >= T::NEWER)
+                wait_vm<T::NEWER * T::COPIES>();
+              else
+                wait_vm<0>();
+            }
+            if (tail != 0 && s + 2 == S) zero_tail(then);
             ring_barrier();
             asm volatile("" : "+s"(sb_next));  // loaded by now
-            if (s + 2 < S) {
-              copy_all(w, s + 2, buf);
-            } else if ((s + 2 == S || S == 1) && next) {
-              open(following);
-              if (GATHER) w = places(w_next);
-              copy_all(w, 0, S == 1 ? buf ^ 1 : buf);
-            }
-            fb[0] = fragment(smem + (buf ^ 1) * T::STAGE + lb, sw);
           }
-          if (last) fb[1] = fragment(smem + (buf ^ 1) * T::STAGE + lb + 2048, sw);
+          // all have read what the copies take the place of
+          if (T::SPLIT && j == T::FROM) asm volatile("s_barrier" ::: "memory");
+          if (j == T::FROM) {
+            const int v = s + T::D;
+            if (v < S) {
+              to_copy = v;
+            } else if (cross && next && v < S + T::D - 1) {
+              to_copy = v - S;
+              if (v == S) {
+                open(following);
+                if (GATHER) w = places(w_next);
+              }
+            }
+            if (to_copy >= 0) ahead = v;
+          }
+          if (j + 2 < FN)
+            fb[j & 1] = fragment(smem + b_column(at, j + 2), sw);
+          else
+            fb[j & 1] = fragment(smem + b_column(then, j + 2 - FN), sw);
+          const int part = j - T::FROM;
+          if (part >= 0 && part < T::ISSUE && to_copy >= 0) {
+#pragma unroll
+            for (int u = part * T::COPIES / T::ISSUE; u < (part + 1) * T::COPIES / T::ISSUE; u++)
+              copy(w, to_copy, later(at), u);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int u = 0; u < FM; u++) sa[u] = *reinterpret_cast<const float*>(smem + ls + (buf ^ 1) * T::SZS + u * 64);
+        for (int u = 0; u < FM; u++) sa[u] = *reinterpret_cast<const float*>(smem + ls + then.a * T::SZS + u * 64);
         sb = sb_next;
-        buf ^= 1;
+        at = then;
       }
       asm volatile("s_nop 15\n\ts_nop 2" ::: "memory");
 #pragma unroll
@@ -370,8 +451,8 @@ struct F8Ring {
           for (int x = 0; x < 4; x++) c[x] = fmaf(p[l][u][x], sc[u], c[x]);
         }
       }
-      // the buffer of the last block, which all have read
-      uint8_t* cst = smem + (buf ^ 1) * T::STAGE + wave * 4096;
+      // the slot of the last block, which all have read
+      uint8_t* cst = smem + (at.a == 0 ? T::D - 1 : at.a - 1) * T::STEP_A + wave * 4096;
       if (t.rows != T::BM || (t.tn + 1) * T::BN > a.N)
         store<-1, 0>(a, t, acc, cst, wm, wn);
       else if (a.e.act == kActGelu)
@@ -380,7 +461,7 @@ struct F8Ring {
         store_typed<kActNone>(a, t, acc, cst, wm, wn);
       if (!next) return;
       t = following;
-      if (tail != 0 && S == 1) zero_tail(buf);
+      first = false;
     }
   }
 
@@ -663,10 +744,11 @@ using Tile16x16 = F8Few<1, 1, 4, 5>;
 using Tile16x32 = F8Few<1, 2, 4, 3>;
 using Tile32x32 = F8Few<2, 2, 4, 4>;
 using Tile32x64 = F8Few<2, 4, 2, 3>;
-using Tile128x128 = F8Cfg<128, 128, 2, 2>;
-using Tile128x128Eight = F8Cfg<128, 128, 4, 2>;
-using Tile256x128 = F8Cfg<256, 128, 4, 2>;
-using Tile256x256 = F8Cfg<256, 256, 4, 2>;
+using Tile128x128 = F8Cfg<128, 128, 2, 2, 2>;
+// with a CU to itself: 8 waves, and two blocks more in flight
+using Tile128x128Deep = F8Cfg<128, 128, 4, 2, 4>;
+using Tile256x128 = F8Cfg<256, 128, 4, 2, 3>;
+using Tile256x256 = F8Cfg<256, 256, 4, 2, 2, true>;
 
 // variant V of kF8Variants
 template <int V, class T>
@@ -706,7 +788,7 @@ hipError_t launch_fp8(const F8Args& args, hipStream_t stream) {
     case 3:
       return launch_variant<3, Tile32x64>(a, stream);
     case 4:
-      return launch_variant<4, Tile128x128Eight>(a, stream);
+      return launch_variant<4, Tile128x128Deep>(a, stream);
     case 5:
       return launch_variant<5, Tile128x128>(a, stream);
     case 6:
