@@ -49,4 +49,22 @@ inline int f8_choice(int64_t M, int64_t N, int64_t K, int64_t E) {
   return best;
 }
 
+// ---- weight gradients ---------------------------------------------------------
+
+constexpr int kGradCus = 256;
+
+struct GradChoice {
+  bool large;
+  int splits;  // of the rows; > 1: partial sums in the workspace
+};
+inline GradChoice grad_choice(int64_t M, int64_t N, int64_t K, int64_t E, int terms) {
+  const int64_t bn = terms == 1 ? 256 : 128;
+  const int64_t large = ((N + bn - 1) / bn) * ((K + 255) / 256) * E;
+  if (large >= kGradCus / 2) return {true, 1};
+  const int64_t small = ((N + 127) / 128) * ((K + 127) / 128) * E;
+  int splits = 1;
+  while (splits < 64 && small * splits * 2 <= 2 * kGradCus && M / E / (splits * 2) >= 256) splits *= 2;
+  return {false, splits};
+}
+
 }  // namespace mxg

@@ -7,14 +7,17 @@
 // Products of bf16 values on the bf16 MFMA, summed in fp32.  x is rounded to
 // bf16: exact where s is a power of two (a code has 4 significant bits).  dY in
 // fp16 or fp32 is taken as the sum of two bf16 values (TERMS = 2), its nearest
-// one and that of the rest: exact for fp16, within 2^-17 of the value for fp32.
+// one and that of the rest: exact for fp16 of at least 2^-10, within 2^-17 of the
+// value for fp32.
 //
 // Both operands are contracted over their rows, so that a lane's 8 elements of
 // an MFMA operand are a column of LDS: ds_read_b64_tr_b16 reads 4 rows of 16
 // columns and hands each lane a column.  Which of the 32 rows of a step an
 // element is cancels out, as both operands use the same: rows 4 g .. 4 g + 3
-// and 16 + 4 g .. 16 + 4 g + 3 for lanes 16 g .. 16 g + 15, so that the 8 rows that
-// 32 lanes read at once lie in different banks (rows are 288 bytes apart).
+// and 16 + 4 g .. 16 + 4 g + 3 for lanes 16 g .. 16 g + 15.  A row's 32-byte pieces
+// (16 columns) are permuted by row % 8, so that the rows that are read at once lie in
+// different banks.
+#include "fp8_choice.h"
 #include "mxg_experts.h"
 #include "mxg_internal.h"
 
@@ -23,23 +26,10 @@ namespace {
 
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
 typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
 
-constexpr int kT = 128;            // tile: 128 x 128 of dW
-constexpr int kBMs = 64;           // rows of a slice
-constexpr int kPitch = 288;        // bytes of a row in LDS
-constexpr int kTile = kBMs * kPitch;
-
-__device__ __forceinline__ v4s read_tr(const uint8_t* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p));
-}
-// Operand of 16 columns at p (LDS; already at the lane's place) for one step of 32 rows.
-__device__ __forceinline__ v8b read_operand(const uint8_t* p) {
-  const v4s lo = read_tr(p), hi = read_tr(p + 16 * kPitch);
-  typedef short v8s __attribute__((ext_vector_type(8)));
-  const v8s v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  return __builtin_bit_cast(v8b, v);
-}
+constexpr int kMS = 64;  // rows of a slice
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return bf16_bits(a) | (bf16_bits(b) << 16); }
 
@@ -53,143 +43,380 @@ __device__ __forceinline__ uint32_t split_bf16(float& f) {
   return h;
 }
 
-// 8 elements n .. n + 7 of a row of dY in fp32; past its end zeros.
-template <int IN>
-__device__ __forceinline__ void load8(const void* p, int64_t at, int n, int N, float (&f)[8]) {
-  using T = typename RowElem<IN>::type;
-  const T* q = (const T*)p + at + n;
-  if (n + 8 <= N) {
-    if constexpr (IN == kOutF32) {
-      const v4f_any a = *reinterpret_cast<const v4f_any*>(q), b = *reinterpret_cast<const v4f_any*>(q + 4);
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        f[i] = a[i];
-        f[4 + i] = b[i];
-      }
-    } else {
-      const v4i w = *reinterpret_cast<const v4i_any*>(q);
-      unpack16<IN>(w, f);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i++) f[i] = n + i < N ? RowElem<IN>::get(q[i]) : 0.0f;
-  }
+// A thread's number in a form that the compiler cannot see through: what is
+// derived from it is formed where it is used, and not held in registers
+// across the loops.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
 
-template <int IN>
-__global__ __launch_bounds__(256) void fp8_weight_grad_kernel(F8GradArgs a) {
-  constexpr int TERMS = IN == kOutBF16 ? 1 : 2;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[(1 + TERMS) * kTile];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int k0 = blockIdx.x * kT, n0 = blockIdx.y * kT, e = blockIdx.z;
-  int m0 = 0, m1 = (int)a.M;
-  if (a.offsets != nullptr) {
-    // as the products read them: inside 0 .. M and never falling
-    int top = max(0, min(a.offsets[0], m1));
-    for (int i = 1; i <= e; i++) top = max(top, min(a.offsets[i], m1));
-    m0 = top;
-    m1 = max(top, min(a.offsets[e + 1], m1));
-  }
-  const int wk = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  uint8_t* lx = lds;
-  uint8_t* ly = lds + kTile;
-  const int g = lane >> 4, i16 = lane & 15;
-  const int place = (4 * g + (i16 >> 2)) * kPitch + (i16 & 3) * 8;
-  v4f acc[4][4] = {};
-  for (int m = m0; m < m1; m += kBMs) {
-    // codes: 64 rows x 128 columns, 16 at a time
+__device__ __forceinline__ void barrier_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Accumulator tied in AGPRs, in program order.
+__device__ __forceinline__ void mfma_bf16_acc(v4f& c, const v8s& x, const v8s& y) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(x), "v"(y));
+}
+
+// BK x BN of dW by WK x WN waves, each with FK x FN fragments.
+template <int BK_, int BN_, int WK_, int WN_, int TERMS_>
+struct GradCfg {
+  static constexpr int BK = BK_, BN = BN_, WK = WK_, WN = WN_, TERMS = TERMS_;
+  static constexpr int NT = WK * WN * 64;
+  static constexpr int FK = BK / WK / 16, FN = BN / WN / 16;
+  static constexpr int PX = BK * 2, PY = BN * 2;  // bytes of a row in LDS
+  static constexpr int OFF_Y = kMS * PX, SZY = kMS * PY, STAGE = OFF_Y + TERMS * SZY;
+  static constexpr int LDS = 2 * STAGE;
+  static constexpr int PER_CU = LDS > 80 * 1024 ? 1 : 2;
+  // pieces of a thread: 16 codes, 8 elements of dY
+  static constexpr int CX = kMS * BK / 16 / NT, CY = kMS * BN / 8 / NT;
+  static_assert(LDS <= 160 * 1024, "fits the 160 KiB LDS of a gfx950 CU");
+  static_assert(CX * NT * 16 == kMS * BK && CY * NT * 8 == kMS * BN && FN >= 2, "pieces split evenly");
+};
+
+template <int IN, class T, bool GATHER>
+struct Grad {
+  static constexpr int FK = T::FK, FN = T::FN, TERMS = T::TERMS, COLS = FN * TERMS;
+  static constexpr int VY = IN == kOutF32 ? 2 : 1;  // registers of 16 bytes of a piece of dY
+
+  // A slice on its way from memory to LDS.
+  struct Held {
+    v4i x[T::CX];
+    float s[T::CX];
+    int bad;  // bit u: the row of x[u] is outside A
+    v4i y[T::CY][VY];
+  };
+  struct Tile {
+    int e, k0, n0;
+    int m0, m1;  // rows
+    int64_t out; // partial sums: which of the splits
+  };
+
+  static __device__ __forceinline__ void load_index(const F8GradArgs& a, const Tile& t, int m, int (&at)[T::CX]) {
+    if constexpr (GATHER) {
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
-      const int c = tid + u * 256, row = c >> 3, k = k0 + (c & 7) * 16;
-      v4i w = {0, 0, 0, 0};
-      float s = 0.0f;
-      if (m + row < m1 && k < a.K) {
-        const int64_t ar = a_row(a, m + row);
-        s = __builtin_nanf("");  // rows outside A are NaN
-        if (ar >= 0) {
-          w = *reinterpret_cast<const v4i*>(a.A + ar * a.K + k);
-          s = a.SA[ar * a.KB + blockIdx.x];
+      for (int u = 0; u < T::CX; u++)
+        at[u] = a.index[min(m + (int)(threadIdx.x + u * T::NT) / (T::BK / 16), t.m1 - 1)];
+    }
+  }
+
+  // Slice of rows m .. m + 63 (m < m1); rows past m1 are fetched as the last one.
+  // Offsets from the slice's first element fit 32 bits (64 rows of 2^20).
+  static __device__ __forceinline__ void load(const F8GradArgs& a, const Tile& t, int m, const int (&at)[T::CX], Held& h) {
+    const int tid = opaque(threadIdx.x);
+    const int most = t.m1 - 1 - m;
+    h.bad = 0;
+#pragma unroll
+    for (int u = 0; u < T::CX; u++) {
+      const int c = tid + u * T::NT;
+      // (nothing is stored of the columns past K)
+      const int k = min(t.k0 + c % (T::BK / 16) * 16, a.K - 16);
+      if constexpr (GATHER) {
+        int64_t row = row_of_index(a, at[u]);
+        if (row < 0) h.bad |= 1 << u;
+        row = max(row, (int64_t)0);
+        h.x[u] = *reinterpret_cast<const v4i*>(a.A + row * a.K + k);
+        h.s[u] = a.SA[row * a.KB + (k >> 7)];
+      } else {
+        const uint32_t row = (uint32_t)min(c / (T::BK / 16), most);
+        h.x[u] = *reinterpret_cast<const v4i*>(a.A + (int64_t)m * a.K + (row * (uint32_t)a.K + (uint32_t)k));
+        h.s[u] = (a.SA + (int64_t)m * a.KB)[row * (uint32_t)a.KB + (uint32_t)(k >> 7)];
+      }
+    }
+    using E = typename RowElem<IN>::type;
+    const E* base = (const E*)a.dY + ((int64_t)m * a.N + t.n0);
+    // elements from there to the end of dY
+    const int64_t left = (a.M - m) * a.N - t.n0;
+    if ((int64_t)min(most, kMS - 1) * a.N + T::BN <= left) {
+      // columns past N hold what follows in memory (nothing of theirs is stored)
+#pragma unroll
+      for (int u = 0; u < T::CY; u++) {
+        const int c = tid + u * T::NT;
+        const uint32_t i = (uint32_t)min(c / (T::BN / 8), most) * (uint32_t)a.N + (uint32_t)(c % (T::BN / 8) * 8);
+#pragma unroll
+        for (int v = 0; v < VY; v++) h.y[u][v] = *reinterpret_cast<const v4i_any*>(base + (i + v * RowElem<IN>::VEC));
+      }
+    } else {
+      // the last rows of dY, whose pieces may end behind it
+#pragma unroll
+      for (int u = 0; u < T::CY; u++) {
+        const int c = tid + u * T::NT;
+        const uint32_t i = (uint32_t)min(c / (T::BN / 8), most) * (uint32_t)a.N + (uint32_t)(c % (T::BN / 8) * 8);
+        constexpr int PER = 4 / sizeof(E);
+#pragma unroll
+        for (int d = 0; d < 4 * VY; d++) {
+          uint32_t x = 0;
+#pragma unroll
+          for (int j = 0; j < PER; j++) {
+            E one = 0;
+            if ((int64_t)i + d * PER + j < left) one = base[i + d * PER + j];
+            if constexpr (PER == 1)
+              x = __float_as_uint(one);
+            else
+              x |= (uint32_t)one << (16 * j);
+          }
+          asm volatile("" : "+v"(x)::"memory");  // one at a time: no registers for all
+          h.y[u][d >> 2][d & 3] = (int)x;
         }
       }
+    }
+  }
+
+  // A slice into its stage; `rows`: those that count, the others become zeros.
+  static __device__ __forceinline__ void put(const Held& h, uint8_t* stage, int rows) {
+    const int tid = opaque(threadIdx.x);
+#pragma unroll
+    for (int u = 0; u < T::CX; u++) {
+      const int c = tid + u * T::NT, row = c / (T::BK / 16), f = c % (T::BK / 16);
       v4i out[2];
+      const float s = GATHER && (h.bad >> u & 1) ? __builtin_nanf("") : h.s[u];
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[j], false);
-        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[j], true);
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(h.x[u][j], false);
+        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(h.x[u][j], true);
         out[j >> 1][2 * (j & 1)] = (int)pack_bf16(lo[0] * s, lo[1] * s);
         out[j >> 1][2 * (j & 1) + 1] = (int)pack_bf16(hi[0] * s, hi[1] * s);
       }
-      v4i* to = reinterpret_cast<v4i*>(lx + row * kPitch + (c & 7) * 32);
+      if (row >= rows) out[0] = out[1] = v4i{0, 0, 0, 0};
+      v4i* to = reinterpret_cast<v4i*>(stage + row * T::PX + ((f ^ (row & 7)) << 5));
       to[0] = out[0];
       to[1] = out[1];
     }
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-      const int c = tid + u * 256, row = c >> 4, n = n0 + (c & 15) * 8;
-      float f[8];
-      if (m + row < m1) {
-        load8<IN>(a.dY, (int64_t)(m + row) * a.N, n, a.N, f);
+    for (int u = 0; u < T::CY; u++) {
+      const int c = tid + u * T::NT, row = c / (T::BN / 8), q = c % (T::BN / 8);
+      uint8_t* to = stage + T::OFF_Y + row * T::PY + (((q >> 1) ^ (row & 7)) << 5) + (q & 1) * 16;
+      if constexpr (TERMS == 1) {
+        *reinterpret_cast<v4i*>(to) = row < rows ? h.y[u][0] : v4i{0, 0, 0, 0};
       } else {
+        float f[8];
+        if constexpr (IN == kOutF32) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) f[i] = 0.0f;
-      }
-#pragma unroll
-      for (int t = 0; t < TERMS; t++) {
-        v4i w;
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          w[i] = t + 1 < TERMS ? (int)(split_bf16(f[2 * i]) | (split_bf16(f[2 * i + 1]) << 16))
-                               : (int)pack_bf16(f[2 * i], f[2 * i + 1]);
-        *reinterpret_cast<v4i*>(ly + t * kTile + row * kPitch + (c & 15) * 16) = w;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int step = 0; step < kBMs / 32; step++) {
-      v8b fx[4];
-#pragma unroll
-      for (int i = 0; i < 4; i++) fx[i] = read_operand(lx + step * 32 * kPitch + place + (wk + 16 * i) * 2);
-#pragma unroll
-      for (int t = 0; t < TERMS; t++) {
+          for (int j = 0; j < 8; j++) f[j] = __int_as_float(h.y[u][j >> 2][j & 3]);
+        } else {
+          unpack16<IN>(h.y[u][0], f);
+        }
+        v4i w[2];
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          const v8b fy = read_operand(ly + t * kTile + step * 32 * kPitch + place + (wn + 16 * j) * 2);
-#pragma unroll
-          for (int i = 0; i < 4; i++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[i], fy, acc[i][j], 0, 0, 0);
+          w[0][j] = (int)(split_bf16(f[2 * j]) | (split_bf16(f[2 * j + 1]) << 16));
+          w[1][j] = (int)pack_bf16(f[2 * j], f[2 * j + 1]);
         }
+#pragma unroll
+        for (int v = 0; v < 2; v++) *reinterpret_cast<v4i*>(to + v * T::SZY) = row < rows ? w[v] : v4i{0, 0, 0, 0};
       }
     }
-    __syncthreads();
   }
-  // a lane holds columns 4 g .. 4 g + 3 of row n = lane % 16 of each fragment
-  const Epi out{a.dW, nullptr, a.out_type, kActNone};
+
+  static __device__ __forceinline__ v4s read_tr(const uint8_t* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p));
+  }
+  // Operand of a step: 16 columns of 32 rows from p, the lane's place in them.
+  static __device__ __forceinline__ v8s operand(const uint8_t* p, int pitch) {
+    const v4s lo = read_tr(p), hi = read_tr(p + 16 * pitch);
+    return v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  }
+
+  static __device__ __forceinline__ void run(const F8GradArgs& a, int tiles_k, int tiles_n, int splits) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wk = wave / T::WN, wn = wave % T::WN;
+    const int g = lane >> 4, i16 = lane & 15;
+    const int per = tiles_k * tiles_n, total = per * a.E * splits;
+
+    // Tile number b: workgroups are dispatched round-robin over the 8 XCDs, so
+    // that each XCD gets a contiguous range; in an expert, groups of 4 tiles of
+    // columns of dY take the tiles of codes in turn.
+    auto find = [&](int b, Tile& t) {
+      if (b >= total) return false;
+      const int x = b & 7, rem = total & 7;
+      const int id = x * (total >> 3) + min(x, rem) + (b >> 3);
+      const int which = id / per, in = id - which * per;
+      const int e = which / splits, z = which - e * splits;
+      const int group = in / (4 * tiles_k), first = group * 4, rows = min(tiles_n - first, 4);
+      const int rest = in - group * 4 * tiles_k;
+      int lo = 0, hi = (int)a.M;
+      if (a.offsets != nullptr) {
+        // the offsets count as kept inside 0 .. M and never falling
+        int top = 0;
+        for (int i = lane; i <= e; i += 64) top = max(top, min(a.offsets[i], (int)a.M));
+        top = __builtin_amdgcn_readlane(wave_scan<true>(top), 63);
+        lo = top;
+        hi = max(lo, min(a.offsets[e + 1], (int)a.M));
+      }
+      // the expert's rows in `splits` parts of whole slices
+      const int part = ((hi - lo + kMS - 1) / kMS + splits - 1) / splits * kMS;
+      t.e = e;
+      t.n0 = (first + rest % rows) * T::BN;
+      t.k0 = rest / rows * T::BK;
+      t.m0 = __builtin_amdgcn_readfirstlane(min(lo + z * part, hi));
+      t.m1 = __builtin_amdgcn_readfirstlane(min(lo + (z + 1) * part, hi));
+      t.out = (int64_t)z * a.E + e;
+      return true;
+    };
+
+    int b = blockIdx.x;
+    Tile t;
+    if (!find(b, t)) return;
+    Held h[2];
+    int at[T::CX];
+    auto start = [&](const Tile& t) {
+      // slices 0 and 1, and the rows of slice 2
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const int n = n0 + wn + 16 * j + i16;
-    if (n >= a.N) continue;
+      for (int i = 0; i < 2; i++) {
+        if (t.m0 + i * kMS < t.m1) {
+          load_index(a, t, t.m0 + i * kMS, at);
+          load(a, t, t.m0 + i * kMS, at, h[i]);
+        }
+      }
+      if (t.m0 + 2 * kMS < t.m1) load_index(a, t, t.m0 + 2 * kMS, at);
+    };
+    start(t);
+
+    for (;;) {
+      const int S = (t.m1 - t.m0 + kMS - 1) / kMS;
+      v4f acc[FK][FN];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int k = k0 + wk + 16 * i + 4 * g;
-      if (k < a.K) store_columns<true>(out, a.K, (int64_t)e * a.N + n, k, acc[i][j]);
+      for (int i = 0; i < FK; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++) {
+          acc[i][j] = v4f{0, 0, 0, 0};
+          asm volatile("" : "+a"(acc[i][j]));
+        }
+      asm volatile("s_nop 7" ::: "memory");
+      // slice s into stage s % 2, and slice s + 2 on its way
+      auto stage_in = [&](int s, Held& held) {
+        put(held, smem + (s & 1) * T::STAGE, t.m1 - t.m0 - s * kMS);
+        if (s + 2 < S) {
+          load(a, t, t.m0 + (s + 2) * kMS, at, held);
+          if (s + 3 < S) load_index(a, t, t.m0 + (s + 3) * kMS, at);
+        }
+      };
+      auto multiply = [&](int s) {
+        const uint8_t* stage = smem + (s & 1) * T::STAGE;
+        // the lane's place in a fragment's rows; column f is at that ^ (f << 5)
+        const int lane = opaque(threadIdx.x & 63), row = 4 * (lane >> 4) + ((lane & 15) >> 2);
+        const int px = row * T::PX + ((row & 7) << 5) + (lane & 3) * 8;
+        const int py = row * T::PY + ((row & 7) << 5) + (lane & 3) * 8;
+        auto column = [&](int step, int c) {
+          return operand(stage + T::OFF_Y + (c / FN) * T::SZY + step * 32 * T::PY + (py ^ ((wn * FN + c % FN) << 5)), T::PY);
+        };
+#pragma unroll
+        for (int step = 0; step < kMS / 32; step++) {
+          v8s fx[FK], fy[2];
+#pragma unroll
+          for (int i = 0; i < FK; i++)
+            fx[i] = operand(stage + step * 32 * T::PX + (px ^ ((wk * FK + i) << 5)), T::PX);
+          fy[0] = column(step, 0);
+          fy[1] = column(step, 1);
+#pragma unroll
+          for (int c = 0; c < COLS; c++) {
+#pragma unroll
+            for (int i = 0; i < FK; i++) mfma_bf16_acc(acc[i][c % FN], fx[i], fy[c & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (c + 2 < COLS) fy[c & 1] = column(step, c + 2);
+          }
+        }
+      };
+      if (S > 0) {
+        stage_in(0, h[0]);
+        barrier_lds();
+        for (int s = 0; s < S; s += 2) {
+          if (s + 1 < S) stage_in(s + 1, h[1]);
+          multiply(s);
+          barrier_lds();
+          if (s + 1 >= S) break;
+          if (s + 2 < S) stage_in(s + 2, h[0]);
+          multiply(s + 1);
+          barrier_lds();
+        }
+      }
+      const Tile now = t;
+      b += gridDim.x;
+      const bool next = find(b, t);
+      if (next) start(t);  // ahead of the stores
+      asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+      // a lane holds columns 4 g .. 4 g + 3 of row n = lane % 16 of each fragment
+      const Epi out{splits > 1 ? a.workspace : a.dW, nullptr, splits > 1 ? kOutF32 : a.out_type, kActNone};
+#pragma unroll
+      for (int j = 0; j < FN; j++) {
+        const int n = now.n0 + (wn * FN + j) * 16 + i16;
+#pragma unroll
+        for (int i = 0; i < FK; i++) {
+          asm volatile("" : "+a"(acc[i][j]));
+          const int k = now.k0 + (wk * FK + i) * 16 + 4 * g;
+          if (n < a.N && k < a.K) store_columns<false>(out, a.K, now.out * a.N + n, k, acc[i][j]);
+        }
+      }
+      if (!next) return;
     }
   }
+};
+
+template <int IN, class T, bool GATHER>
+__global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2))) void fp8_weight_grad_kernel(
+    F8GradArgs a, int tiles_k, int tiles_n, int splits) {
+  Grad<IN, T, GATHER>::run(a, tiles_k, tiles_n, splits);
+}
+
+// dW = sum over the splits, in their order.
+__global__ __launch_bounds__(256) void fp8_weight_grad_sum_kernel(const float* part, int splits, int64_t n, void* dW,
+                                                                  int type) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  v4f s = *reinterpret_cast<const v4f*>(part + i);
+  for (int z = 1; z < splits; z++) s += *reinterpret_cast<const v4f*>(part + z * n + i);
+  store_columns<false>(Epi{(uint8_t*)dW + i * epi_elem_bytes(type), nullptr, type, kActNone}, 4, 0, 0, s);
+}
+
+template <int IN, class T>
+hipError_t launch_tiles(const F8GradArgs& a, int splits, hipStream_t stream) {
+  const int tiles_n = (a.N + T::BN - 1) / T::BN, tiles_k = (a.K + T::BK - 1) / T::BK;
+  const int64_t tiles = (int64_t)tiles_n * tiles_k * a.E * splits;
+  if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const int64_t most = (int64_t)kGradCus * T::PER_CU;
+  const dim3 grid((unsigned)(tiles < most ? tiles : most)), block(T::NT);
+  if (a.index != nullptr)
+    hipLaunchKernelGGL((fp8_weight_grad_kernel<IN, T, true>), grid, block, 0, stream, a, tiles_k, tiles_n, splits);
+  else
+    hipLaunchKernelGGL((fp8_weight_grad_kernel<IN, T, false>), grid, block, 0, stream, a, tiles_k, tiles_n, splits);
+  return hipGetLastError();
+}
+
+template <int IN>
+hipError_t launch_in(const F8GradArgs& a, hipStream_t stream) {
+  constexpr int TERMS = IN == kOutBF16 ? 1 : 2;
+  using Large = GradCfg<256, TERMS == 1 ? 256 : 128, 4, 2, TERMS>;
+  using Small = GradCfg<128, 128, 2, 2, TERMS>;
+  const GradChoice c = grad_choice(a.M, a.N, a.K, a.E, TERMS);
+  if (c.large) return launch_tiles<IN, Large>(a, 1, stream);
+  hipError_t e = launch_tiles<IN, Small>(a, c.splits, stream);
+  if (e != hipSuccess || c.splits == 1) return e;
+  const int64_t n = (int64_t)a.E * a.N * a.K;
+  hipLaunchKernelGGL(fp8_weight_grad_sum_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, stream,
+                     (const float*)a.workspace, c.splits, n, a.dW, a.out_type);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t fp8_weight_grad_bytes(int64_t M, int64_t N, int64_t K, int64_t E) { return 0; }
+// The workspace is as large for any type of dY.
+int64_t fp8_weight_grad_bytes(int64_t M, int64_t N, int64_t K, int64_t E) {
+  int64_t most = 0;
+  for (int terms = 1; terms <= 2; terms++) {
+    const GradChoice c = grad_choice(M, N, K, E, terms);
+    if (c.splits > 1 && c.splits * E * N * K * 4 > most) most = c.splits * E * N * K * 4;
+  }
+  return most;
+}
 
 hipError_t launch_fp8_weight_grad(const F8GradArgs& args, int y_type, hipStream_t stream) {
   F8GradArgs a = args;
   set_division(a);
-  const dim3 grid((unsigned)a.KB, (unsigned)((a.N + kT - 1) / kT), (unsigned)a.E);
-  if (y_type == kOutF32)
-    hipLaunchKernelGGL(fp8_weight_grad_kernel<kOutF32>, grid, dim3(256), 0, stream, a);
-  else if (y_type == kOutBF16)
-    hipLaunchKernelGGL(fp8_weight_grad_kernel<kOutBF16>, grid, dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL(fp8_weight_grad_kernel<kOutF16>, grid, dim3(256), 0, stream, a);
-  return hipGetLastError();
+  if (y_type == kOutF32) return launch_in<kOutF32>(a, stream);
+  if (y_type == kOutBF16) return launch_in<kOutBF16>(a, stream);
+  return launch_in<kOutF16>(a, stream);
 }
 
 }  // namespace mxg
