@@ -92,64 +92,93 @@ struct Grad {
     int64_t out; // partial sums: which of the splits
   };
 
+  // What a thread keeps of its places in a tile's slices, so that a slice needs no
+  // index arithmetic: offsets of its first piece from a slice's first row (those of
+  // the others are a whole number of rows behind) and its places in LDS.
+  struct Place {
+    uint32_t x, s, y;  // elements of A, SA, dY
+    int to_x, to_y;    // bytes
+  };
+  static constexpr int ROWS_X = T::NT * 16 / T::BK, ROWS_Y = T::NT * 8 / T::BN;  // rows between pieces
+  static_assert(ROWS_X % 8 == 0 && ROWS_Y % 8 == 0, "pieces of a thread have one permutation");
+  static __device__ __forceinline__ Place place(const F8GradArgs& a, const Tile& t) {
+    Place w;
+    const int tid = opaque(threadIdx.x);
+    const int rx = tid / (T::BK / 16), f = tid % (T::BK / 16);
+    const int ry = tid / (T::BN / 8), q = tid % (T::BN / 8);
+    // (nothing is stored of the columns past K)
+    const int k = min(t.k0 + f * 16, a.K - 16);
+    w.x = (GATHER ? 0u : (uint32_t)rx * (uint32_t)a.K) + (uint32_t)k;
+    w.s = (GATHER ? 0u : (uint32_t)rx * (uint32_t)a.KB) + (uint32_t)(k >> 7);
+    w.y = (uint32_t)ry * (uint32_t)a.N + (uint32_t)(t.n0 + q * 8);
+    w.to_x = rx * T::PX + ((f ^ (rx & 7)) << 5);
+    w.to_y = T::OFF_Y + ry * T::PY + (((q >> 1) ^ (ry & 7)) << 5) + (q & 1) * 16;
+    return w;
+  }
+
   static __device__ __forceinline__ void load_index(const F8GradArgs& a, const Tile& t, int m, int (&at)[T::CX]) {
     if constexpr (GATHER) {
 #pragma unroll
       for (int u = 0; u < T::CX; u++)
-        at[u] = a.index[min(m + (int)(threadIdx.x + u * T::NT) / (T::BK / 16), t.m1 - 1)];
+        at[u] = a.index[min(m + (int)threadIdx.x / (T::BK / 16) + u * ROWS_X, t.m1 - 1)];
     }
   }
 
-  // Slice of rows m .. m + 63 (m < m1); rows past m1 are fetched as the last one.
-  // Offsets from the slice's first element fit 32 bits (64 rows of 2^20).
-  static __device__ __forceinline__ void load(const F8GradArgs& a, const Tile& t, int m, const int (&at)[T::CX], Held& h) {
-    const int tid = opaque(threadIdx.x);
+  // The pieces of rows m .. m + 63 (m < m1).  Offsets from the slice's first element
+  // fit 32 bits (64 rows of 2^20).  FULL: all rows exist and no piece ends behind
+  // dY (columns past N hold what follows in memory: nothing of theirs is stored).
+  // Else rows past m1 are fetched as the last one, and dY element by element.
+  template <bool FULL>
+  static __device__ __forceinline__ void load_slice(const F8GradArgs& a, const Tile& t, int m, const Place& w,
+                                                    const int (&at)[T::CX], Held& h) {
+    using E = typename RowElem<IN>::type;
     const int most = t.m1 - 1 - m;
     h.bad = 0;
 #pragma unroll
     for (int u = 0; u < T::CX; u++) {
-      const int c = tid + u * T::NT;
-      // (nothing is stored of the columns past K)
-      const int k = min(t.k0 + c % (T::BK / 16) * 16, a.K - 16);
       if constexpr (GATHER) {
         int64_t row = row_of_index(a, at[u]);
         if (row < 0) h.bad |= 1 << u;
         row = max(row, (int64_t)0);
-        h.x[u] = *reinterpret_cast<const v4i*>(a.A + row * a.K + k);
-        h.s[u] = a.SA[row * a.KB + (k >> 7)];
+        h.x[u] = *reinterpret_cast<const v4i*>(a.A + row * a.K + w.x);
+        h.s[u] = a.SA[row * a.KB + w.s];
       } else {
-        const uint32_t row = (uint32_t)min(c / (T::BK / 16), most);
-        h.x[u] = *reinterpret_cast<const v4i*>(a.A + (int64_t)m * a.K + (row * (uint32_t)a.K + (uint32_t)k));
-        h.s[u] = (a.SA + (int64_t)m * a.KB)[row * (uint32_t)a.KB + (uint32_t)(k >> 7)];
+        uint32_t x = w.x, s = w.s;
+        int64_t r = m + u * ROWS_X;
+        if constexpr (!FULL) {
+          const int rx = opaque(threadIdx.x) / (T::BK / 16);
+          const uint32_t back = (uint32_t)(rx + u * ROWS_X - min(rx + u * ROWS_X, most));
+          // (from the slice's own first row, as that of the piece may not exist)
+          x += (uint32_t)(u * ROWS_X) * (uint32_t)a.K - back * (uint32_t)a.K;
+          s += (uint32_t)(u * ROWS_X) * (uint32_t)a.KB - back * (uint32_t)a.KB;
+          r = m;
+        }
+        h.x[u] = *reinterpret_cast<const v4i*>(a.A + r * a.K + x);
+        h.s[u] = (a.SA + r * a.KB)[s];
       }
     }
-    using E = typename RowElem<IN>::type;
-    const E* base = (const E*)a.dY + ((int64_t)m * a.N + t.n0);
-    // elements from there to the end of dY
-    const int64_t left = (a.M - m) * a.N - t.n0;
-    if ((int64_t)min(most, kMS - 1) * a.N + T::BN <= left) {
-      // columns past N hold what follows in memory (nothing of theirs is stored)
+    if constexpr (FULL) {
 #pragma unroll
       for (int u = 0; u < T::CY; u++) {
-        const int c = tid + u * T::NT;
-        const uint32_t i = (uint32_t)min(c / (T::BN / 8), most) * (uint32_t)a.N + (uint32_t)(c % (T::BN / 8) * 8);
+        const E* base = (const E*)a.dY + (int64_t)(m + u * ROWS_Y) * a.N;
 #pragma unroll
-        for (int v = 0; v < VY; v++) h.y[u][v] = *reinterpret_cast<const v4i_any*>(base + (i + v * RowElem<IN>::VEC));
+        for (int v = 0; v < VY; v++) h.y[u][v] = *reinterpret_cast<const v4i_any*>(base + w.y + v * RowElem<IN>::VEC);
       }
     } else {
-      // the last rows of dY, whose pieces may end behind it
+      const E* base = (const E*)a.dY + (int64_t)m * a.N;
+      const int64_t left = (a.M - m) * a.N;  // elements from there to the end of dY
+      constexpr int PER = 4 / sizeof(E);
 #pragma unroll
       for (int u = 0; u < T::CY; u++) {
-        const int c = tid + u * T::NT;
-        const uint32_t i = (uint32_t)min(c / (T::BN / 8), most) * (uint32_t)a.N + (uint32_t)(c % (T::BN / 8) * 8);
-        constexpr int PER = 4 / sizeof(E);
+        const int tid = opaque(threadIdx.x), ry = tid / (T::BN / 8) + u * ROWS_Y;
+        const int64_t i = (int64_t)min(ry, most) * a.N + t.n0 + tid % (T::BN / 8) * 8;
 #pragma unroll
         for (int d = 0; d < 4 * VY; d++) {
           uint32_t x = 0;
 #pragma unroll
           for (int j = 0; j < PER; j++) {
             E one = 0;
-            if ((int64_t)i + d * PER + j < left) one = base[i + d * PER + j];
+            if (i + d * PER + j < left) one = base[i + d * PER + j];
             if constexpr (PER == 1)
               x = __float_as_uint(one);
             else
@@ -161,33 +190,54 @@ struct Grad {
       }
     }
   }
+  static __device__ __forceinline__ void load(const F8GradArgs& a, const Tile& t, int m, const Place& w,
+                                              const int (&at)[T::CX], Held& h) {
+    // a row more than the slice's: the last pieces of a row end up to BN - 1 columns behind it
+    if (m + kMS <= t.m1 && ((a.M - m - (kMS - 1)) * a.N - t.n0 >= T::BN))
+      load_slice<true>(a, t, m, w, at, h);
+    else
+      load_slice<false>(a, t, m, w, at, h);
+  }
 
-  // A slice into its stage; `rows`: those that count, the others become zeros.
-  static __device__ __forceinline__ void put(const Held& h, uint8_t* stage, int rows) {
-    const int tid = opaque(threadIdx.x);
+  // The pieces into their stage; `rows`: those that count, the others become zeros.
+  static __device__ __forceinline__ void put(const Held& h, const Place& w, uint8_t* stage, int rows) {
+    // Scales that are powers of two (within 2^+-100) are applied by the conversion
+    // itself, exactly: 8 instructions where the products and their rounding take 32.
+    bool simple = true;
+    float s[T::CX];
 #pragma unroll
     for (int u = 0; u < T::CX; u++) {
-      const int c = tid + u * T::NT, row = c / (T::BK / 16), f = c % (T::BK / 16);
-      v4i out[2];
-      const float s = GATHER && (h.bad >> u & 1) ? __builtin_nanf("") : h.s[u];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(h.x[u][j], false);
-        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(h.x[u][j], true);
-        out[j >> 1][2 * (j & 1)] = (int)pack_bf16(lo[0] * s, lo[1] * s);
-        out[j >> 1][2 * (j & 1) + 1] = (int)pack_bf16(hi[0] * s, hi[1] * s);
-      }
-      if (row >= rows) out[0] = out[1] = v4i{0, 0, 0, 0};
-      v4i* to = reinterpret_cast<v4i*>(stage + row * T::PX + ((f ^ (row & 7)) << 5));
-      to[0] = out[0];
-      to[1] = out[1];
+      s[u] = GATHER && (h.bad >> u & 1) ? __builtin_nanf("") : h.s[u];
+      const uint32_t bits = __float_as_uint(s[u]);
+      simple = simple && (bits & 0x7fffffu) == 0u && bits - 0x0d800000u <= 0x64000000u;
     }
+    v4i out[T::CX][2];
+    if (__all(simple)) {
+#pragma unroll
+      for (int u = 0; u < T::CX; u++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          out[u][j >> 1][2 * (j & 1)] =
+              __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)h.x[u][j], s[u], false));
+          out[u][j >> 1][2 * (j & 1) + 1] =
+              __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)h.x[u][j], s[u], true));
+        }
+    } else {
+#pragma unroll
+      for (int u = 0; u < T::CX; u++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(h.x[u][j], false);
+          const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(h.x[u][j], true);
+          out[u][j >> 1][2 * (j & 1)] = (int)pack_bf16(lo[0] * s[u], lo[1] * s[u]);
+          out[u][j >> 1][2 * (j & 1) + 1] = (int)pack_bf16(hi[0] * s[u], hi[1] * s[u]);
+        }
+    }
+    v4i y[T::CY][TERMS];
 #pragma unroll
     for (int u = 0; u < T::CY; u++) {
-      const int c = tid + u * T::NT, row = c / (T::BN / 8), q = c % (T::BN / 8);
-      uint8_t* to = stage + T::OFF_Y + row * T::PY + (((q >> 1) ^ (row & 7)) << 5) + (q & 1) * 16;
       if constexpr (TERMS == 1) {
-        *reinterpret_cast<v4i*>(to) = row < rows ? h.y[u][0] : v4i{0, 0, 0, 0};
+        y[u][0] = h.y[u][0];
       } else {
         float f[8];
         if constexpr (IN == kOutF32) {
@@ -196,16 +246,36 @@ struct Grad {
         } else {
           unpack16<IN>(h.y[u][0], f);
         }
-        v4i w[2];
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          w[0][j] = (int)(split_bf16(f[2 * j]) | (split_bf16(f[2 * j + 1]) << 16));
-          w[1][j] = (int)pack_bf16(f[2 * j], f[2 * j + 1]);
+          y[u][0][j] = (int)(split_bf16(f[2 * j]) | (split_bf16(f[2 * j + 1]) << 16));
+          y[u][1][j] = (int)pack_bf16(f[2 * j], f[2 * j + 1]);
         }
-#pragma unroll
-        for (int v = 0; v < 2; v++) *reinterpret_cast<v4i*>(to + v * T::SZY) = row < rows ? w[v] : v4i{0, 0, 0, 0};
       }
     }
+    if (rows < kMS) {
+      const int tid = opaque(threadIdx.x);
+#pragma unroll
+      for (int u = 0; u < T::CX; u++)
+        if (tid / (T::BK / 16) + u * ROWS_X >= rows) out[u][0] = out[u][1] = v4i{0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < T::CY; u++)
+        if (tid / (T::BN / 8) + u * ROWS_Y >= rows) {
+#pragma unroll
+          for (int v = 0; v < TERMS; v++) y[u][v] = v4i{0, 0, 0, 0};
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < T::CX; u++) {
+      v4i* to = reinterpret_cast<v4i*>(stage + w.to_x + u * ROWS_X * T::PX);
+      to[0] = out[u][0];
+      to[1] = out[u][1];
+    }
+#pragma unroll
+    for (int u = 0; u < T::CY; u++)
+#pragma unroll
+      for (int v = 0; v < TERMS; v++)
+        *reinterpret_cast<v4i*>(stage + w.to_y + u * ROWS_Y * T::PY + v * T::SZY) = y[u][v];
   }
 
   static __device__ __forceinline__ v4s read_tr(const uint8_t* p) {
@@ -261,13 +331,19 @@ struct Grad {
     if (!find(b, t)) return;
     Held h[2];
     int at[T::CX];
+    Place w;
+    // the lane's place in a fragment's rows; column f is at that ^ (f << 5)
+    const int row = 4 * g + (i16 >> 2);
+    const int px = row * T::PX + ((row & 7) << 5) + (i16 & 3) * 8;
+    const int py = row * T::PY + ((row & 7) << 5) + (i16 & 3) * 8;
     auto start = [&](const Tile& t) {
+      w = place(a, t);
       // slices 0 and 1, and the rows of slice 2
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         if (t.m0 + i * kMS < t.m1) {
           load_index(a, t, t.m0 + i * kMS, at);
-          load(a, t, t.m0 + i * kMS, at, h[i]);
+          load(a, t, t.m0 + i * kMS, w, at, h[i]);
         }
       }
       if (t.m0 + 2 * kMS < t.m1) load_index(a, t, t.m0 + 2 * kMS, at);
@@ -287,49 +363,49 @@ struct Grad {
       asm volatile("s_nop 7" ::: "memory");
       // slice s into stage s % 2, and slice s + 2 on its way
       auto stage_in = [&](int s, Held& held) {
-        put(held, smem + (s & 1) * T::STAGE, t.m1 - t.m0 - s * kMS);
+        put(held, w, smem + (s & 1) * T::STAGE, t.m1 - t.m0 - s * kMS);
         if (s + 2 < S) {
-          load(a, t, t.m0 + (s + 2) * kMS, at, held);
-          if (s + 3 < S) load_index(a, t, t.m0 + (s + 3) * kMS, at);
+          const int m = t.m0 + (s + 2) * kMS;
+          load(a, t, m, w, at, held);
+          if (s + 3 < S) load_index(a, t, m + kMS, at);
         }
       };
-      auto multiply = [&](int s) {
+      // MFMAs of 32 rows of slice s
+      auto multiply = [&](int s, int step) {
         const uint8_t* stage = smem + (s & 1) * T::STAGE;
-        // the lane's place in a fragment's rows; column f is at that ^ (f << 5)
-        const int lane = opaque(threadIdx.x & 63), row = 4 * (lane >> 4) + ((lane & 15) >> 2);
-        const int px = row * T::PX + ((row & 7) << 5) + (lane & 3) * 8;
-        const int py = row * T::PY + ((row & 7) << 5) + (lane & 3) * 8;
-        auto column = [&](int step, int c) {
+        auto column = [&](int c) {
           return operand(stage + T::OFF_Y + (c / FN) * T::SZY + step * 32 * T::PY + (py ^ ((wn * FN + c % FN) << 5)), T::PY);
         };
+        v8s fx[FK], fy[2];
 #pragma unroll
-        for (int step = 0; step < kMS / 32; step++) {
-          v8s fx[FK], fy[2];
+        for (int i = 0; i < FK; i++) fx[i] = operand(stage + step * 32 * T::PX + (px ^ ((wk * FK + i) << 5)), T::PX);
+        fy[0] = column(0);
+        fy[1] = column(1);
 #pragma unroll
-          for (int i = 0; i < FK; i++)
-            fx[i] = operand(stage + step * 32 * T::PX + (px ^ ((wk * FK + i) << 5)), T::PX);
-          fy[0] = column(step, 0);
-          fy[1] = column(step, 1);
+        for (int c = 0; c < COLS; c++) {
 #pragma unroll
-          for (int c = 0; c < COLS; c++) {
-#pragma unroll
-            for (int i = 0; i < FK; i++) mfma_bf16_acc(acc[i][c % FN], fx[i], fy[c & 1]);
-            __builtin_amdgcn_sched_barrier(0);
-            if (c + 2 < COLS) fy[c & 1] = column(step, c + 2);
-          }
+          for (int i = 0; i < FK; i++) mfma_bf16_acc(acc[i][c % FN], fx[i], fy[c & 1]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (c + 2 < COLS) fy[c & 1] = column(c + 2);
+          __builtin_amdgcn_sched_barrier(0);
         }
+      };
+      // Slice s, and slice s + 1 into the other stage.  The two waves of a SIMD do the
+      // latter at different times, so that one converts while the other multiplies.
+      auto slice = [&](int s, Held& held) {
+        const bool more = s + 1 < S;
+        if (more && wave < T::NT / 128) stage_in(s + 1, held);
+        multiply(s, 0);
+        if (more && wave >= T::NT / 128) stage_in(s + 1, held);
+        multiply(s, 1);
+        barrier_lds();
       };
       if (S > 0) {
         stage_in(0, h[0]);
         barrier_lds();
         for (int s = 0; s < S; s += 2) {
-          if (s + 1 < S) stage_in(s + 1, h[1]);
-          multiply(s);
-          barrier_lds();
-          if (s + 1 >= S) break;
-          if (s + 2 < S) stage_in(s + 2, h[0]);
-          multiply(s + 1);
-          barrier_lds();
+          slice(s, h[1]);
+          if (s + 1 < S) slice(s + 1, h[0]);
         }
       }
       const Tile now = t;
