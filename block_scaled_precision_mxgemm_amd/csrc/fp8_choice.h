@@ -50,21 +50,53 @@ inline int f8_choice(int64_t M, int64_t N, int64_t K, int64_t E) {
 }
 
 // ---- weight gradients ---------------------------------------------------------
-
+//
+// Tiles of 256 x 256 (one workgroup a CU; with dY in two terms 256 x 128, two a CU)
+// or of 128 x 128 (two a CU), the latter with the rows in up to 64 parts whose
+// sums are added by a second kernel.  The estimate: rounds x (slices of 64 rows x us
+// + extra), with a CU to itself `alone` instead of `us`; and for parts what a
+// launch and the partial sums' bytes take.  Measured, in us (fp32 result; * what is
+// taken):
+//                                       bf16: 256  128   in 2  in 8    fp16: large  128   in 2  in 8
+//   2047 x 4100 x 2064                    69.4*  77.0  87.1   160          117*   149   139   195
+//   8192 x 4096 x 4096                     242*   332   374   568          466*   717   757   920
+//   16384 x 1024 x 1024                    442    235   124  55.1*         724    535   274   103*
+//   16384 x 256 x 512                      437    232   121  38.3*         717    530   269  75.8*  (in 32: 30 and 40)
+//   4096 x 2048 x 2048                     118   63.3  57.4* 88.3          187    138   105*  135
+//   512 x 4096 x 4096                     33.9*  31.7  82.7   279         48.6*  55.6  99.9   287
+//   4096 x 4 rows of 16 of 4096 x 2048     379*   465                      605*   887
+//   4096 x 2 rows of 4 of 512 x 512       71.7   42.0                      111   79.8               (in 4: 28 and 36)
 constexpr int kGradCus = 256;
 
 struct GradChoice {
   bool large;
   int splits;  // of the rows; > 1: partial sums in the workspace
 };
+
 inline GradChoice grad_choice(int64_t M, int64_t N, int64_t K, int64_t E, int terms) {
-  const int64_t bn = terms == 1 ? 256 : 128;
-  const int64_t large = ((N + bn - 1) / bn) * ((K + 255) / 256) * E;
-  if (large >= kGradCus / 2) return {true, 1};
-  const int64_t small = ((N + 127) / 128) * ((K + 127) / 128) * E;
-  int splits = 1;
-  while (splits < 64 && small * splits * 2 <= 2 * kGradCus && M / E / (splits * 2) >= 256) splits *= 2;
-  return {false, splits};
+  auto estimate = [&](bool large, int splits) {
+    const int bn = large && terms == 1 ? 256 : 128, bk = large ? 256 : 128;
+    const int per_cu = large && terms == 1 ? 1 : 2;
+    const double us = large ? (terms == 1 ? 1.75 : 3.6) : (terms == 1 ? 1.3 : 2.8);
+    const double alone = large ? (terms == 1 ? 1.75 : 2.8) : (terms == 1 ? 0.91 : 2.1);
+    const double extra = large ? 10.0 : 5.0;
+    const double tiles = (double)((N + bn - 1) / bn) * (double)((K + bk - 1) / bk) * (double)E * splits;
+    const double full = tiles / (kGradCus * per_cu);
+    const double rounds = full > 4.0 ? full + 0.5 : __builtin_ceil(full);
+    const double slices = __builtin_ceil((double)M / E / 64.0 / splits);
+    const double t = rounds * (slices * (tiles <= kGradCus ? alone : us) + extra);
+    return splits == 1 ? t : t + 4.0 + 8.0 * splits * (double)E * N * K / 5.0e6;
+  };
+  GradChoice best = {true, 1};
+  double least = estimate(true, 1);
+  for (int splits = 1; splits <= 64; splits *= 2) {
+    const double t = estimate(false, splits);
+    if (t < least) {
+      least = t;
+      best = {false, splits};
+    }
+  }
+  return best;
 }
 
 }  // namespace mxg

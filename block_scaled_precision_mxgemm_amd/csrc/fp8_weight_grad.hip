@@ -17,6 +17,8 @@
 // and 16 + 4 g .. 16 + 4 g + 3 for lanes 16 g .. 16 g + 15.  A row's 32-byte pieces
 // (16 columns) are permuted by row % 8, so that the rows that are read at once lie in
 // different banks.
+#include <type_traits>
+
 #include "fp8_choice.h"
 #include "mxg_experts.h"
 #include "mxg_internal.h"
@@ -28,8 +30,6 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
-
-constexpr int kMS = 64;  // rows of a slice
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return bf16_bits(a) | (bf16_bits(b) << 16); }
 
@@ -58,25 +58,27 @@ __device__ __forceinline__ void mfma_bf16_acc(v4f& c, const v8s& x, const v8s& y
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(x), "v"(y));
 }
 
-// BK x BN of dW by WK x WN waves, each with FK x FN fragments.
-template <int BK_, int BN_, int WK_, int WN_, int TERMS_>
+// BK x BN of dW by WK x WN waves, each with FK x FN fragments, in slices of MS rows.
+template <int BK_, int BN_, int WK_, int WN_, int TERMS_, int MS_>
 struct GradCfg {
+  static constexpr int MS = MS_;
   static constexpr int BK = BK_, BN = BN_, WK = WK_, WN = WN_, TERMS = TERMS_;
   static constexpr int NT = WK * WN * 64;
   static constexpr int FK = BK / WK / 16, FN = BN / WN / 16;
   static constexpr int PX = BK * 2, PY = BN * 2;  // bytes of a row in LDS
-  static constexpr int OFF_Y = kMS * PX, SZY = kMS * PY, STAGE = OFF_Y + TERMS * SZY;
+  static constexpr int OFF_Y = MS * PX, SZY = MS * PY, STAGE = OFF_Y + TERMS * SZY;
   static constexpr int LDS = 2 * STAGE;
   static constexpr int PER_CU = LDS > 80 * 1024 ? 1 : 2;
   // pieces of a thread: 16 codes, 8 elements of dY
-  static constexpr int CX = kMS * BK / 16 / NT, CY = kMS * BN / 8 / NT;
+  static constexpr int CX = MS * BK / 16 / NT, CY = MS * BN / 8 / NT;
   static_assert(LDS <= 160 * 1024, "fits the 160 KiB LDS of a gfx950 CU");
-  static_assert(CX * NT * 16 == kMS * BK && CY * NT * 8 == kMS * BN && FN >= 2, "pieces split evenly");
+  static_assert(CX * NT * 16 == MS * BK && CY * NT * 8 == MS * BN && FN >= 2, "pieces split evenly");
 };
 
 template <int IN, class T, bool GATHER>
 struct Grad {
   static constexpr int FK = T::FK, FN = T::FN, TERMS = T::TERMS, COLS = FN * TERMS;
+  static constexpr int kMS = T::MS;
   static constexpr int VY = IN == kOutF32 ? 2 : 1;  // registers of 16 bytes of a piece of dY
 
   // A slice on its way from memory to LDS.
@@ -390,14 +392,17 @@ struct Grad {
           __builtin_amdgcn_sched_barrier(0);
         }
       };
-      // Slice s, and slice s + 1 into the other stage.  The two waves of a SIMD do the
-      // latter at different times, so that one converts while the other multiplies.
+      // Slice s, and slice s + 1 into the other stage.  Where two waves of a workgroup
+      // share a SIMD they do the latter at different times, so that one converts
+      // while the other multiplies.
       auto slice = [&](int s, Held& held) {
         const bool more = s + 1 < S;
-        if (more && wave < T::NT / 128) stage_in(s + 1, held);
+        constexpr int STEPS = kMS / 32;
+        const bool late = T::NT > 256 && STEPS == 2 && wave >= T::NT / 128;
+        if (more && !late) stage_in(s + 1, held);
         multiply(s, 0);
-        if (more && wave >= T::NT / 128) stage_in(s + 1, held);
-        multiply(s, 1);
+        if (more && late) stage_in(s + 1, held);
+        if constexpr (STEPS == 2) multiply(s, 1);
         barrier_lds();
       };
       if (S > 0) {
@@ -422,7 +427,7 @@ struct Grad {
         for (int i = 0; i < FK; i++) {
           asm volatile("" : "+a"(acc[i][j]));
           const int k = now.k0 + (wk * FK + i) * 16 + 4 * g;
-          if (n < a.N && k < a.K) store_columns<false>(out, a.K, now.out * a.N + n, k, acc[i][j]);
+          if (n < a.N && k < a.K) store_columns<true>(out, a.K, now.out * a.N + n, k, acc[i][j]);
         }
       }
       if (!next) return;
@@ -463,8 +468,9 @@ hipError_t launch_tiles(const F8GradArgs& a, int splits, hipStream_t stream) {
 template <int IN>
 hipError_t launch_in(const F8GradArgs& a, hipStream_t stream) {
   constexpr int TERMS = IN == kOutBF16 ? 1 : 2;
-  using Large = GradCfg<256, TERMS == 1 ? 256 : 128, 4, 2, TERMS>;
-  using Small = GradCfg<128, 128, 2, 2, TERMS>;
+  // (two workgroups a CU where dY is two terms)
+  using Large = typename std::conditional<TERMS == 1, GradCfg<256, 256, 4, 2, 1, 64>, GradCfg<256, 128, 4, 1, 2, 32>>::type;
+  using Small = GradCfg<128, 128, 2, 2, TERMS, TERMS == 1 ? 64 : 32>;
   const GradChoice c = grad_choice(a.M, a.N, a.K, a.E, TERMS);
   if (c.large) return launch_tiles<IN, Large>(a, 1, stream);
   hipError_t e = launch_tiles<IN, Small>(a, c.splits, stream);

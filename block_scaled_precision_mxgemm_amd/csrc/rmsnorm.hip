@@ -338,43 +338,180 @@ __global__ __launch_bounds__(256) void rmsnorm_dweight_kernel(NormGradArgs a, in
   for (int j = 0; j < VEC / 4; j++)
     *reinterpret_cast<v4f*>(p + 4 * j) = v4f{acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]};
 }
+
+// 64 columns a workgroup: 16 lanes of 4 columns, 16 of them at a time over the strips.
 __global__ __launch_bounds__(256) void rmsnorm_dweight_sum_kernel(const float* part, int strips, int K, float* dW) {
-  const int k = blockIdx.x * 256 + threadIdx.x;
-  if (k >= K) return;
-  float s = 0.0f;
-  for (int i = 0; i < strips; i++) s += part[(int64_t)i * K + k];
-  dW[k] = s;
+  __shared__ __attribute__((aligned(16))) v4f sums[256];
+  const int k = blockIdx.x * 64 + (threadIdx.x & 15) * 4;
+  v4f s = {0, 0, 0, 0};
+  if (k < K) {
+    for (int i = threadIdx.x >> 4; i < strips; i += 16) s += *reinterpret_cast<const v4f*>(part + (int64_t)i * K + k);
+  }
+  sums[threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.x < 16 && k < K) {
+#pragma unroll
+    for (int i = 1; i < 16; i++) s += sums[threadIdx.x + 16 * i];
+    *reinterpret_cast<v4f*>(dW + k) = s;
+  }
 }
 
-// Strips of rows that the weight's gradient is summed over.
-int strips_of(int64_t rows) { return (int)(rows < 256 ? rows : 256); }
+// Both gradients in one pass over dY and H: a workgroup takes every G-th row (or
+// group of rows, where L lanes are less than a workgroup), holds a row's pieces and
+// the sums of its columns in registers, and has the next row on its way meanwhile.
+// The sums go to `part`, one row of them for each workgroup.
+template <int IN, int HELD, int L>
+__global__ __launch_bounds__(norm_threads(L)) void rmsnorm_backward_fused_kernel(NormGradArgs a, float* sums) {
+  constexpr int VEC = RowElem<IN>::VEC, PER = norm_threads(L) / L;
+  using T = typename RowElem<IN>::type;
+  __shared__ float part[16];
+  __shared__ __attribute__((aligned(16))) float join[PER > 1 ? (PER - 1) * HELD * L * VEC : 1];
+  const int tid = threadIdx.x % L, sub = threadIdx.x / L;
+  const int nv = a.K / VEC;
+  const v4i zero = {0, 0, 0, 0};
+  float acc[HELD][VEC] = {}, w[HELD][VEC];
+#pragma unroll
+  for (int u = 0; u < HELD; u++) {
+    const int i = tid + u * L;
+#pragma unroll
+    for (int j = 0; j < VEC; j++) w[u][j] = 0.0f;
+    if (i < nv) load_weights<VEC>(a.W, a.w_type, i * VEC, w[u]);
+  }
+  v4i y[HELD], h[HELD];
+  float rstd = 0.0f;
+  auto load = [&](int64_t row) {
+    const bool live = row < a.rows;
+    rstd = live ? a.rstd[row] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < HELD; u++) {
+      const int i = tid + u * L;
+      const bool some = live && i < nv;
+      y[u] = some ? __builtin_nontemporal_load(reinterpret_cast<const v4i*>((const T*)a.dY + row * a.K) + i) : zero;
+      h[u] = some ? __builtin_nontemporal_load(reinterpret_cast<const v4i*>((const T*)a.H + row * a.K) + i) : zero;
+    }
+  };
+  // rows of all of a workgroup's parts together, so that its barriers are passed by all
+  const int64_t step = (int64_t)gridDim.x * PER;
+  int64_t row = (int64_t)blockIdx.x * PER + sub;
+  load(row);
+  for (int64_t base = (int64_t)blockIdx.x * PER; base < a.rows; base += step, row += step) {
+    v4i ny[HELD], nh[HELD], dh[HELD];
+    const float r = rstd;
+    const bool live = row < a.rows;
+#pragma unroll
+    for (int u = 0; u < HELD; u++) {
+      ny[u] = y[u];
+      nh[u] = h[u];
+      const int i = tid + u * L;
+      dh[u] = zero;
+      if (a.dH != nullptr && live && i < nv)
+        dh[u] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>((const T*)a.dH + row * a.K) + i);
+    }
+    load(row + step);
+    float dot = 0.0f;
+#pragma unroll
+    for (int u = 0; u < HELD; u++) {
+      float f[VEC], g[VEC];
+      unpack16<IN>(ny[u], g);
+      unpack16<IN>(nh[u], f);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        const float hat = f[j] * r;
+        acc[u][j] = fmaf(g[j], hat, acc[u][j]);
+        dot = fmaf(g[j] * w[u][j], hat, dot);
+      }
+    }
+    const float c = row_sum<L>(dot, part) / (float)a.K;
+    if (live) {
+      v4i* dx = reinterpret_cast<v4i*>((T*)a.dX + row * a.K);
+#pragma unroll
+      for (int u = 0; u < HELD; u++) {
+        const int i = tid + u * L;
+        if (i >= nv) continue;
+        float f[VEC], g[VEC], o[VEC];
+        unpack16<IN>(ny[u], g);
+        unpack16<IN>(nh[u], f);
+        unpack16<IN>(dh[u], o);
+#pragma unroll
+        for (int j = 0; j < VEC; j++) {
+          f[j] = r * (g[j] * w[u][j] - f[j] * r * c);
+          if (a.dH != nullptr) f[j] += o[j];
+        }
+        __builtin_nontemporal_store(pack16<IN>(f), dx + i);
+      }
+    }
+  }
+  if constexpr (PER > 1) {
+    // the workgroup's parts, in their order
+    if (sub > 0) {
+#pragma unroll
+      for (int u = 0; u < HELD; u++)
+#pragma unroll
+        for (int j = 0; j < VEC; j++) join[((sub - 1) * HELD + u) * L * VEC + j * L + tid] = acc[u][j];
+    }
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int p = 0; p < PER - 1; p++)
+#pragma unroll
+      for (int u = 0; u < HELD; u++)
+#pragma unroll
+        for (int j = 0; j < VEC; j++) acc[u][j] += join[(p * HELD + u) * L * VEC + j * L + tid];
+  }
+  float* out = sums + (int64_t)blockIdx.x * a.K;
+#pragma unroll
+  for (int u = 0; u < HELD; u++) {
+    const int i = tid + u * L;
+    if (i >= nv) continue;
+#pragma unroll
+    for (int j = 0; j < VEC / 4; j++)
+      *reinterpret_cast<v4f*>(out + i * VEC + 4 * j) = v4f{acc[u][4 * j], acc[u][4 * j + 1], acc[u][4 * j + 2], acc[u][4 * j + 3]};
+  }
+}
+
+// Rows of partial sums: as many as workgroups that have two a CU (their traffic
+// is 1 / 16 of the rest at 8192 rows), or strips of the long rows' kernel.
+constexpr int kStrips = 512;
+int strips_of(int64_t rows) { return (int)(rows < kStrips ? rows : kStrips); }
 
 template <int IN, int HELD, int L>
-void backward_rows(const NormGradArgs& a, hipStream_t stream) {
-  constexpr int threads = norm_threads(L), per = threads / L;
-  const int64_t groups = (a.rows + per - 1) / per, most = 1 << 20;
-  const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)((groups + most - 1) / most));
-  hipLaunchKernelGGL((rmsnorm_backward_kernel<IN, HELD, L>), grid, dim3(threads), 0, stream, a);
+void backward_fused(const NormGradArgs& a, hipStream_t stream) {
+  constexpr int per = norm_threads(L) / L;
+  const int64_t groups = (a.rows + per - 1) / per;
+  const int grid = strips_of(groups);
+  float* part = reinterpret_cast<float*>(a.workspace);
+  // one workgroup's sums are the result
+  hipLaunchKernelGGL((rmsnorm_backward_fused_kernel<IN, HELD, L>), dim3((unsigned)grid), dim3(norm_threads(L)), 0, stream, a,
+                     grid == 1 ? a.dW : part);
+  if (grid > 1)
+    hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel, dim3((unsigned)((a.K + 63) / 64)), dim3(256), 0, stream, part, grid, a.K,
+                       a.dW);
 }
 
 template <int IN>
 void backward_in(const NormGradArgs& a, hipStream_t stream) {
   const int64_t pieces = a.K / RowElem<IN>::VEC;
+  if (pieces <= 64) return backward_fused<IN, 1, 64>(a, stream);
+  if (pieces <= 2 * 64) return backward_fused<IN, 2, 64>(a, stream);
+  if (pieces <= 256) return backward_fused<IN, 1, 256>(a, stream);
+  if (pieces <= 2 * 256) return backward_fused<IN, 2, 256>(a, stream);
+  if (pieces <= 4 * 256) return backward_fused<IN, 4, 256>(a, stream);
+  if (pieces <= 2 * 1024) return backward_fused<IN, 2, 1024>(a, stream);
+  // longer rows: the sums of the columns in a pass of their own (first: dX may be dY)
   const int strips = strips_of(a.rows);
   float* part = reinterpret_cast<float*>(a.workspace);
-  // the sums first: dX may be dY
-  hipLaunchKernelGGL((rmsnorm_dweight_kernel<IN>), dim3((unsigned)((pieces + 255) / 256), (unsigned)strips), dim3(256), 0,
-                     stream, a, (a.rows + strips - 1) / strips, part);
-  hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel, dim3((unsigned)((a.K + 255) / 256)), dim3(256), 0, stream, part, strips,
-                     a.K, a.dW);
-  if (pieces <= 64)
-    backward_rows<IN, 1, 64>(a, stream);
-  else if (pieces <= 2 * 256)
-    backward_rows<IN, 2, 256>(a, stream);
-  else if (pieces <= 4 * 1024)
-    backward_rows<IN, 4, 1024>(a, stream);
+  const int64_t strip = (a.rows + strips - 1) / strips;
+  const int used = (int)((a.rows + strip - 1) / strip);
+  hipLaunchKernelGGL((rmsnorm_dweight_kernel<IN>), dim3((unsigned)((pieces + 255) / 256), (unsigned)used), dim3(256), 0,
+                     stream, a, strip, part);
+  hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel, dim3((unsigned)((a.K + 63) / 64)), dim3(256), 0, stream, part, used, a.K,
+                     a.dW);
+  const int64_t most = 1 << 20;
+  const dim3 grid((unsigned)(a.rows < most ? a.rows : most), (unsigned)((a.rows + most - 1) / most));
+  if (pieces <= 4 * 1024)
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<IN, 4, 1024>), grid, dim3(1024), 0, stream, a);
   else
-    backward_rows<IN, 0, 1024>(a, stream);
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<IN, 0, 1024>), grid, dim3(1024), 0, stream, a);
 }
 
 }  // namespace
