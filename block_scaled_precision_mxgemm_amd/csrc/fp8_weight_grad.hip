@@ -297,14 +297,21 @@ struct Grad {
     const int g = lane >> 4, i16 = lane & 15;
     const int per = tiles_k * tiles_n, total = per * a.E * splits;
 
-    // Tile number b: workgroups are dispatched round-robin over the 8 XCDs, so
-    // that each XCD gets a contiguous range; in an expert, groups of 4 tiles of
-    // columns of dY take the tiles of codes in turn.
+    // Tile number b: workgroups are dispatched round-robin over the 8 XCDs.  Each
+    // XCD gets an eighth of every expert's tiles (their numbers of rows differ),
+    // or a contiguous range where they do not split evenly; in an expert, groups of
+    // 4 tiles of columns of dY take the tiles of codes in turn.
     auto find = [&](int b, Tile& t) {
-      if (b >= total) return false;
       const int x = b & 7, rem = total & 7;
-      const int id = x * (total >> 3) + min(x, rem) + (b >> 3);
-      const int which = id / per, in = id - which * per;
+      int which, in;
+      if (per % 8 == 0) {
+        which = (b >> 3) / (per >> 3);
+        in = (b >> 3) - which * (per >> 3) + x * (per >> 3);
+      } else {
+        const int id = x * (total >> 3) + min(x, rem) + (b >> 3);
+        which = id / per;
+        in = id - which * per;
+      }
       const int e = which / splits, z = which - e * splits;
       const int group = in / (4 * tiles_k), first = group * 4, rows = min(tiles_n - first, 4);
       const int rest = in - group * 4 * tiles_k;
@@ -325,12 +332,10 @@ struct Grad {
       t.m0 = __builtin_amdgcn_readfirstlane(min(lo + z * part, hi));
       t.m1 = __builtin_amdgcn_readfirstlane(min(lo + (z + 1) * part, hi));
       t.out = (int64_t)z * a.E + e;
-      return true;
     };
 
-    int b = blockIdx.x;
     Tile t;
-    if (!find(b, t)) return;
+    find(blockIdx.x, t);
     Held h[2];
     int at[T::CX];
     Place w;
@@ -352,7 +357,7 @@ struct Grad {
     };
     start(t);
 
-    for (;;) {
+    {
       const int S = (t.m1 - t.m0 + kMS - 1) / kMS;
       v4f acc[FK][FN];
 #pragma unroll
@@ -413,24 +418,19 @@ struct Grad {
           if (s + 1 < S) slice(s + 1, h[0]);
         }
       }
-      const Tile now = t;
-      b += gridDim.x;
-      const bool next = find(b, t);
-      if (next) start(t);  // ahead of the stores
       asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
       // a lane holds columns 4 g .. 4 g + 3 of row n = lane % 16 of each fragment
       const Epi out{splits > 1 ? a.workspace : a.dW, nullptr, splits > 1 ? kOutF32 : a.out_type, kActNone};
 #pragma unroll
       for (int j = 0; j < FN; j++) {
-        const int n = now.n0 + (wn * FN + j) * 16 + i16;
+        const int n = t.n0 + (wn * FN + j) * 16 + i16;
 #pragma unroll
         for (int i = 0; i < FK; i++) {
           asm volatile("" : "+a"(acc[i][j]));
-          const int k = now.k0 + (wk * FK + i) * 16 + 4 * g;
-          if (n < a.N && k < a.K) store_columns<true>(out, a.K, now.out * a.N + n, k, acc[i][j]);
+          const int k = t.k0 + (wk * FK + i) * 16 + 4 * g;
+          if (n < a.N && k < a.K) store_columns<true>(out, a.K, t.out * a.N + n, k, acc[i][j]);
         }
       }
-      if (!next) return;
     }
   }
 };
@@ -455,9 +455,8 @@ template <int IN, class T>
 hipError_t launch_tiles(const F8GradArgs& a, int splits, hipStream_t stream) {
   const int tiles_n = (a.N + T::BN - 1) / T::BN, tiles_k = (a.K + T::BK - 1) / T::BK;
   const int64_t tiles = (int64_t)tiles_n * tiles_k * a.E * splits;
-  if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const int64_t most = (int64_t)kGradCus * T::PER_CU;
-  const dim3 grid((unsigned)(tiles < most ? tiles : most)), block(T::NT);
+  if (tiles * T::NT > 0xffffffffll) return hipErrorInvalidConfiguration;  // threads of a launch
+  const dim3 grid((unsigned)tiles), block(T::NT);
   if (a.index != nullptr)
     hipLaunchKernelGGL((fp8_weight_grad_kernel<IN, T, true>), grid, block, 0, stream, a, tiles_k, tiles_n, splits);
   else
