@@ -461,8 +461,9 @@ int64_t rmsnorm_backward_workspace(int64_t rows, int64_t K) {
 
 int rmsnorm_backward(const void* dY, const void* H, const void* dH, int type, const void* W, int w_type, const float* rstd,
                      int64_t rows, int64_t K, void* dX, float* dW, void* workspace, void* stream) {
-  if (!dY || !H || !W || !rstd || !dX || !dW || !workspace) return MXG_EINVAL;
+  if (!dY || !H || !W || !rstd || !dX || !dW) return MXG_EINVAL;
   if (!type_ok(type) || !type_ok(w_type) || !norm_dims_ok(rows, K)) return MXG_EINVAL;
+  if (!workspace && mxg::rmsnorm_backward_bytes(rows, K) > 0) return MXG_EINVAL;
   if (!aligned16(dY) || !aligned16(H) || !aligned16(dH) || !aligned16(W) || !aligned16(dX) || !aligned16(dW) ||
       !aligned16(workspace) || !aligned4(rstd))
     return MXG_EALIGN;

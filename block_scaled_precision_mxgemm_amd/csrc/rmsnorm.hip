@@ -469,6 +469,70 @@ __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_backward_fused_kernel
   }
 }
 
+// Few and short rows, where a second launch takes longer than the work: each
+// workgroup of 16 waves forms the sums of all rows for itself (they come from the
+// caches) and then the gradients of 64 pieces of their columns, a wave a row.
+constexpr int kFewRows = 64;
+constexpr int64_t kFewBytes = 512 * 1024;  // of H in fp32
+template <int IN>
+__global__ __launch_bounds__(1024) void rmsnorm_backward_few_kernel(NormGradArgs a) {
+  constexpr int VEC = RowElem<IN>::VEC;
+  using T = typename RowElem<IN>::type;
+  __shared__ float c[kFewRows];
+  __shared__ float sums[16][VEC][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int nv = a.K / VEC, rows = (int)a.rows;
+  for (int row = wave; row < rows; row += 16) {
+    const v4i* dy = reinterpret_cast<const v4i*>((const T*)a.dY + (int64_t)row * a.K);
+    const v4i* h = reinterpret_cast<const v4i*>((const T*)a.H + (int64_t)row * a.K);
+    const float r = a.rstd[row];
+    float dot = 0.0f;
+#pragma unroll 4
+    for (int i = lane; i < nv; i += 64) {
+      float f[VEC], g[VEC], w[VEC];
+      unpack16<IN>(dy[i], g);
+      unpack16<IN>(h[i], f);
+      load_weights<VEC>(a.W, a.w_type, i * VEC, w);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) dot = fmaf(g[j] * w[j], f[j] * r, dot);
+    }
+    dot = wave_sum(dot);
+    if (lane == 0) c[row] = dot / (float)a.K;
+  }
+  __syncthreads();
+  const int i = blockIdx.x * 64 + lane;
+  float acc[VEC] = {};
+  if (i < nv) {
+    float w[VEC];
+    load_weights<VEC>(a.W, a.w_type, i * VEC, w);
+    for (int row = wave; row < rows; row += 16) {
+      const int64_t base = (int64_t)row * a.K;
+      float f[VEC], g[VEC], o[VEC];
+      unpack16<IN>(reinterpret_cast<const v4i*>((const T*)a.dY + base)[i], g);
+      unpack16<IN>(reinterpret_cast<const v4i*>((const T*)a.H + base)[i], f);
+      if (a.dH != nullptr) unpack16<IN>(reinterpret_cast<const v4i*>((const T*)a.dH + base)[i], o);
+      const float r = a.rstd[row], mean = c[row];
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        acc[j] = fmaf(g[j], f[j] * r, acc[j]);
+        f[j] = r * (g[j] * w[j] - f[j] * r * mean);
+        if (a.dH != nullptr) f[j] += o[j];
+      }
+      reinterpret_cast<v4i*>((T*)a.dX + base)[i] = pack16<IN>(f);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; j++) sums[wave][j][lane] = acc[j];
+  __syncthreads();
+  if (wave >= VEC || i >= nv) return;
+  float s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; k++) s += sums[k][wave][lane];
+  a.dW[i * VEC + wave] = s;
+}
+
+bool few_rows(int64_t rows, int64_t K) { return rows <= kFewRows && rows * K * 4 <= kFewBytes; }
+
 // Rows of partial sums: as many as workgroups that have two a CU (their traffic
 // is 1 / 16 of the rest at 8192 rows), or strips of the long rows' kernel.
 constexpr int kStrips = 512;
@@ -491,13 +555,17 @@ void backward_fused(const NormGradArgs& a, hipStream_t stream) {
 template <int IN>
 void backward_in(const NormGradArgs& a, hipStream_t stream) {
   const int64_t pieces = a.K / RowElem<IN>::VEC;
+  if (few_rows(a.rows, a.K)) {
+    hipLaunchKernelGGL((rmsnorm_backward_few_kernel<IN>), dim3((unsigned)((pieces + 63) / 64)), dim3(1024), 0, stream, a);
+    return;
+  }
   if (pieces <= 64) return backward_fused<IN, 1, 64>(a, stream);
   if (pieces <= 2 * 64) return backward_fused<IN, 2, 64>(a, stream);
   if (pieces <= 256) return backward_fused<IN, 1, 256>(a, stream);
   if (pieces <= 2 * 256) return backward_fused<IN, 2, 256>(a, stream);
   if (pieces <= 4 * 256) return backward_fused<IN, 4, 256>(a, stream);
   if (pieces <= 2 * 1024) return backward_fused<IN, 2, 1024>(a, stream);
-  // longer rows: the sums of the columns in a pass of their own (first: dX may be dY)
+  // longer rows: the sums of the columns in a pass of their own
   const int strips = strips_of(a.rows);
   float* part = reinterpret_cast<float*>(a.workspace);
   const int64_t strip = (a.rows + strips - 1) / strips;
@@ -530,7 +598,9 @@ hipError_t launch_rmsnorm(const NormArgs& a, int type, hipStream_t stream) {
   return hipGetLastError();
 }
 
-int64_t rmsnorm_backward_bytes(int64_t rows, int64_t K) { return (int64_t)strips_of(rows) * K * 4; }
+int64_t rmsnorm_backward_bytes(int64_t rows, int64_t K) {
+  return few_rows(rows, K) ? 0 : (int64_t)strips_of(rows) * K * 4;
+}
 
 hipError_t launch_rmsnorm_backward(const NormGradArgs& a, int type, hipStream_t stream) {
   switch (type) {

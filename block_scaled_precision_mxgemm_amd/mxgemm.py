@@ -760,7 +760,7 @@ def rmsnorm_backward(d_y, h, weight, rstd, d_h: torch.Tensor | None = None, d_x:
                      d_weight: torch.Tensor | None = None, stream=None):
     """Gradients (d_x in h's type, of x and of the residual alike; d_weight K float32)
     of rmsnorm_quantize's y from d_y, with h and rstd as it gave them.  d_h: the
-    gradient that h gets besides, added to d_x.  d_x may be d_y or d_h.  The rounding
+    gradient that h gets besides, added to d_x.  d_x may be d_h.  The rounding
     to codes counts as the identity."""
     h = _arg(h, "h", _FLOATS, dim=2)
     rows, K = h.shape

@@ -661,10 +661,10 @@ int rmsnorm_quantize(const void *X, const void *R, int type, const void *W,
  *   dY, H, dH  device, rows x K of `type`, 16-byte aligned; dH (the gradient that H
  *              gets besides) may be NULL
  *   W, w_type, rows, K  as for rmsnorm_quantize;  rstd  device, rows fp32
- *   dX         device, rows x K of `type`, 16-byte aligned (written; may be dY or dH)
+ *   dX         device, rows x K of `type`, 16-byte aligned (written; may be dH)
  *   dW         device, K fp32, 16-byte aligned (written)
- *   workspace  device, rmsnorm_backward_workspace(rows, K) bytes, 16-byte aligned.
- *              Holds nothing between calls.
+ *   workspace  device, rmsnorm_backward_workspace(rows, K) bytes, 16-byte aligned;
+ *              NULL when that is 0.  Holds nothing between calls.
  * Returns MXG_OK or an error status.  Deterministic.
  */
 int64_t rmsnorm_backward_workspace(int64_t rows, int64_t K);

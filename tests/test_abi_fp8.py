@@ -98,7 +98,8 @@ def test_workspaces(lib):
     assert lib.fp8gemm_weight_grad_workspace(64 << 20, 1 << 20, 1 << 20, 1) >= 0
     assert lib.rmsnorm_backward_workspace(0, 64) == -1
     assert lib.rmsnorm_backward_workspace(4, 24) == -1
-    assert lib.rmsnorm_backward_workspace(4, 64) > 0
+    assert lib.rmsnorm_backward_workspace(4, 64) >= 0
+    assert lib.rmsnorm_backward_workspace(1000, 4096) > 0
 
 
 @pytest.mark.parametrize("change,want", [
@@ -120,7 +121,7 @@ def test_norm(lib, change, want):
     (dict(K=20), EINVAL), (dict(dY=A + 8), EALIGN), (dict(H=A + 8), EALIGN), (dict(dH=A + 8), EALIGN), (dict(W=A + 8), EALIGN),
     (dict(rstd=A + 2), EALIGN), (dict(dX=A + 8), EALIGN), (dict(dW=A + 8), EALIGN), (dict(ws=A + 8), EALIGN)])
 def test_norm_backward(lib, change, want):
-    p = dict(dY=A, H=A, dH=None, kind=1, W=A, wkind=0, rstd=A, rows=4, K=64, dX=A, dW=A, ws=A) | change
+    p = dict(dY=A, H=A, dH=None, kind=1, W=A, wkind=0, rstd=A, rows=1000, K=4096, dX=A, dW=A, ws=A) | change
     assert lib.rmsnorm_backward(p["dY"], p["H"], p["dH"], p["kind"], p["W"], p["wkind"], p["rstd"], p["rows"], p["K"], p["dX"],
                                 p["dW"], p["ws"], None) == want
 
