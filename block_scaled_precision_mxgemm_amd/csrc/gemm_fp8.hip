@@ -84,6 +84,9 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(F8Args a, int tiles_n) {
   }
 }
 
+// 16 bytes at any element's address
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
+
 // scales that a whole wave shares, by scalar loads
 typedef __attribute__((address_space(4))) float float_const;
 
@@ -539,15 +542,76 @@ struct F8Ring {
     }
   }
 
+  // The same for whole tiles of 16-bit results: bias, activation and rounding first,
+  // so that 32 rows x 64 columns go through the 4 KiB at once and come back 8
+  // columns a lane (half the LDS bytes, barriers and stores).
+  template <int OUT, int ACT>
+  static __device__ __forceinline__ void store16(const F8Args& a, const ExpertTile& t, v4f (&acc)[FM][FN], uint8_t* cst,
+                                                 int wm, int wn) {
+    const int lane = opaque(threadIdx.x & 63);
+    const int rr = lane >> 4, cc = lane & 15;
+    const int64_t eb = (int64_t)t.expert * a.N;
+    const int n0 = t.tn * T::BN + wn * T::TN;
+    bool out[FM];  // rows of A that do not exist
+#pragma unroll
+    for (int u = 0; u < FM; u++) out[u] = GATHER && a_row(a, t.row0 + wm * T::TM + 16 * u + cc) < 0;
+#pragma unroll
+    for (int h = 0; h < T::TN / 64; h++) {
+      v4f bias[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        // -0 leaves every sum as it is
+        bias[j] = v4f{-0.f, -0.f, -0.f, -0.f};
+        if (a.e.bias != nullptr)
+          bias[j] = *reinterpret_cast<const v4f_any*>(a.e.bias + eb + n0 + h * 64 + j * 16 + rr * 4);
+      }
+      // the next tile's first copies are older than these loads: none of them
+      // is in flight behind this, and the stores are not waited for with them
+      if (h == 0) wait_vm<0>();
+#pragma unroll
+      for (int u0 = 0; u0 < FM; u0 += 2) {
+#pragma unroll
+        for (int u = u0; u < u0 + 2; u++) {
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            v4f v = acc[u][h * 4 + j] + bias[j];
+            uint32_t b[4];
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+              if (GATHER) v[x] = out[u] ? __builtin_nanf("") : v[x];
+              if (ACT == kActGelu) v[x] = gelu(v[x]);
+              // fp32 values first (no conversion fused with GELU's last product)
+              if (OUT == kOutF16) asm("" : "+v"(v[x]));
+              b[x] = OUT == kOutBF16 ? bf16_bits(v[x]) : f16_bits(v[x]);
+            }
+            const int chunk = 2 * j + (rr >> 1);
+            *reinterpret_cast<v2i*>(cst + (u - u0) * 2048 + cc * 128 + ((chunk ^ (cc & 7)) << 4) + (rr & 1) * 8) =
+                v2i{(int)(b[0] | (b[1] << 16)), (int)(b[2] | (b[3] << 16))};
+          }
+        }
+        wave_sync();
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const int row = q * 8 + (lane >> 3), chunk = lane & 7;
+          const v4i v = *reinterpret_cast<const v4i*>(cst + row * 128 + ((chunk ^ (row & 7)) << 4));
+          const int64_t m = t.row0 + wm * T::TM + 16 * u0 + row;
+          __builtin_nontemporal_store(
+              (v4i_any)v, reinterpret_cast<v4i_any*>((uint16_t*)a.e.C + m * a.N + n0 + h * 64 + chunk * 8));
+        }
+        wave_sync();
+      }
+    }
+  }
+
   template <int ACT>
   static __device__ __forceinline__ void store_typed(const F8Args& a, const ExpertTile& t, v4f (&acc)[FM][FN], uint8_t* cst,
                                                      int wm, int wn) {
     if (a.e.out == kOutF32)
       store<kOutF32, ACT>(a, t, acc, cst, wm, wn);
     else if (a.e.out == kOutBF16)
-      store<kOutBF16, ACT>(a, t, acc, cst, wm, wn);
+      store16<kOutBF16, ACT>(a, t, acc, cst, wm, wn);
     else
-      store<kOutF16, ACT>(a, t, acc, cst, wm, wn);
+      store16<kOutF16, ACT>(a, t, acc, cst, wm, wn);
   }
 };
 
