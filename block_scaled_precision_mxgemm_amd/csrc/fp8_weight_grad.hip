@@ -146,23 +146,25 @@ struct Grad {
         h.s[u] = a.SA[row * a.KB + w.s];
       } else {
         uint32_t x = w.x, s = w.s;
-        int64_t r = m + u * ROWS_X;
-        if constexpr (!FULL) {
+        const uint8_t* from_x = a.A + (int64_t)m * a.K;
+        const float* from_s = a.SA + (int64_t)m * a.KB;
+        if constexpr (FULL) {
+          from_x += u * ((int64_t)ROWS_X * a.K);
+          from_s += u * ((int64_t)ROWS_X * a.KB);
+        } else {
           const int rx = opaque(threadIdx.x) / (T::BK / 16);
           const uint32_t back = (uint32_t)(rx + u * ROWS_X - min(rx + u * ROWS_X, most));
-          // (from the slice's own first row, as that of the piece may not exist)
           x += (uint32_t)(u * ROWS_X) * (uint32_t)a.K - back * (uint32_t)a.K;
           s += (uint32_t)(u * ROWS_X) * (uint32_t)a.KB - back * (uint32_t)a.KB;
-          r = m;
         }
-        h.x[u] = *reinterpret_cast<const v4i*>(a.A + r * a.K + x);
-        h.s[u] = (a.SA + r * a.KB)[s];
+        h.x[u] = *reinterpret_cast<const v4i*>(from_x + x);
+        h.s[u] = from_s[s];
       }
     }
     if constexpr (FULL) {
 #pragma unroll
       for (int u = 0; u < T::CY; u++) {
-        const E* base = (const E*)a.dY + (int64_t)(m + u * ROWS_Y) * a.N;
+        const E* base = (const E*)a.dY + (int64_t)m * a.N + u * ((int64_t)ROWS_Y * a.N);
 #pragma unroll
         for (int v = 0; v < VY; v++) h.y[u][v] = *reinterpret_cast<const v4i_any*>(base + w.y + v * RowElem<IN>::VEC);
       }
@@ -201,8 +203,10 @@ struct Grad {
       load_slice<false>(a, t, m, w, at, h);
   }
 
-  // The pieces into their stage; `rows`: those that count, the others become zeros.
-  static __device__ __forceinline__ void put(const Held& h, const Place& w, uint8_t* stage, int rows) {
+  // The pieces into their stage; `rows`: those that count, the others become zeros
+  // (FULL: all count).
+  template <bool FULL>
+  static __device__ __forceinline__ void put_rows(const Held& h, const Place& w, uint8_t* stage, int rows) {
     // Scales that are powers of two (within 2^+-100) are applied by the conversion
     // itself, exactly: 8 instructions where the products and their rounding take 32.
     bool simple = true;
@@ -255,7 +259,7 @@ struct Grad {
         }
       }
     }
-    if (rows < kMS) {
+    if constexpr (!FULL) {
       const int tid = opaque(threadIdx.x);
 #pragma unroll
       for (int u = 0; u < T::CX; u++)
@@ -278,6 +282,13 @@ struct Grad {
 #pragma unroll
       for (int v = 0; v < TERMS; v++)
         *reinterpret_cast<v4i*>(stage + w.to_y + u * ROWS_Y * T::PY + v * T::SZY) = y[u][v];
+  }
+
+  static __device__ __forceinline__ void put(const Held& h, const Place& w, uint8_t* stage, int rows) {
+    if (rows >= kMS)
+      put_rows<true>(h, w, stage, rows);
+    else
+      put_rows<false>(h, w, stage, rows);
   }
 
   static __device__ __forceinline__ v4s read_tr(const uint8_t* p) {
@@ -357,79 +368,77 @@ struct Grad {
     };
     start(t);
 
-    {
-      const int S = (t.m1 - t.m0 + kMS - 1) / kMS;
-      v4f acc[FK][FN];
+    const int S = (t.m1 - t.m0 + kMS - 1) / kMS;
+    v4f acc[FK][FN];
 #pragma unroll
-      for (int i = 0; i < FK; i++)
-#pragma unroll
-        for (int j = 0; j < FN; j++) {
-          acc[i][j] = v4f{0, 0, 0, 0};
-          asm volatile("" : "+a"(acc[i][j]));
-        }
-      asm volatile("s_nop 7" ::: "memory");
-      // slice s into stage s % 2, and slice s + 2 on its way
-      auto stage_in = [&](int s, Held& held) {
-        put(held, w, smem + (s & 1) * T::STAGE, t.m1 - t.m0 - s * kMS);
-        if (s + 2 < S) {
-          const int m = t.m0 + (s + 2) * kMS;
-          load(a, t, m, w, at, held);
-          if (s + 3 < S) load_index(a, t, m + kMS, at);
-        }
-      };
-      // MFMAs of 32 rows of slice s
-      auto multiply = [&](int s, int step) {
-        const uint8_t* stage = smem + (s & 1) * T::STAGE;
-        auto column = [&](int c) {
-          return operand(stage + T::OFF_Y + (c / FN) * T::SZY + step * 32 * T::PY + (py ^ ((wn * FN + c % FN) << 5)), T::PY);
-        };
-        v8s fx[FK], fy[2];
-#pragma unroll
-        for (int i = 0; i < FK; i++) fx[i] = operand(stage + step * 32 * T::PX + (px ^ ((wk * FK + i) << 5)), T::PX);
-        fy[0] = column(0);
-        fy[1] = column(1);
-#pragma unroll
-        for (int c = 0; c < COLS; c++) {
-#pragma unroll
-          for (int i = 0; i < FK; i++) mfma_bf16_acc(acc[i][c % FN], fx[i], fy[c & 1]);
-          __builtin_amdgcn_sched_barrier(0);
-          if (c + 2 < COLS) fy[c & 1] = column(c + 2);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      };
-      // Slice s, and slice s + 1 into the other stage.  Where two waves of a workgroup
-      // share a SIMD they do the latter at different times, so that one converts
-      // while the other multiplies.
-      auto slice = [&](int s, Held& held) {
-        const bool more = s + 1 < S;
-        constexpr int STEPS = kMS / 32;
-        const bool late = T::NT > 256 && STEPS == 2 && wave >= T::NT / 128;
-        if (more && !late) stage_in(s + 1, held);
-        multiply(s, 0);
-        if (more && late) stage_in(s + 1, held);
-        if constexpr (STEPS == 2) multiply(s, 1);
-        barrier_lds();
-      };
-      if (S > 0) {
-        stage_in(0, h[0]);
-        barrier_lds();
-        for (int s = 0; s < S; s += 2) {
-          slice(s, h[1]);
-          if (s + 1 < S) slice(s + 1, h[0]);
-        }
-      }
-      asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-      // a lane holds columns 4 g .. 4 g + 3 of row n = lane % 16 of each fragment
-      const Epi out{splits > 1 ? a.workspace : a.dW, nullptr, splits > 1 ? kOutF32 : a.out_type, kActNone};
+    for (int i = 0; i < FK; i++)
 #pragma unroll
       for (int j = 0; j < FN; j++) {
-        const int n = t.n0 + (wn * FN + j) * 16 + i16;
+        acc[i][j] = v4f{0, 0, 0, 0};
+        asm volatile("" : "+a"(acc[i][j]));
+      }
+    asm volatile("s_nop 7" ::: "memory");
+    // slice s into stage s % 2, and slice s + 2 on its way
+    auto stage_in = [&](int s, Held& held) {
+      put(held, w, smem + (s & 1) * T::STAGE, t.m1 - t.m0 - s * kMS);
+      if (s + 2 < S) {
+        const int m = t.m0 + (s + 2) * kMS;
+        load(a, t, m, w, at, held);
+        if (s + 3 < S) load_index(a, t, m + kMS, at);
+      }
+    };
+    // MFMAs of 32 rows of slice s
+    auto multiply = [&](int s, int step) {
+      const uint8_t* stage = smem + (s & 1) * T::STAGE;
+      auto column = [&](int c) {
+        return operand(stage + T::OFF_Y + (c / FN) * T::SZY + step * 32 * T::PY + (py ^ ((wn * FN + c % FN) << 5)), T::PY);
+      };
+      v8s fx[FK], fy[2];
 #pragma unroll
-        for (int i = 0; i < FK; i++) {
-          asm volatile("" : "+a"(acc[i][j]));
-          const int k = t.k0 + (wk * FK + i) * 16 + 4 * g;
-          if (n < a.N && k < a.K) store_columns<true>(out, a.K, t.out * a.N + n, k, acc[i][j]);
-        }
+      for (int i = 0; i < FK; i++) fx[i] = operand(stage + step * 32 * T::PX + (px ^ ((wk * FK + i) << 5)), T::PX);
+      fy[0] = column(0);
+      fy[1] = column(1);
+#pragma unroll
+      for (int c = 0; c < COLS; c++) {
+#pragma unroll
+        for (int i = 0; i < FK; i++) mfma_bf16_acc(acc[i][c % FN], fx[i], fy[c & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (c + 2 < COLS) fy[c & 1] = column(c + 2);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // Slice s, and slice s + 1 into the other stage.  Where two waves of a workgroup
+    // share a SIMD they do the latter at different times, so that one converts
+    // while the other multiplies.
+    auto slice = [&](int s, Held& held) {
+      const bool more = s + 1 < S;
+      constexpr int STEPS = kMS / 32;
+      const bool late = T::NT > 256 && STEPS == 2 && wave >= T::NT / 128;
+      if (more && !late) stage_in(s + 1, held);
+      multiply(s, 0);
+      if (more && late) stage_in(s + 1, held);
+      if constexpr (STEPS == 2) multiply(s, 1);
+      barrier_lds();
+    };
+    if (S > 0) {
+      stage_in(0, h[0]);
+      barrier_lds();
+      for (int s = 0; s < S; s += 2) {
+        slice(s, h[1]);
+        if (s + 1 < S) slice(s + 1, h[0]);
+      }
+    }
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    // a lane holds columns 4 g .. 4 g + 3 of row n = lane % 16 of each fragment
+    const Epi out{splits > 1 ? a.workspace : a.dW, nullptr, splits > 1 ? kOutF32 : a.out_type, kActNone};
+#pragma unroll
+    for (int j = 0; j < FN; j++) {
+      const int n = t.n0 + (wn * FN + j) * 16 + i16;
+#pragma unroll
+      for (int i = 0; i < FK; i++) {
+        asm volatile("" : "+a"(acc[i][j]));
+        const int k = t.k0 + (wk * FK + i) * 16 + 4 * g;
+        if (n < a.N && k < a.K) store_columns<true>(out, a.K, t.out * a.N + n, k, acc[i][j]);
       }
     }
   }
