@@ -209,3 +209,37 @@ def test_reference_weight_gradient_against_differences():
 
 def test_reference_expert_ranges():
     assert ref.rows_of_experts([-3, 2, 1, 99, 5], 8) == [(0, 2), (2, 2), (2, 8), (8, 8)]
+
+
+# ---- which tile the GPU tests' sizes take ---------------------------------------
+
+
+def test_large_tile_cases_take_their_tiles():
+    import test_gpu_fp8_large as large
+
+    chosen = large.load_choice()
+    for tile, M, N, K in large.DENSE:
+        assert chosen(M, N, K) == tile
+    for tile, E, tokens, k, N, K in large.EXPERTS:
+        assert chosen(tokens * k, N, K, E) == tile
+    for tile, rows, N, K in large.OFFSETS:
+        assert chosen(rows, N, K, 3) == tile
+    for cases, E in ((large.BLOCKS, 0), (large.BLOCKS_EXPERTS, 1)):
+        for tile, M, N in cases:
+            assert all(chosen(M, N, 128 * n - short, E) == tile for n in range(1, 7) for short in (0, 48, 96))
+    assert {c[0] for c in large.DENSE} == set(large.TILES)
+
+
+def test_gradient_cases_take_every_form():
+    """Large tiles, small ones, and rows in parts, with dY in one and two terms."""
+    import ctypes
+
+    import test_gpu_fp8_grad as grad
+
+    lib = ctypes.CDLL(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libfp8_choice.so"))
+    lib.fp8_grad_choice.argtypes = [ctypes.c_int64] * 4 + [ctypes.c_int]
+    for terms in (1, 2):
+        taken = {lib.fp8_grad_choice(M, N, K, 1, terms) for M, N, K in grad.SIZES}
+        assert {0, 1} <= taken and len(taken) >= 4
+        taken = {lib.fp8_grad_choice(t * k, N, K, E, terms) for E, t, k, N, K in grad.EXPERTS}
+        assert {0, 1} <= taken and len(taken) >= 3

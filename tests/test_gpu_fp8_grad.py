@@ -25,7 +25,7 @@ def exact_d(g, rows, N, kind):
 
 SIZES = [(1, 1, 16), (1, 130, 128), (2, 16, 144), (31, 7, 272), (32, 128, 256), (33, 129, 1040), (64, 100, 96), (65, 257, 384),
          (127, 300, 640), (200, 64, 2064), (513, 384, 512), (1000, 1030, 400), (2047, 515, 304), (4096, 256, 256), (9000, 24, 48),
-         (300, 2050, 1168), (8200, 136, 128)]
+         (300, 2050, 1168), (8200, 136, 128), (700, 4096, 2064), (130, 4100, 4112), (5000, 1000, 1040)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -109,9 +109,12 @@ def expert_grad(d, a, a_s, offsets, index, div, E):
     return out
 
 
-@pytest.mark.parametrize("E,tokens,k,N,K", [(1, 1, 1, 16, 128), (4, 3, 2, 130, 144), (8, 16, 2, 300, 400), (64, 16, 4, 128, 256),
-                                            (7, 100, 3, 257, 272), (16, 300, 4, 520, 640), (2, 1000, 2, 256, 256),
-                                            (130, 40, 8, 64, 128), (1024, 30, 2, 32, 48), (16, 1024, 4, 512, 512)])
+EXPERTS = [(1, 1, 1, 16, 128), (4, 3, 2, 130, 144), (8, 16, 2, 300, 400), (64, 16, 4, 128, 256), (7, 100, 3, 257, 272),
+           (16, 300, 4, 520, 640), (2, 1000, 2, 256, 256), (130, 40, 8, 64, 128), (1024, 30, 2, 32, 48), (16, 1024, 4, 512, 512),
+           (6, 700, 2, 2100, 1552), (3, 5000, 2, 136, 272), (16, 600, 3, 2048, 1024)]
+
+
+@pytest.mark.parametrize("E,tokens,k,N,K", EXPERTS)
 @pytest.mark.parametrize("kind", [0, 1])
 def test_experts(E, tokens, k, N, K, kind):
     say("weight grad experts", E, tokens, k, N, K, kind)
