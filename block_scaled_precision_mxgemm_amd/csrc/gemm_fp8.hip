@@ -668,7 +668,7 @@ __global__ __launch_bounds__(T::NW * 64) void fp8_few_kernel(F8Args a, int tiles
   const int cw = wave % CW, kw = wave / CW;
   const int g = lane >> 4, r = lane & 15;
   ExpertTile t;
-  if (!find_tile(a, T::BM, tiles_n, blockIdx.x, lane, t)) return;
+  if (!find_tile(a, T::BM, tiles_n, (int64_t)blockIdx.y * gridDim.x + blockIdx.x, lane, t)) return;
   const int K = a.K, n0 = t.tn * T::BN, cols = min(T::BN, a.N - n0);
   const int S = a.KB, tail = K & 127;  // blocks
   const int I = (S + KW - 1) / KW;     // stages
@@ -794,7 +794,9 @@ hipError_t launch_few(const F8Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
   const int64_t tiles = tiles_n * expert_tiles_m(a, T::BM);
   if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)tiles), block(T::NW * 64);
+  // in two dimensions: a launch has less than 2^32 threads in one
+  const int64_t most = 1 << 20;
+  const dim3 grid((unsigned)(tiles < most ? tiles : most), (unsigned)((tiles + most - 1) / most)), block(T::NW * 64);
   if (a.index != nullptr)
     hipLaunchKernelGGL((fp8_few_kernel<T, true>), grid, block, 0, stream, a, (int)tiles_n);
   else

@@ -208,3 +208,22 @@ def test_streams_and_replays_of_large_tiles():
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(held, want))
         assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_more_tiles_than_a_launch_has_threads():
+    """1000 rows over 1024 experts of 2^20 x 16: 2^24 tiles of 512 threads."""
+    say("fp8 large many tiles")
+    E, N, K, M = 1024, 1 << 20, 16, 1000
+    assert load_choice()(M, N, K, E) == "32x64"
+    g = gen(11)
+    a, a_s = exact_codes(g, M, K)
+    b = torch.randint(0x30, 0x40, (E, N, K), generator=g, device=DEV, dtype=torch.uint8)  # 0.5 .. 1.875
+    b_s = torch.exp2(torch.randint(-2, 3, (E, N // 128, 1), generator=g, device=DEV).float())
+    expert = torch.randint(0, E, (M,), generator=g, device=DEV).sort()[0]
+    off = torch.searchsorted(expert, torch.arange(E + 1, device=DEV)).int()
+    got = binding().fp8gemm_run_grouped(a, a_s, b, b_s, off, out_type=1)
+    for p in (0, 1, 333, 500, 998, 999):
+        e = int(expert[p])
+        y = ref.dequantize(b[e], b_s[e], 128) @ ref.dequantize(a[p:p + 1], a_s[p:p + 1])[0]
+        assert torch.equal(got[p], y.float().bfloat16())
+    assert bool(torch.isfinite(got).all()) and int((got == 0).all(-1).sum()) == 0
