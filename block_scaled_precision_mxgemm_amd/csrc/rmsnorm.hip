@@ -472,23 +472,28 @@ __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_backward_fused_kernel
 // Few and short rows, where a second launch takes longer than the work: each
 // workgroup of 16 waves forms the sums of all rows for itself (they come from the
 // caches) and then the gradients of 64 pieces of their columns, a wave a row.
+// fp32, one launch against two, in us: replayed in a graph 2 x 4096 3.6 and 5.2, 8 x
+// 4096 5.6 and 5.2, 17 x 2048 5.9 and 4.9, 64 x 2048 15.7 and 5.7; called one by one,
+// where a launch costs the host 4, 17 x 2064 10.6 and 14.9.
 constexpr int kFewRows = 64;
-constexpr int64_t kFewBytes = 512 * 1024;  // of H in fp32
+constexpr int64_t kFewElements = 48 * 1024;
 template <int IN>
 __global__ __launch_bounds__(1024) void rmsnorm_backward_few_kernel(NormGradArgs a) {
   constexpr int VEC = RowElem<IN>::VEC;
   using T = typename RowElem<IN>::type;
-  __shared__ float c[kFewRows];
+  __shared__ float c[kFewRows];  // of each row, or (fewer than 9) of each of its parts
   __shared__ float sums[16][VEC][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int nv = a.K / VEC, rows = (int)a.rows;
-  for (int row = wave; row < rows; row += 16) {
+  const int parts = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;
+  for (int item = wave; item < rows * parts; item += 16) {
+    const int row = item / parts;
     const v4i* dy = reinterpret_cast<const v4i*>((const T*)a.dY + (int64_t)row * a.K);
     const v4i* h = reinterpret_cast<const v4i*>((const T*)a.H + (int64_t)row * a.K);
     const float r = a.rstd[row];
     float dot = 0.0f;
 #pragma unroll 4
-    for (int i = lane; i < nv; i += 64) {
+    for (int i = item % parts * 64 + lane; i < nv; i += 64 * parts) {
       float f[VEC], g[VEC], w[VEC];
       unpack16<IN>(dy[i], g);
       unpack16<IN>(h[i], f);
@@ -497,7 +502,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_few_kernel(NormGradArgs
       for (int j = 0; j < VEC; j++) dot = fmaf(g[j] * w[j], f[j] * r, dot);
     }
     dot = wave_sum(dot);
-    if (lane == 0) c[row] = dot / (float)a.K;
+    if (lane == 0) c[item] = dot;
   }
   __syncthreads();
   const int i = blockIdx.x * 64 + lane;
@@ -511,7 +516,10 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_few_kernel(NormGradArgs
       unpack16<IN>(reinterpret_cast<const v4i*>((const T*)a.dY + base)[i], g);
       unpack16<IN>(reinterpret_cast<const v4i*>((const T*)a.H + base)[i], f);
       if (a.dH != nullptr) unpack16<IN>(reinterpret_cast<const v4i*>((const T*)a.dH + base)[i], o);
-      const float r = a.rstd[row], mean = c[row];
+      const float r = a.rstd[row];
+      float mean = 0.0f;
+      for (int p = 0; p < parts; p++) mean += c[row * parts + p];
+      mean /= (float)a.K;
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
         acc[j] = fmaf(g[j], f[j] * r, acc[j]);
@@ -531,7 +539,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_few_kernel(NormGradArgs
   a.dW[i * VEC + wave] = s;
 }
 
-bool few_rows(int64_t rows, int64_t K) { return rows <= kFewRows && rows * K * 4 <= kFewBytes; }
+bool few_rows(int64_t rows, int64_t K) { return rows <= kFewRows && rows * K <= kFewElements; }
 
 // Rows of partial sums: as many as workgroups that have two a CU (their traffic
 // is 1 / 16 of the rest at 8192 rows), or strips of the long rows' kernel.

@@ -703,6 +703,8 @@ def fp8gemm_weight_grad_grouped(d_c, a_q, a_s, offsets, index: torch.Tensor | No
     a_s = _arg(a_s, "a_s", (torch.float32,), (rows_a, _blocks(K)), like=d_c)
     offsets = _arg(offsets, "offsets", (torch.int32,), dim=1, like=d_c)
     E = offsets.shape[0] - 1
+    if E < 1:
+        raise ValueError("offsets must have an entry per expert and one more")
     if index is not None:
         index = _arg(index, "index", (torch.int32,), (rows,), like=d_c)
     elif rows_a < rows:

@@ -204,7 +204,8 @@ def test_norm_rows_past_4_gib():
 
 
 BACK = [(64, 2048), (65, 2048), (64, 16), (63, 2064), (1, 16), (3, 64), (5, 96), (7, 528), (33, 1024), (1, 4096), (17, 2064), (300, 608), (4, 8192), (3, 14336), (2, 32768),
-        (2, 65552), (1, 131072), (5000, 128), (2049, 4096), (257, 8208)]
+        (2, 65552), (1, 131072), (5000, 128), (2049, 4096), (257, 8208),
+        (1, 49152), (1, 49168), (2, 24576), (3, 16384), (8, 6144), (9, 5456), (24, 2048), (25, 2048), (64, 768), (65, 752), (2, 48)]
 
 
 @pytest.mark.parametrize("rows,K", BACK)
