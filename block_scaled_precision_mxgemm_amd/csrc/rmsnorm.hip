@@ -3,50 +3,53 @@
 //
 //   h = x + r, rounded to the rows' type (what the backward pass is given is
 //       what was normed);
-//   rstd = 1 / sqrt(sum_k h_k^2 / K + eps);   y_k = (h_k rstd) w_k in fp32;
+//   rstd = 1 / sqrt(sum_k h_k^2 / K + eps);   y_k = h_k rstd w_k, rounded to fp32;
 //   codes of y: int8 with a scale per row, E4M3 with one per 128 columns, or
 //   E4M3 with a UE8M0 scale per 32 (the rules of the three quantizers, applied
 //   to the fp32 values: y is not rounded to 16 bits in between).
 //
 // One pass over memory: a row is held in registers between its sum and its
-// codes.  Sums are in fp32: a lane's own, then over the lanes, then over the
-// waves of a row.
+// codes.  The squares are summed in 64 bits (those of 16-bit values exactly, and
+// whatever the lanes' share, the same rstd), the gradients' sums in fp32: a lane's
+// own, then over the lanes, then over the waves of a row.
 #include "mxg_codes.h"
 #include "mxg_internal.h"
 
 namespace mxg {
 namespace {
 
-__device__ __forceinline__ float wave_sum(float x) {
+template <class F>
+__device__ __forceinline__ F wave_sum(F x) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
   return x;
 }
 
 // Sum / largest over the L lanes of a row (all lanes of the workgroup that
-// belong to it call these); `part` is 16 words of LDS.
-template <int L>
-__device__ __forceinline__ float row_sum(float x, float* part) {
+// belong to it call these); `part` is 16 elements of LDS.
+template <int L, class F>
+__device__ __forceinline__ F row_sum(F x, F* part) {
   x = wave_sum(x);
   if constexpr (L > 64) {
     __syncthreads();  // what `part` held has been read
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
     __syncthreads();
-    x = 0.0f;
+    x = 0;
 #pragma unroll
     for (int w = 0; w < L / 64; w++) x += part[w];
   }
   return x;
 }
 template <int L>
-__device__ __forceinline__ uint32_t row_max(uint32_t x, float* part) {
+__device__ __forceinline__ uint32_t row_max(uint32_t x, double* sums) {
+  uint32_t* const part = reinterpret_cast<uint32_t*>(sums);
   x = lanes_max<64>(x);
   if constexpr (L > 64) {
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = __uint_as_float(x);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < L / 64; w++) x = max(x, __float_as_uint(part[w]));
+    for (int w = 0; w < L / 64; w++) x = max(x, part[w]);
   }
   return x;
 }
@@ -99,7 +102,7 @@ template <int IN, int HELD, int L>
 __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_kernel(NormArgs a) {
   constexpr int VEC = RowElem<IN>::VEC;
   using T = typename RowElem<IN>::type;
-  __shared__ float part[16];
+  __shared__ double part[16];
   const int64_t row = norm_row<L>(a.rows);
   if (row < 0) return;
   const int tid = threadIdx.x % L;
@@ -112,7 +115,7 @@ __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_kernel(NormArgs a) {
   const int steps = HELD > 0 ? HELD : (nv + L - 1) / L;
 
   // the rounded sum's piece i, with the sum of its squares
-  float sum = 0.0f;
+  double sum = 0.0;
   auto add = [&](int i, v4i w) {
     float f[VEC];
     unpack16<IN>(w, f);
@@ -126,7 +129,7 @@ __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_kernel(NormArgs a) {
       unpack16<IN>(w, f);
     }
 #pragma unroll
-    for (int j = 0; j < VEC; j++) sum = fmaf(f[j], f[j], sum);
+    for (int j = 0; j < VEC; j++) sum = fma((double)f[j], (double)f[j], sum);
     return w;
   };
   v4i held[HELD > 0 ? HELD : 1];
@@ -144,8 +147,13 @@ __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_kernel(NormArgs a) {
   } else {
     for (int i = tid; i < nv; i += L) add(i, x[i]);
   }
-  sum = row_sum<L>(sum, part);
-  const float rstd = 1.0f / sqrtf(sum / (float)a.K + a.eps);
+  // An error of rstd is the whole row's: in 64 bits, and y takes it and the rest of it, so
+  // that all of h rstd w is rounded once.  At 8192 x 8192 in MXFP8 codes 19 of 67 million
+  // are not those of the real y, which is what fp32 values leave; with sums in fp32 and
+  // y = (h rstd) w 46.  8192 x 4096 takes 41.6 us instead of 39.1, 8192 x 8192 92.5
+  // instead of 91.9.
+  const double exact = 1.0 / sqrt(row_sum<L>(sum, part) / a.K + (double)a.eps);
+  const float rstd = (float)exact, rest = rstd <= 3.0e38f ? (float)(exact - (double)rstd) : 0.0f;
   if (a.rstd != nullptr && tid == 0) a.rstd[row] = rstd;
 
   // y of step u (zeros past the row's end)
@@ -160,7 +168,11 @@ __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_kernel(NormArgs a) {
         unpack16<IN>(from[i], y);
       load_weights<VEC>(a.W, a.w_type, i * VEC, w);
 #pragma unroll
-      for (int j = 0; j < VEC; j++) y[j] = y[j] * rstd * w[j];
+      for (int j = 0; j < VEC; j++) {
+        const float p = y[j] * rstd;
+        const float low = fmaf(y[j], rest, fmaf(y[j], rstd, -p));  // h rstd - p
+        y[j] = fmaf(p, w[j], low * w[j]);
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < VEC; j++) y[j] = 0.0f;

@@ -630,7 +630,7 @@ int fp8gemm_weight_grad_grouped(const void *dC, int c_type, int64_t rows,
  * it and codes for the products as its output:
  *   H    = X + R in fp32, rounded to their type (R == NULL: H is X);
  *   rstd = 1 / sqrt(sum_k H[r][k]^2 / K + eps);
- *   y    = (H * rstd) * W in fp32;
+ *   y    = H * W / sqrt(that), rounded to fp32 (squares are summed in 64 bits);
  *   Q, S = codes of y by the rule of the quantizer that `quant` names, from the fp32
  *          values; Y = y rounded to the rows' type.
  *

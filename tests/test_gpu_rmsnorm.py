@@ -307,3 +307,21 @@ def test_binding_refusals():
                  lambda: bn.rmsnorm_quantize(x, w, quant=1, q=q), lambda: bn.rmsnorm_backward(x.half(), x, w, w[:4])):
         with pytest.raises(TypeError):
             call()
+
+
+@pytest.mark.parametrize("rows,K", [(64, 256), (33, 4096), (9, 8192), (5, 16416), (3, 131072)])
+@pytest.mark.parametrize("kind", [1, 2])
+def test_rstd_and_y_are_rounded_once(rows, K, kind):
+    """16-bit rows: the sum of the squares is exact in 64 bits up to 2^-52 a term of it,
+    so rstd is the fp32 value next to the real one (2^-40 of a step apart at most), and
+    so is y: its product with the rest of rstd has 2^-47."""
+    say("norm rounded once", rows, K, kind)
+    g = gen(K)
+    x, w = randn(g, rows, K).to(TYPES[kind]), randn(g, K).to(TYPES[kind]).float()
+    _, _, _, y, rstd = binding().rmsnorm_quantize(x, w, quant=0)
+    real, _ = ref.norm(x, w, 1e-6)
+    assert bool(((rstd.double() - real).abs() <= real * (U * (1 + 2.0 ** -16))).all())
+    # fp32 rows, so that y is seen as it is
+    _, _, _, y, rstd = binding().rmsnorm_quantize(x.float(), w, quant=0)
+    want = x.double() * ref.norm(x.float(), w, 1e-6)[0][:, None] * w.double()
+    assert bool(((y.double() - want).abs() <= want.abs() * (U * (1 + 2.0 ** -16)) + 2.0 ** -149).all())
