@@ -351,19 +351,31 @@ __global__ __launch_bounds__(256) void rmsnorm_dweight_kernel(NormGradArgs a, in
     *reinterpret_cast<v4f*>(p + 4 * j) = v4f{acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]};
 }
 
-// 64 columns a workgroup: 16 lanes of 4 columns, 16 of them at a time over the strips.
-__global__ __launch_bounds__(256) void rmsnorm_dweight_sum_kernel(const float* part, int strips, int K, float* dW) {
-  __shared__ __attribute__((aligned(16))) v4f sums[256];
-  const int k = blockIdx.x * 64 + (threadIdx.x & 15) * 4;
+// 32 columns a workgroup: 8 lanes of 4 columns, 8 WAVES of them at a time over the
+// strips; 16 waves above 64 strips, else 2 (the whole backward pass of
+// 8191 x 4096 53.3 us, 59.4 with 4 waves on 64 columns; of 1 x 131072 26.9 with 2 waves,
+// 37.1 with 16).
+template <int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void rmsnorm_dweight_sum_kernel(const float* part, int strips, int K, float* dW) {
+  __shared__ __attribute__((aligned(16))) v4f sums[WAVES][8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int k = blockIdx.x * 32 + (lane & 7) * 4;
   v4f s = {0, 0, 0, 0};
   if (k < K) {
-    for (int i = threadIdx.x >> 4; i < strips; i += 16) s += *reinterpret_cast<const v4f*>(part + (int64_t)i * K + k);
+#pragma unroll 4
+    for (int i = threadIdx.x >> 3; i < strips; i += WAVES * 8) s += *reinterpret_cast<const v4f*>(part + (int64_t)i * K + k);
   }
-  sums[threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.x < 16 && k < K) {
 #pragma unroll
-    for (int i = 1; i < 16; i++) s += sums[threadIdx.x + 16 * i];
+  for (int d = 8; d < 64; d <<= 1) {
+#pragma unroll
+    for (int x = 0; x < 4; x++) s[x] += __shfl_xor(s[x], d);
+  }
+  if (lane < 8) sums[wave][lane] = s;
+  __syncthreads();
+  if (threadIdx.x < 8 && k < K) {
+    s = sums[0][lane];
+#pragma unroll
+    for (int i = 1; i < WAVES; i++) s += sums[i][lane];
     *reinterpret_cast<v4f*>(dW + k) = s;
   }
 }
@@ -485,7 +497,7 @@ __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_backward_fused_kernel
 // workgroup of 16 waves forms the sums of all rows for itself (they come from the
 // caches) and then the gradients of 64 pieces of their columns, a wave a row.
 // fp32, one launch against two, in us: replayed in a graph 2 x 4096 3.6 and 5.2, 8 x
-// 4096 5.6 and 5.2, 17 x 2048 5.9 and 4.9, 64 x 2048 15.7 and 5.7; called one by one,
+// 4096 5.6 and 5.4, 17 x 2048 5.8 and 4.8, 64 x 2048 15.7 and 4.7; called one by one,
 // where a launch costs the host 4, 17 x 2064 10.6 and 14.9.
 constexpr int kFewRows = 64;
 constexpr int64_t kFewElements = 48 * 1024;
@@ -551,6 +563,14 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_few_kernel(NormGradArgs
   a.dW[i * VEC + wave] = s;
 }
 
+void sum_strips(const float* part, int strips, const NormGradArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.K + 31) / 32));
+  if (strips > 64)
+    hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel<16>, grid, dim3(1024), 0, stream, part, strips, a.K, a.dW);
+  else
+    hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel<2>, grid, dim3(128), 0, stream, part, strips, a.K, a.dW);
+}
+
 bool few_rows(int64_t rows, int64_t K) { return rows <= kFewRows && rows * K <= kFewElements; }
 
 // Rows of partial sums: as many as workgroups that have two a CU (their traffic
@@ -567,9 +587,7 @@ void backward_fused(const NormGradArgs& a, hipStream_t stream) {
   // one workgroup's sums are the result
   hipLaunchKernelGGL((rmsnorm_backward_fused_kernel<IN, HELD, L>), dim3((unsigned)grid), dim3(norm_threads(L)), 0, stream, a,
                      grid == 1 ? a.dW : part);
-  if (grid > 1)
-    hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel, dim3((unsigned)((a.K + 63) / 64)), dim3(256), 0, stream, part, grid, a.K,
-                       a.dW);
+  if (grid > 1) sum_strips(part, grid, a, stream);
 }
 
 template <int IN>
@@ -592,8 +610,7 @@ void backward_in(const NormGradArgs& a, hipStream_t stream) {
   const int used = (int)((a.rows + strip - 1) / strip);
   hipLaunchKernelGGL((rmsnorm_dweight_kernel<IN>), dim3((unsigned)((pieces + 255) / 256), (unsigned)used), dim3(256), 0,
                      stream, a, strip, part);
-  hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel, dim3((unsigned)((a.K + 63) / 64)), dim3(256), 0, stream, part, used, a.K,
-                     a.dW);
+  sum_strips(part, used, a, stream);
   const int64_t most = 1 << 20;
   const dim3 grid((unsigned)(a.rows < most ? a.rows : most), (unsigned)((a.rows + most - 1) / most));
   if (pieces <= 4 * 1024)
