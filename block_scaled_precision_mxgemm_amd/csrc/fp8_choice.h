@@ -82,14 +82,17 @@ inline int f8_choice(int64_t M, int64_t N, int64_t K, int64_t E) {
 // launch and the partial sums' bytes take.  Measured, in us (fp32 result; * what is
 // taken):
 //                                       bf16: 256  128   in 2  in 8    fp16: large  128   in 2  in 8
-//   2047 x 4100 x 2064                    69.4*  77.0  87.1   160          117*   149   139   195
-//   8192 x 4096 x 4096                     242*   332   374   568          466*   717   757   920
-//   16384 x 1024 x 1024                    442    235   124  55.1*         724    535   274   103*
-//   16384 x 256 x 512                      437    232   121  38.3*         717    530   269  75.8*  (in 32: 30 and 40)
-//   4096 x 2048 x 2048                     118   63.3  57.4* 88.3          187    138   105*  135
-//   512 x 4096 x 4096                     33.9*  31.7  82.7   279         48.6*  55.6  99.9   287
-//   4096 x 4 rows of 16 of 4096 x 2048     379*   465                      605*   887
-//   4096 x 2 rows of 4 of 512 x 512       71.7   42.0                      111   79.8               (in 4: 28 and 36)
+//   2047 x 4100 x 2064                    64.2*  76.2  88.4   166          114*   126   123   165
+//   8192 x 4096 x 4096                     229*   306   342   507          459*   664   649   743
+//   16384 x 1024 x 1024                    409    224   118  50.8*         705    545   278   101*
+//   16384 x 256 x 512                      408    221   114  36.3          701    543   275  76.6   (* in 32: 30 and 40)
+//   4096 x 2048 x 2048                     108   59.3*  52.5  79.4         181    140   103*  113
+//   2048 x 512 x 512                      56.1   30.7  19.9  14.2*         92.0   71.0  40.0  19.4   (* fp16 in 16)
+//   512 x 4096 x 4096                     25.9*  28.0  70.3   214         40.4*  48.0  82.0   203
+//   4096 x 4 rows of 16 of 4096 x 2048     326*   439                      570*   688
+//   4096 x 4 rows of 32 of 2048 x 1024     122*   146                      168*   198
+//   4096 x 2 rows of 4 of 512 x 512       64.2   42.6                      111   81.3   (* in 4: 28 and 36)
+//   300 x 2 rows of 8 of 1024 x 1024      16.6   12.9*                    15.2   12.7*
 constexpr int kGradCus = 256;
 
 struct GradChoice {

@@ -137,8 +137,9 @@ __device__ __forceinline__ v8i fragment(const uint8_t* p, int sw) {
 // start of a block on, and the first half of a wave's columns has been read in its
 // middle.  A barrier there lets the copies of the block after the next go
 // out: A and the first halves into the buffers that are left, the second halves
-// into a third buffer (8192 x 14336 x 4096: 470 us with the copies behind the one
-// barrier).
+// into a third buffer.  8192 x 14336 x 4096 to bf16 takes 443 us so (2170 TFLOP/s; 470
+// with the copies behind the one barrier); MFMAs and fmas alone 283, with the LDS
+// reads 326, with the barriers 338, and with the copies 431 (of 8192 x 4096 x 14336).
 //
 // A workgroup takes tile after tile; the first blocks of the next tile are
 // copied while the last ones of the present tile are multiplied, and the output
@@ -646,7 +647,8 @@ hipError_t launch_ring(const F8Args& a, hipStream_t stream) {
 // holds KW blocks, one for each group of waves, and each wave's copy of the
 // scales of A for its block; D stages are in flight or in use, so that a CU
 // keeps most of its LDS of memory requests going, which is what bounds such
-// products.  The groups' sums are added through LDS at the end.
+// products (16 x 28672 x 8192: 235 MB in 39 us, 47.6 in changing calls through Python,
+// 4.9 TB/s).  The groups' sums are added through LDS at the end.
 template <int MB_, int CW_, int KW_, int D_>
 struct F8Few {
   static constexpr int MB = MB_, CW = CW_, KW = KW_, D = D_;

