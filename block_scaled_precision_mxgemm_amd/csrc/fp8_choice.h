@@ -75,7 +75,7 @@ inline int f8_choice(int64_t M, int64_t N, int64_t K, int64_t E) {
 
 // ---- weight gradients ---------------------------------------------------------
 //
-// Tiles of 256 x 256 (one workgroup a CU; with dY in two terms 256 x 128, two a CU)
+// Tiles of 256 x 256 (one workgroup a CU; with dY in two or three terms 256 x 128, two a CU)
 // or of 128 x 128 (two a CU), the latter with the rows in up to 64 parts whose
 // sums are added by a second kernel.  The estimate: rounds x (slices of 64 rows x us
 // + extra), with a CU to itself `alone` instead of `us`; and for parts what a
@@ -104,8 +104,9 @@ inline GradChoice grad_choice(int64_t M, int64_t N, int64_t K, int64_t E, int te
   auto estimate = [&](bool large, int splits) {
     const int bn = large && terms == 1 ? 256 : 128, bk = large ? 256 : 128;
     const int per_cu = large && terms == 1 ? 1 : 2;
-    const double us = large ? (terms == 1 ? 1.75 : 3.6) : (terms == 1 ? 1.3 : 2.8);
-    const double alone = large ? (terms == 1 ? 1.75 : 2.8) : (terms == 1 ? 0.91 : 2.1);
+    const double more = terms == 3 ? 1.4 : 1.0;
+    const double us = more * (large ? (terms == 1 ? 1.75 : 3.6) : (terms == 1 ? 1.3 : 2.8));
+    const double alone = more * (large ? (terms == 1 ? 1.75 : 2.8) : (terms == 1 ? 0.91 : 2.1));
     const double extra = large ? 10.0 : 5.0;
     const double tiles = (double)((N + bn - 1) / bn) * (double)((K + bk - 1) / bk) * (double)E * splits;
     const double full = tiles / (kGradCus * per_cu);

@@ -6,9 +6,8 @@
 //
 // Products of bf16 values on the bf16 MFMA, summed in fp32.  x is rounded to
 // bf16: exact where s is a power of two (a code has 4 significant bits).  dY in
-// fp16 or fp32 is taken as the sum of two bf16 values (TERMS = 2), its nearest
-// one and that of the rest: exact for fp16 of at least 2^-10, within 2^-17 of the
-// value for fp32.
+// fp16 is taken as the sum of two bf16 values (TERMS = 2), its nearest one and that of
+// the rest (11 bits are 8 and 3), in fp32 as that of three (24 bits).
 //
 // Both operands are contracted over their rows, so that a lane's 8 elements of
 // an MFMA operand are a column of LDS: ds_read_b64_tr_b16 reads 4 rows of 16
@@ -39,7 +38,7 @@ typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return bf16_bits(a) | (bf16_bits(b) << 16); }
 
-// bf16 bits of f, and what they leave of it.  A finite value beyond bf16's range is
+// bf16 bits of f, and what they leave of it (exactly).  A finite value beyond bf16's range is
 // cut off instead of rounded; infinities and NaNs leave nothing.
 __device__ __forceinline__ uint32_t split_bf16(float& f) {
   uint32_t h = bf16_bits(f);
@@ -249,7 +248,7 @@ struct Grad {
 #pragma unroll
     for (int u = 0; u < T::CY; u++) {
       if constexpr (TERMS == 1) {
-        y[u][0] = h.y[u][0];
+        y[u][0] = h.y[u][0];  // bf16 as it is
       } else {
         float f[8];
         if constexpr (IN == kOutF32) {
@@ -260,8 +259,9 @@ struct Grad {
         }
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          y[u][0][j] = (int)(split_bf16(f[2 * j]) | (split_bf16(f[2 * j + 1]) << 16));
-          y[u][1][j] = (int)pack_bf16(f[2 * j], f[2 * j + 1]);
+#pragma unroll
+          for (int v = 0; v < TERMS - 1; v++) y[u][v][j] = (int)(split_bf16(f[2 * j]) | (split_bf16(f[2 * j + 1]) << 16));
+          y[u][TERMS - 1][j] = (int)pack_bf16(f[2 * j], f[2 * j + 1]);
         }
       }
     }
@@ -543,9 +543,9 @@ hipError_t launch_tiles(const F8GradArgs& a, int splits, hipStream_t stream) {
 
 template <int IN>
 hipError_t launch_in(const F8GradArgs& a, hipStream_t stream) {
-  constexpr int TERMS = IN == kOutBF16 ? 1 : 2;
-  // (two workgroups a CU where dY is two terms)
-  using Large = typename std::conditional<TERMS == 1, GradCfg<256, 256, 4, 2, 1, 64>, GradCfg<256, 128, 4, 1, 2, 32>>::type;
+  constexpr int TERMS = IN == kOutBF16 ? 1 : IN == kOutF16 ? 2 : 3;
+  // (two workgroups a CU where dY is more than one term)
+  using Large = typename std::conditional<TERMS == 1, GradCfg<256, 256, 4, 2, 1, 64>, GradCfg<256, 128, 4, 1, TERMS, 32>>::type;
   using Small = GradCfg<128, 128, 2, 2, TERMS, TERMS == 1 ? 64 : 32>;
   const GradChoice c = grad_choice(a.M, a.N, a.K, a.E, TERMS);
   if (c.large) return launch_tiles<IN, Large>(a, 1, stream);
@@ -562,7 +562,7 @@ hipError_t launch_in(const F8GradArgs& a, hipStream_t stream) {
 // The workspace is as large for any type of dY.
 int64_t fp8_weight_grad_bytes(int64_t M, int64_t N, int64_t K, int64_t E) {
   int64_t most = 0;
-  for (int terms = 1; terms <= 2; terms++) {
+  for (int terms = 1; terms <= 3; terms++) {
     const GradChoice c = grad_choice(M, N, K, E, terms);
     if (c.splits > 1 && c.splits * E * N * K * 4 > most) most = c.splits * E * N * K * 4;
   }

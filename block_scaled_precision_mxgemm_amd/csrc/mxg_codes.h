@@ -55,9 +55,18 @@ __device__ __forceinline__ float block_scale(uint32_t amax, bool pow2) {
   const float s = fmaxf(__uint_as_float(amax) / 448.0f, 0x1p-126f);
   return pow2 ? __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u) : s;
 }
-// What the block's values are multiplied by: 1 / s in fp32, and 0 where s is 0
-// or NaN.
+// 1 / s in fp32, and 0 where s is 0 or NaN.
 __device__ __forceinline__ float block_inverse(float s) { return s > 0.0f ? 1.0f / s : 0.0f; }
+
+// x / s rounded to fp32, from inv = fl32(1 / s): the quotient x inv corrected by its
+// remainder, which an fma gives exactly, is the nearest one (P. Markstein,
+// Computation of elementary functions on the IBM RISC System/6000 processor, 1990).
+// For s of at least 2^-60, where only quotients far below the smallest code have a
+// remainder below fp32's range.  A zero keeps its sign.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  const float t = x * inv;
+  return fmaf(-fmaf(s, t, -x), inv, t);
+}
 
 // E4M3 codes of 4 values: nearest, ties to even, saturated to +-448.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -68,15 +77,28 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
-// The codes f * inv of N values in N / 4 words; `live` false: zeros (a block
-// that holds NaNs or infinities).
+// The codes of N values in N / 4 words; `live` false: zeros (a block that holds NaNs
+// or infinities).
 template <int N>
-__device__ __forceinline__ void e4m3_codes(const float (&f)[N], float inv, bool live, uint32_t (&c)[N / 4]) {
+__device__ __forceinline__ void e4m3_codes(const float (&f)[N], bool live, uint32_t (&c)[N / 4]) {
 #pragma unroll
   for (int i = 0; i < N / 4; i++) {
-    const uint32_t v = e4m3x4(f[4 * i] * inv, f[4 * i + 1] * inv, f[4 * i + 2] * inv, f[4 * i + 3] * inv);
+    const uint32_t v = e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
     c[i] = live ? v : 0u;
   }
+}
+// Those of f / s, s and inv the block's scale and its inverse.
+template <int N>
+__device__ __forceinline__ void e4m3_block_codes(const float (&f)[N], float s, float inv, uint32_t (&c)[N / 4]) {
+  float t[N];
+  if (inv > 0x1p60f) {
+#pragma unroll
+    for (int i = 0; i < N; i++) t[i] = f[i] / s;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i++) t[i] = quotient(f[i], s, inv);
+  }
+  e4m3_codes<N>(t, s == s, c);
 }
 
 // Largest of a value over groups of L consecutive lanes (L = 4 .. 64), by register

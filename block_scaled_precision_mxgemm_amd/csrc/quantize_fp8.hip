@@ -2,8 +2,8 @@
 // per row and 128 columns (activations) or per 128 x 128 block (weights).
 //
 // Rule: s from the block's largest magnitude (block_scale in mxg_codes.h);
-// code = x * fl32(1 / s), rounded to the nearest E4M3 value, ties to even,
-// saturated to +-448.  A block that holds a NaN or an infinity gets s = NaN and
+// code = fl32(x / s) rounded to the nearest E4M3 value, ties to even, saturated to
+// +-448.  A block that holds a NaN or an infinity gets s = NaN and
 // zero codes, as a block of the MX quantizer does.
 //
 // Both kernels hold a block in registers between its maximum and its codes, so
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256) void quantize_fp8_rows_kernel(const typename R
     unpack16<IN>(w[u], f);
     const uint32_t amax = lanes_max<L>(magnitude_bits<VEC>(f));
     const float s = block_scale(amax, pow2), inv = block_inverse(s);
-    e4m3_codes<VEC>(f, inv, s == s, c);
+    e4m3_block_codes<VEC>(f, s, inv, c);
     if (at[u] >= 0) store_codes<VEC>(Q + at[u], c);
     if (b < total && sub == 0) S[b] = s;
   }
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(512) void quantize_fp8_blocks_kernel(const typename
       float f[VEC];
       uint32_t c[VEC / 4];
       unpack16<IN>(w[u], f);
-      e4m3_codes<VEC>(f, inv, s == s, c);
+      e4m3_block_codes<VEC>(f, s, inv, c);
       store_codes<VEC>(Q + base + (int64_t)row * K + k, c);
     }
   }

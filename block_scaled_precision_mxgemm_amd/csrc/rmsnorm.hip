@@ -221,14 +221,13 @@ __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_kernel(NormArgs a) {
       const int exponent = amax == 0u ? -127 : min(max(__builtin_amdgcn_frexp_expf(__uint_as_float(amax)) - 9, -127), 127);
 #pragma unroll
       for (int j = 0; j < VEC; j++) y[j] = ldexpf(y[j], -exponent);
-      e4m3_codes<VEC>(y, 1.0f, !bad, c);
+      e4m3_codes<VEC>(y, !bad, c);
       if (valid && i % LB == 0)
         reinterpret_cast<uint8_t*>(a.S)[row * (a.K / 32) + i / LB] = bad ? (uint8_t)255 : (uint8_t)(exponent + 127);
     } else if (a.quant != kQuantNone) {
       constexpr int LB = kBlock / VEC;
       const float sb = block_scale(lanes_max<LB>(magnitude_bits<VEC>(y)), a.quant == kQuantFp8Pow2);
-      const float ib = block_inverse(sb);
-      e4m3_codes<VEC>(y, ib, sb == sb, c);
+      e4m3_block_codes<VEC>(y, sb, block_inverse(sb), c);
       if (valid && i % LB == 0) reinterpret_cast<float*>(a.S)[row * KB + i / LB] = sb;
     }
     if (a.quant != kQuantNone && valid) store_codes<VEC>(q + (int64_t)i * VEC, c);

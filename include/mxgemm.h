@@ -509,7 +509,7 @@ int expert_combine_backward(const void *dOut, int out_type, const void *Y,
  *   s    = amax / 448 in fp32 (amax: its largest magnitude), at least 2^-126 when
  *          amax > 0; with pow2 the next power of two that is not smaller; 0 when
  *          amax = 0;
- *   code = x * (1 / s), each in fp32, rounded to the nearest E4M3 value, ties to
+ *   code = x / s in fp32, rounded to the nearest E4M3 value, ties to
  *          even, saturated to +-448; the sign is kept (-0 -> 0x80).
  * A block holding a NaN or an infinity gets s = NaN and zero codes.  Values with
  * pow2 scales are bf16 values (fp8gemm_weight_grad).
@@ -584,7 +584,7 @@ int fp8gemm_run_grouped(const uint8_t *A, const float *scaleA, int64_t rowsA,
  * * A[m][k] rounded to bf16 (exact for scales that are powers of two, as
  * fp8gemm_quantize and rmsnorm_quantize give with pow2).  Sums in fp32 on the
  * bf16 MFMA, rounded once to out_type; dC in fp16 or fp32 goes in as the sum of two
- * bf16 values (exact for fp16 of at least 2^-10, else within 2^-17 of a value).
+ * or of three bf16 values.
  * The gradient is that of the dequantized activations.
  *
  *   dC         device, M x N elements of c_type, 16-byte aligned

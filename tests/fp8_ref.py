@@ -65,8 +65,8 @@ def quantize(x, block_rows=1, pow2=False):
     bad = block_amax((~torch.isfinite(x)).float(), block_rows) > 0
     amax = block_amax(torch.where(torch.isfinite(x), x, torch.zeros_like(x)), block_rows)
     s = scale_of(amax, pow2)
-    inv = torch.where((s > 0) & ~bad, divide(torch.ones_like(s), s), torch.zeros_like(s))
-    t = torch.where(torch.isfinite(x), x, torch.zeros_like(x)) * expand(inv, rows, K, block_rows)
+    by = expand(torch.where((s > 0) & ~bad, s, torch.ones_like(s)), rows, K, block_rows)
+    t = divide(torch.where(torch.isfinite(x), x, torch.zeros_like(x)), by)
     q = encode(t.double())
     q = torch.where(expand(bad.to(torch.uint8), rows, K, block_rows) != 0, torch.zeros_like(q), q)
     return q, torch.where(bad, torch.full_like(s, float("nan")), s)

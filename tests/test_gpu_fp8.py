@@ -85,6 +85,38 @@ def test_quantize_borders(kind, block_rows):
         assert torch.equal(q, q_r)
 
 
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_next_to_ties(block_rows):
+    """fp32 values that are a few steps from a tie of two codes, for scales of any
+    mantissa and of every size."""
+    say("fp8 quantize next to ties", block_rows)
+    v = ref.values().to(DEV)
+    ties = (v[1:] + v[:-1]) / 2
+    blocks = 6 * 250
+    g = gen(block_rows)
+    exponent = torch.arange(250, device=DEV).repeat(6) - 125
+    amax = torch.ldexp(1 + torch.rand(blocks, generator=g, device=DEV), exponent)
+    s = ref.scale_of(amax, False).double()
+    x = torch.zeros(blocks, 128, device=DEV)
+    at = torch.randint(0, 126, (blocks, 127), generator=g, device=DEV)
+    near = (ties[at] * s[:, None]).float()
+    step = torch.randint(-2, 3, (blocks, 127), generator=g, device=DEV)
+    for _ in range(2):
+        near = torch.where(step > 0, torch.nextafter(near, near + 1e30), torch.where(step < 0, torch.nextafter(near, -near), near))
+        step = step - step.sign()
+    x[:, 1:] = near * torch.where(torch.rand(blocks, 127, generator=g, device=DEV) < 0.5, -1.0, 1.0)
+    x = torch.minimum(torch.maximum(x, -amax[:, None]), amax[:, None])
+    x[:, 0] = amax
+    if block_rows == 128:
+        full = torch.zeros(blocks, 128, 128, device=DEV)
+        full[:, 77] = x
+        x = full.view(blocks * 128, 128)
+    q, scale = binding().fp8gemm_quantize(x, block_rows)
+    q_r, s_r = ref.quantize(x, block_rows)
+    assert torch.equal(scale, s_r)
+    assert torch.equal(q, q_r)
+
+
 def test_quantize_experts():
     say("fp8 quantize experts")
     for block_rows in (1, 128):
