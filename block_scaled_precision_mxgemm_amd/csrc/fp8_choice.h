@@ -81,18 +81,17 @@ inline int f8_choice(int64_t M, int64_t N, int64_t K, int64_t E) {
 // + extra), with a CU to itself `alone` instead of `us`; and for parts what a
 // launch and the partial sums' bytes take.  Measured, in us (fp32 result; * what is
 // taken):
-//                                       bf16: 256  128   in 2  in 8    fp16: large  128   in 2  in 8
-//   2047 x 4100 x 2064                    64.2*  76.2  88.4   166          114*   126   123   165
-//   8192 x 4096 x 4096                     229*   306   342   507          459*   664   649   743
-//   16384 x 1024 x 1024                    409    224   118  50.8*         705    545   278   101*
-//   16384 x 256 x 512                      408    221   114  36.3          701    543   275  76.6   (* in 32: 30 and 40)
-//   4096 x 2048 x 2048                     108   59.3*  52.5  79.4         181    140   103*  113
-//   2048 x 512 x 512                      56.1   30.7  19.9  14.2*         92.0   71.0  40.0  19.4   (* fp16 in 16)
-//   512 x 4096 x 4096                     25.9*  28.0  70.3   214         40.4*  48.0  82.0   203
-//   4096 x 4 rows of 16 of 4096 x 2048     326*   439                      570*   688
-//   4096 x 4 rows of 32 of 2048 x 1024     122*   146                      168*   198
-//   4096 x 2 rows of 4 of 512 x 512       64.2   42.6                      111   81.3   (* in 4: 28 and 36)
-//   300 x 2 rows of 8 of 1024 x 1024      16.6   12.9*                    15.2   12.7*
+//                              bf16: 256   128  in 2  in 8   fp16: large   128  in 2  in 8   fp32: large   128  in 2  in 8
+//   2047 x 4100 x 2064             64.2*  76.2  88.4   166           114*   126   123   165           180*   228   201   241
+//   8192 x 4096 x 4096              229*   306   342   507           459*   664   649   743           719*  1059  1077  1172
+//   16384 x 1024 x 1024             409    224   118  50.8*          705    545   278   101*         1075    810   411   147*
+//   4096 x 2048 x 2048              108   59.3*  52.5  79.4          181    140   103*  113           274    207   148*  169
+//   512 x 4096 x 4096              25.9*  28.0  70.3   214          40.4*  48.0  82.0   203          53.8*  74.2   111   229
+//   4096 x 4 of 16 of 4096 x 2048   326*   439                       570*   688                       830*  1159
+//   4096 x 4 of 32 of 2048 x 1024   122*   146                       168*   198                       236*   320
+//   300 x 2 of 8 of 1024 x 1024    16.6   12.9*                     15.2   12.7*                     16.9   14.7*
+//   (rows x columns of dY x columns of the codes; tokens x choices of experts of N x K)
+//   16384 x 256 x 512 in 32 parts (fp32: 64) 29, 39 and 54; 4096 x 2 of 4 of 512 x 512 in 4 (8) 23, 30 and 35
 constexpr int kGradCus = 256;
 
 struct GradChoice {
@@ -104,7 +103,7 @@ inline GradChoice grad_choice(int64_t M, int64_t N, int64_t K, int64_t E, int te
   auto estimate = [&](bool large, int splits) {
     const int bn = large && terms == 1 ? 256 : 128, bk = large ? 256 : 128;
     const int per_cu = large && terms == 1 ? 1 : 2;
-    const double more = terms == 3 ? 1.4 : 1.0;
+    const double more = terms == 3 ? 1.5 : 1.0;
     const double us = more * (large ? (terms == 1 ? 1.75 : 3.6) : (terms == 1 ? 1.3 : 2.8));
     const double alone = more * (large ? (terms == 1 ? 1.75 : 2.8) : (terms == 1 ? 0.91 : 2.1));
     const double extra = large ? 10.0 : 5.0;
