@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import fp8_ref as ref
-from gpu_util import binding, say
+from gpu_util import binding, poison_lds, say
 from test_gpu_fp8 import DEV, TYPES, U, exact_codes, gen, randn
 
 pytestmark = pytest.mark.gpu
@@ -327,3 +327,25 @@ def test_expert_layer_step():
             assert ((d_down[i].double() - want).norm() / want.norm()).item() < 2.0 ** -20
             want = h[at].double().t() @ xe
             assert ((d_up[i].double() - want).norm() / want.norm()).item() < 2.0 ** -20
+
+
+# rows of experts: none, part of a slice of 64, odd and even numbers of slices
+COUNTS = [0, 1, 64, 500, 65, 448, 449, 512, 0, 513, 576, 577, 640, 129, 1000, 128, 1024, 1, 700, 192, 193, 0]
+
+
+@pytest.mark.parametrize("N,K", [(1010, 1264), (1024, 1280), (2020, 992), (300, 400)])
+@pytest.mark.parametrize("kind,out", [(1, 0), (1, 1), (1, 2), (0, 0), (2, 1)])
+@pytest.mark.parametrize("gather", [True, False])
+def test_experts_of_every_size(N, K, kind, out, gather):
+    say("weight grad experts of every size", N, K, kind, out, gather)
+    g = gen(N + K)
+    E, rows, T = len(COUNTS), sum(COUNTS), 900
+    offsets = torch.tensor([0] + COUNTS, device=DEV).cumsum(0).int()
+    a, a_s = exact_codes(g, T if gather else rows, K)
+    index = torch.randint(0, 3 * T, (rows,), generator=g, device=DEV).int() if gather else None
+    d = exact_d(g, rows, N, kind)
+    want = expert_grad(d, a, a_s, offsets, index, 3, E)
+    poison_lds()
+    got = torch.full((E, N, K), float("nan"), dtype=TYPES[out], device=DEV)
+    binding().fp8gemm_weight_grad_grouped(d, a, a_s, offsets, index=index, index_div=3, out=got, out_type=out)
+    assert torch.equal(got, want.float().to(TYPES[out]))
