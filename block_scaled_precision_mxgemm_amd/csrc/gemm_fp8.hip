@@ -129,8 +129,10 @@ __device__ __forceinline__ v8i fragment(const uint8_t* p, int sw) {
 // codes, without the fmas 4200.  The fragments of B are read two columns ahead,
 // those of A for the next block behind the last column's MFMAs.
 //
-// What bounds the loop is the time from a copy's issue to its arrival (about
-// 1.5 us with the chip full).  A barrier behind the column before the last says
+// What bounds the loop is LDS: a block of 256 x 256 is 2048 cycles of MFMAs on each
+// SIMD, for which the waves read 192 KB and the copies write 64 KB, at 128 bytes a
+// cycle as many cycles; and a copy takes about 1.5 us to arrive with the chip full.
+// A barrier behind the column before the last says
 // that the next block has arrived.  Where D > 2 blocks fit, it also says that the
 // block at hand has been read, and copies of D blocks later take its place.
 // SPLIT (256 x 256, where D = 2): A's fragments are in registers from the

@@ -227,3 +227,26 @@ def test_more_tiles_than_a_launch_has_threads():
         y = ref.dequantize(b[e], b_s[e], 128) @ ref.dequantize(a[p:p + 1], a_s[p:p + 1])[0]
         assert torch.equal(got[p], y.float().bfloat16())
     assert bool(torch.isfinite(got).all()) and int((got == 0).all(-1).sum()) == 0
+
+
+@pytest.mark.parametrize("tile,M,N,K", [("256x128", 2 ** 20, 300, 4224), ("16x32", 16, 2 ** 20, 4224), ("256x256", 2 ** 17 + 9, 20000, 400)])
+def test_operands_past_4_gib(tile, M, N, K):
+    """A, B and C of more than 4 GiB."""
+    say("fp8 large past 4 GiB", tile, M, N, K)
+    assert load_choice()(M, N, K) == tile
+    g = gen(K + N)
+
+    def operand(rows, block_rows):
+        q = torch.randint(0, 4, (rows, K), generator=g, device=DEV, dtype=torch.uint8).mul_(4).add_(0x30)   # 0.5 .. 1.5
+        s = torch.exp2(torch.randint(0, 2, (-(-rows // block_rows), -(-K // 128)), generator=g, device=DEV).float())
+        return q, s
+
+    (a, a_s), (b, b_s) = operand(M, 1), operand(N, 128)
+    got = binding().fp8gemm_run(a, a_s, b, b_s, out_type=1)
+    # sums of multiples of 1 / 16 below 2^16: exact in fp32
+    rows = torch.tensor([0, M // 2 + 1, M - 2, M - 1], device=DEV)
+    for n0 in sorted({0, max(0, N // 256 * 128 - 128), (N - 1) // 128 * 128}):
+        cols = slice(n0, min(n0 + 128, N))
+        want = ref.dequantize(a[rows], a_s[rows]) @ ref.dequantize(b[cols], b_s[n0 // 128:n0 // 128 + 1], 128).t()
+        assert torch.equal(got[rows, cols], want.float().bfloat16())
+    assert bool(torch.isfinite(got).all()) and not bool((got == 0).any())
