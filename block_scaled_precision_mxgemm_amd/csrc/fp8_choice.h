@@ -91,7 +91,8 @@ inline int f8_choice(int64_t M, int64_t N, int64_t K, int64_t E) {
 //   4096 x 4 of 32 of 2048 x 1024   122*   146                       168*   198                       236*   320
 //   300 x 2 of 8 of 1024 x 1024    16.6   12.9*                     15.2   12.7*                     16.9   14.7*
 //   (rows x columns of dY x columns of the codes; tokens x choices of experts of N x K)
-//   16384 x 256 x 512 in 32 parts (fp32: 64) 29, 39 and 54; 4096 x 2 of 4 of 512 x 512 in 4 (8) 23, 30 and 35
+//   in more parts, 1 / 4 / 16 / 64 / 256: bf16 16384 x 16 x 64 220 / 61 / 22.5 / 12.2* / 13.1, 16384 x 100 x 512
+//   223 / 62 / 23.6 / 15.9* / 31; fp32 the same two 804 / 207 / 59 / 21.1* / 15.1 and 813 / 209 / 60 / 25.7* / 31
 constexpr int kGradCus = 256;
 
 struct GradChoice {

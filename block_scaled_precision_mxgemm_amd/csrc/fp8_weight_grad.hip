@@ -518,13 +518,24 @@ __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2))) void
   Grad<IN, T, GATHER>::run(a, tiles_k, tiles_n, splits);
 }
 
-// dW = sum over the splits, in their order.
+// dW = sum over the splits: each of 4 waves adds every fourth one for 256 elements, 8
+// of them on their way at once (2048 x 16 x 64 in 32 parts: 8.6 us with the products, 19.6
+// with one after the other; 16384 x 16 x 64 in 64 parts 11.9, 34.3).
 __global__ __launch_bounds__(256) void fp8_weight_grad_sum_kernel(const float* part, int splits, int64_t n, void* dW,
                                                                   int type) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
-  v4f s = *reinterpret_cast<const v4f*>(part + i);
-  for (int z = 1; z < splits; z++) s += *reinterpret_cast<const v4f*>(part + z * n + i);
+  __shared__ __attribute__((aligned(16))) v4f sums[3][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t i = ((int64_t)blockIdx.x * 64 + lane) * 4;
+  v4f s = {0, 0, 0, 0};
+  if (i < n) {
+#pragma unroll 8
+    for (int z = wave; z < splits; z += 4) s += *reinterpret_cast<const v4f*>(part + z * n + i);
+  }
+  if (wave > 0) sums[wave - 1][lane] = s;
+  __syncthreads();
+  if (wave > 0 || i >= n) return;
+#pragma unroll
+  for (int w = 0; w < 3; w++) s += sums[w][lane];
   store_columns<false>(Epi{(uint8_t*)dW + i * epi_elem_bytes(type), nullptr, type, kActNone}, 4, 0, 0, s);
 }
 
@@ -552,7 +563,7 @@ hipError_t launch_in(const F8GradArgs& a, hipStream_t stream) {
   hipError_t e = launch_tiles<IN, Small>(a, c.splits, stream);
   if (e != hipSuccess || c.splits == 1) return e;
   const int64_t n = (int64_t)a.E * a.N * a.K;
-  hipLaunchKernelGGL(fp8_weight_grad_sum_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, stream,
+  hipLaunchKernelGGL(fp8_weight_grad_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
                      (const float*)a.workspace, c.splits, n, a.dW, a.out_type);
   return hipGetLastError();
 }
