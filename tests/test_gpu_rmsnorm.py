@@ -309,7 +309,7 @@ def test_binding_refusals():
             call()
 
 
-@pytest.mark.parametrize("rows,K", [(64, 256), (33, 4096), (9, 8192), (5, 16416), (3, 131072)])
+@pytest.mark.parametrize("rows,K", [(64, 256), (33, 4096), (9, 8192), (6, 8208), (5, 14336), (4, 16384), (5, 16416), (3, 131072)])
 @pytest.mark.parametrize("kind", [1, 2])
 def test_rstd_and_y_are_rounded_once(rows, K, kind):
     """16-bit rows: the sum of the squares is exact in 64 bits up to 2^-52 a term of it,
