@@ -30,6 +30,15 @@ namespace mxg {
 //   1024 x 8 of 64 of 2048 x 4096                  616    343    280     231     201     167*
 //   2048 x 4 of 16 of 4096 x 2048                  685    313    151     123     144     125
 //   4096 x 4 of 16 of 4096 x 2048                 1325    600    301     237     236     197*
+// and 64x128, in a run of its own with some of the others beside it:
+//                                  32x64    deep 128x128 256x128  64x128
+//   256 x 4096 x 4096               21.0*   36.2    36.8    55.0    22.8
+//   512 x 4096 x 4096               36.9    34.2    36.2    49.5    22.6*
+//   1000 x 2000 x 8192              61.0    56.6    68.2    87.3    38.7*
+//   1024 x 4096 x 4096              66.5    33.2*   36.9    47.2    33.8
+//   777 x 4100 x 2064               35.0    18.6*   19.3    23.1    20.3
+//   500 x 2 of 4 of 2048 x 2048     28.3    21.8*   25.1    33.9    21.9
+//   1000 x 2 of 4 of 1024 x 4096    39.4    38.2*   41.3    55.9    30.0
 struct F8Variant {
   int bm, bn, per_cu;
   double us, extra;
@@ -37,8 +46,9 @@ struct F8Variant {
 // the order is that of the launches in gemm_fp8.hip
 constexpr F8Variant kF8Variants[] = {
     {16, 16, 2, 0.22, 1.8},   {16, 32, 2, 0.22, 1.8},   {32, 32, 1, 0.19, 2.4},   {32, 64, 2, 0.48, 1.5},
-    {128, 128, 1, 0.72, 4.0}, {128, 128, 2, 1.26, 4.5}, {256, 128, 1, 1.17, 4.0}, {256, 256, 1, 1.85, 7.5}};
-constexpr int kF8VariantCount = 8;
+    {128, 128, 1, 0.72, 4.0}, {128, 128, 2, 1.26, 4.5}, {256, 128, 1, 1.17, 4.0}, {256, 256, 1, 1.85, 7.5},
+    {64, 128, 2, 0.80, 3.0}};
+constexpr int kF8VariantCount = 9;
 
 constexpr int kCus = 256;
 constexpr double kBytesPerUs = 5.2e6;

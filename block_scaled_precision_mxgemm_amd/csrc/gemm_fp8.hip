@@ -819,6 +819,8 @@ using Tile128x128 = F8Cfg<128, 128, 2, 2, 2>;
 using Tile128x128Deep = F8Cfg<128, 128, 4, 2, 4>;
 using Tile256x128 = F8Cfg<256, 128, 4, 2, 3>;
 using Tile256x256 = F8Cfg<256, 256, 4, 2, 2, true>;
+// where tiles of 128 x 128 are too few for all CUs
+using Tile64x128 = F8Cfg<64, 128, 2, 2, 3>;
 
 // variant V of kF8Variants
 template <int V, class T>
@@ -863,8 +865,10 @@ hipError_t launch_fp8(const F8Args& args, hipStream_t stream) {
       return launch_variant<5, Tile128x128>(a, stream);
     case 6:
       return launch_variant<6, Tile256x128>(a, stream);
-    default:
+    case 7:
       return launch_variant<7, Tile256x256>(a, stream);
+    default:
+      return launch_variant<8, Tile64x128>(a, stream);
   }
 }
 
