@@ -459,9 +459,12 @@ struct F8Ring {
       }
       // the slot of the last block, which all have read
       uint8_t* cst = smem + (at.a == 0 ? T::D - 1 : at.a - 1) * T::STEP_A + wave * 4096;
-      if (t.rows != T::BM || (t.tn + 1) * T::BN > a.N)
-        store<-1, 0>(a, t, acc, cst, wm, wn);
-      else if (a.e.act == kActGelu)
+      if (t.rows != T::BM || (t.tn + 1) * T::BN > a.N) {
+        if (a.e.out == kOutF32)
+          store<-1, 0>(a, t, acc, cst, wm, wn);
+        else
+          store16<-1, 0>(a, t, acc, cst, wm, wn);
+      } else if (a.e.act == kActGelu)
         store_typed<kActGelu>(a, t, acc, cst, wm, wn);
       else
         store_typed<kActNone>(a, t, acc, cst, wm, wn);
@@ -545,19 +548,24 @@ struct F8Ring {
     }
   }
 
-  // The same for whole tiles of 16-bit results: bias, activation and rounding first,
-  // so that 32 rows x 64 columns go through the 4 KiB at once and come back 8
-  // columns a lane (half the LDS bytes, barriers and stores).
+  // The same for 16-bit results: bias, activation and rounding first, so that 32 rows x
+  // 64 columns go through the 4 KiB at once and come back 8 columns a lane (half the
+  // LDS bytes, barriers and stores).
   template <int OUT, int ACT>
   static __device__ __forceinline__ void store16(const F8Args& a, const ExpertTile& t, v4f (&acc)[FM][FN], uint8_t* cst,
                                                  int wm, int wn) {
+    constexpr bool FULL = OUT >= 0;
+    const bool bf16 = FULL ? OUT == kOutBF16 : a.e.out == kOutBF16, act = FULL ? ACT == kActGelu : a.e.act == kActGelu;
     const int lane = opaque(threadIdx.x & 63);
     const int rr = lane >> 4, cc = lane & 15;
     const int64_t eb = (int64_t)t.expert * a.N;
     const int n0 = t.tn * T::BN + wn * T::TN;
     bool out[FM];  // rows of A that do not exist
 #pragma unroll
-    for (int u = 0; u < FM; u++) out[u] = GATHER && a_row(a, t.row0 + wm * T::TM + 16 * u + cc) < 0;
+    for (int u = 0; u < FM; u++) {
+      const int row = wm * T::TM + 16 * u + cc;
+      out[u] = GATHER && (FULL || row < t.rows) && a_row(a, t.row0 + row) < 0;
+    }
 #pragma unroll
     for (int h = 0; h < T::TN / 64; h++) {
       v4f bias[4];
@@ -565,8 +573,13 @@ struct F8Ring {
       for (int j = 0; j < 4; j++) {
         // -0 leaves every sum as it is
         bias[j] = v4f{-0.f, -0.f, -0.f, -0.f};
-        if (a.e.bias != nullptr)
-          bias[j] = *reinterpret_cast<const v4f_any*>(a.e.bias + eb + n0 + h * 64 + j * 16 + rr * 4);
+        if (a.e.bias != nullptr) {
+          const int n = n0 + h * 64 + j * 16 + rr * 4;
+          if (FULL)
+            bias[j] = *reinterpret_cast<const v4f_any*>(a.e.bias + eb + n);
+          else
+            bias[j] = load_columns(a.e.bias + eb, n, a.N, 0.0f);
+        }
       }
       // the next tile's first copies are older than these loads: none of them
       // is in flight behind this, and the stores are not waited for with them
@@ -582,10 +595,10 @@ struct F8Ring {
 #pragma unroll
             for (int x = 0; x < 4; x++) {
               if (GATHER) v[x] = out[u] ? __builtin_nanf("") : v[x];
-              if (ACT == kActGelu) v[x] = gelu(v[x]);
+              if (act) v[x] = gelu(v[x]);
               // fp32 values first (no conversion fused with GELU's last product)
-              if (OUT == kOutF16) asm("" : "+v"(v[x]));
-              b[x] = OUT == kOutBF16 ? bf16_bits(v[x]) : f16_bits(v[x]);
+              if (OUT != kOutBF16) asm("" : "+v"(v[x]));
+              b[x] = bf16 ? bf16_bits(v[x]) : f16_bits(v[x]);
             }
             const int chunk = 2 * j + (rr >> 1);
             *reinterpret_cast<v2i*>(cst + (u - u0) * 2048 + cc * 128 + ((chunk ^ (cc & 7)) << 4) + (rr & 1) * 8) =
@@ -598,8 +611,15 @@ struct F8Ring {
           const int row = q * 8 + (lane >> 3), chunk = lane & 7;
           const v4i v = *reinterpret_cast<const v4i*>(cst + row * 128 + ((chunk ^ (row & 7)) << 4));
           const int64_t m = t.row0 + wm * T::TM + 16 * u0 + row;
-          __builtin_nontemporal_store(
-              (v4i_any)v, reinterpret_cast<v4i_any*>((uint16_t*)a.e.C + m * a.N + n0 + h * 64 + chunk * 8));
+          const int n = n0 + h * 64 + chunk * 8;
+          uint16_t* const to = (uint16_t*)a.e.C + m * a.N + n;
+          if (FULL || (wm * T::TM + 16 * u0 + row < t.rows && n + 8 <= a.N)) {
+            __builtin_nontemporal_store((v4i_any)v, reinterpret_cast<v4i_any*>(to));
+          } else if (wm * T::TM + 16 * u0 + row < t.rows) {
+#pragma unroll
+            for (int x = 0; x < 7; x++)
+              if (n + x < a.N) to[x] = (uint16_t)(v[x >> 1] >> 16 * (x & 1));
+          }
         }
         wave_sync();
       }
