@@ -10,23 +10,24 @@ namespace mxg {
 // the workgroups that run at once, us per block of 128 k with the chip full
 // (seven tenths of it where a variant that fits twice on a CU has it for
 // itself), and what a tile costs besides; and as no less than the weights'
-// time from memory.  The smallest estimate is taken, the first of equal ones.
+// time from memory.  The smallest estimate is taken; of equal ones 16 x 32, which
+// where memory bounds both is the faster one beside 16 x 16, then the first.
 // The constants are measured; what the choice is worth, in us (bf16 output,
 // operands from memory, calls of one captured graph; dense M x N x K, or tokens
 // x choices of experts of N x K; * what is taken).
 //                                  16x16  16x32  32x32  32x64   deep 128x128 256x128 256x256
 //   16 x 4096 x 4096                 7.0*   7.8    8.5   13.0   23.5    27.5    31.7    55.1
-//   16 x 28672 x 8192               65.6   49.7*  56.6   49.8   58.5    73.1    65.2     109
-//   32 x 28672 x 8192                122   68.1   62.5   53.2*  55.9    73.1    64.7     109
-//   64 x 4096 x 14336               57.6   32.8   25.4*  38.1   79.3     115    97.8     182
-//   256 x 4096 x 4096               72.4   31.8   27.4   18.4*  25.8    29.1    38.1    58.1
-//   1024 x 4096 x 4096               282    114    102   60.8   27.1*   31.7    38.1    60.2
-//   777 x 4100 x 2064                156   65.4   60.7   35.3   19.0*   20.2    24.4    38.5
-//   512 x 14336 x 4096               520    215    192    115   66.5    54.2*   54.3    67.7
+//   16 x 28672 x 8192               51.1   49.7*  56.6   49.8   58.5    73.1    65.2     109
+//   32 x 28672 x 8192               85.5   68.1   62.5   53.2*  55.9    73.1    64.7     109
+//   64 x 4096 x 14336               41.1   32.8   25.4*  38.1   79.3     115    97.8     182
+//   256 x 4096 x 4096               43.1   31.8   27.4   18.4*  25.8    29.1    38.1    58.1
+//   1024 x 4096 x 4096               159    114    102   60.8   27.1*   31.7    38.1    60.2
+//   777 x 4100 x 2064               88.0   65.4   60.7   35.3   19.0*   20.2    24.4    38.5
+//   512 x 14336 x 4096               298    215    192    115   66.5    54.2*   54.3    67.7
 //   2048 x 4096 x 4096                                    117   49.3    40.2    42.0*   60.9
 //   8192 x 14336 x 4096                                  1609    758     601     584     466*
-//   16 x 4 of 64 of 2048 x 4096      148   73.5*  97.2   81.0   95.8     107     110     128
-//   256 x 4 of 64 of 2048 x 4096     299    140    152    115*   138     150     158     152
+//   16 x 4 of 64 of 2048 x 4096     90.2   73.5*  97.2   81.0   95.8     107     110     128
+//   256 x 4 of 64 of 2048 x 4096     195    140    152    115*   138     150     158     152
 //   1024 x 8 of 64 of 2048 x 4096                  616    343    280     231     201     167*
 //   2048 x 4 of 16 of 4096 x 2048                  685    313    151     123     144     125
 //   4096 x 4 of 16 of 4096 x 2048                 1325    600    301     237     236     197*
@@ -39,13 +40,21 @@ namespace mxg {
 //   777 x 4100 x 2064               35.0    18.6*   19.3    23.1    20.3
 //   500 x 2 of 4 of 2048 x 2048     28.3    21.8*   25.1    33.9    21.9
 //   1000 x 2 of 4 of 1024 x 4096    39.4    38.2*   41.3    55.9    30.0
+// and few rows over experts, where the estimates are at the weights' time:
+//                                  16x16  16x32  32x32  32x64  64x128
+//   1 x 8 of 32 of 4096 x 4096      37.8   27.2*   38.2   27.8   29.6
+//   4 x 4 of 32 of 4096 x 4096      52.7   40.8*   59.2   43.5   41.5
+//   2 x 4 of 64 of 2048 x 4096      22.6   17.7*   22.8   18.9   27.2
+//   8 x 4 of 64 of 2048 x 4096      52.9   40.7*   59.5   43.3   41.7
+//   4 x 8 of 128 of 1024 x 2048     24.1   17.5*   25.5   16.1   17.8
+//   2 x 2 of 8 of 14336 x 4096      60.5   48.6*   65.0   49.0   48.0
 struct F8Variant {
   int bm, bn, per_cu;
   double us, extra;
 };
 // the order is that of the launches in gemm_fp8.hip
 constexpr F8Variant kF8Variants[] = {
-    {16, 16, 2, 0.22, 1.8},   {16, 32, 2, 0.22, 1.8},   {32, 32, 1, 0.19, 2.4},   {32, 64, 2, 0.48, 1.5},
+    {16, 16, 2, 0.21, 1.8},   {16, 32, 2, 0.22, 1.8},   {32, 32, 1, 0.19, 2.4},   {32, 64, 2, 0.48, 1.5},
     {128, 128, 1, 0.72, 4.0}, {128, 128, 2, 1.26, 4.5}, {256, 128, 1, 1.17, 4.0}, {256, 256, 1, 1.85, 7.5},
     {64, 128, 2, 0.80, 3.0}};
 constexpr int kF8VariantCount = 9;
@@ -69,11 +78,11 @@ inline double f8_estimate(const F8Variant& v, int64_t M, int64_t N, int64_t K, i
   return t > floor ? t : floor;
 }
 
-// Index of the variant with the smallest estimate, the first of equal ones.
+// Index of the variant with the smallest estimate; of equal ones 16 x 32, then the first.
 inline int f8_choice(int64_t M, int64_t N, int64_t K, int64_t E) {
-  int best = 0;
-  double least = f8_estimate(kF8Variants[0], M, N, K, E);
-  for (int v = 1; v < kF8VariantCount; v++) {
+  int best = 1;
+  double least = f8_estimate(kF8Variants[1], M, N, K, E);
+  for (int v = 0; v < kF8VariantCount; v++) {
     const double t = f8_estimate(kF8Variants[v], M, N, K, E);
     if (t < least) {
       best = v;
