@@ -154,8 +154,12 @@ __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_kernel(NormArgs a) {
   // y = (h rstd) w 46.  8192 x 4096 takes 41.6 us instead of 39.1, 8192 x 8192 92.5
   // instead of 91.9.
   const double exact = 1.0 / sqrt(row_sum<L>(sum, part) / a.K + (double)a.eps);
-  const float rstd = (float)exact, rest = rstd <= 3.0e38f ? (float)(exact - (double)rstd) : 0.0f;
-  if (a.rstd != nullptr && tid == 0) a.rstd[row] = rstd;
+  if (a.rstd != nullptr && tid == 0) a.rstd[row] = (float)exact;
+  // Where that is no fp32 value or one of few bits (eps = 0 and rows below 2^-127, rows above
+  // 2^126), h is multiplied by its power of two first, exactly.
+  const int shift = __builtin_amdgcn_readfirstlane(exact >= 0x1p-100 && exact <= 0x1p100 ? 0 : __builtin_amdgcn_frexp_exp(exact));
+  const double scaled = ldexp(exact, -shift);
+  const float rstd = (float)scaled, rest = (float)(scaled - (double)rstd);
 
   // y of step u (zeros past the row's end)
   const v4i* from = a.R != nullptr ? h : x;
@@ -168,6 +172,10 @@ __global__ __launch_bounds__(norm_threads(L)) void rmsnorm_kernel(NormArgs a) {
       else
         unpack16<IN>(from[i], y);
       load_weights<VEC>(a.W, a.w_type, i * VEC, w);
+      if (shift != 0) {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) y[j] = ldexpf(y[j], shift);
+      }
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
         const float p = y[j] * rstd;

@@ -643,7 +643,9 @@ int fp8gemm_weight_grad_grouped(const void *dC, int c_type, int64_t rows,
  *   Y      device, rows x K of `type`, 16-byte aligned (written), or NULL
  *   Q, S   device, Q rows x K bytes, 16-byte aligned, S 4-byte aligned (MXFP8:
  *          any); NULL for MXG_QUANT_NONE, which takes a Y
- *   rstd   device, rows fp32, 4-byte aligned (written), or NULL
+ *   rstd   device, rows fp32, 4-byte aligned (written), or NULL; an infinity where it is
+ *          beyond fp32's range (eps = 0 and a row below 2^-128: Y and the codes are those
+ *          of the real one; rmsnorm_backward takes rstd as it is)
  * Returns MXG_OK or an error status.  Deterministic.
  */
 int rmsnorm_quantize(const void *X, const void *R, int type, const void *W,
