@@ -512,7 +512,7 @@ __global__ __launch_bounds__(T::NW * 64) void int8_few_kernel(I8Args a, int tile
   const int cw = wave % CW, kw = wave / CW;
   const int g = lane >> 4, r = lane & 15;
   I8Tile t;
-  if (!find_tile(a, T::BM, tiles_n, blockIdx.x, lane, t)) return;
+  if (!find_tile(a, T::BM, tiles_n, (int64_t)blockIdx.y * gridDim.x + blockIdx.x, lane, t)) return;
   const int K = a.K, n0 = t.tn * T::BN, cols = min(T::BN, a.N - n0);
   const int S = (K + 127) >> 7, tail = K & 127;  // slices
   const int I = (S + KW - 1) / KW;               // stages
@@ -625,7 +625,9 @@ hipError_t launch_few(const I8Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
   const int64_t tiles = tiles_n * expert_tiles_m(a, T::BM);
   if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)tiles), block(T::NW * 64);
+  // in two dimensions: a launch has less than 2^32 threads in one
+  const int64_t most = 1 << 20;
+  const dim3 grid((unsigned)(tiles < most ? tiles : most), (unsigned)((tiles + most - 1) / most)), block(T::NW * 64);
   if (a.index != nullptr)
     hipLaunchKernelGGL((int8_few_kernel<T, true>), grid, block, 0, stream, a, (int)tiles_n);
   else

@@ -1,5 +1,8 @@
 """Products by expert of so many few-row tiles that their grid takes its second dimension
 (more than 2^20 of them), every result compared bit for bit."""
+import ctypes
+import os
+
 import pytest
 import torch
 
@@ -50,4 +53,29 @@ def test_fp8(gather):
         for n in range(0, N, N // 4):
             to = slice(n, n + N // 4)
             want = x[at] @ ref.dequantize(b[e, to], b_s[e, n // 128:(n + N // 4) // 128], 128).t()
+            assert torch.equal(got[at, to].double(), want), (e, n)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+def test_int8(gather):
+    say("int8 tiles in two dimensions", gather)
+    lib = ctypes.CDLL(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libint8_choice.so"))
+    lib.int8_choice.argtypes = [ctypes.c_int64] * 4
+    v = lib.int8_choice(M, N, K, E)
+    assert v < 2 and tiles(16, (16, 32)[v]) > 1 << 20
+    g = gen(22)
+    a = torch.randint(-8, 9, (M, K), generator=g, device=DEV).to(torch.int8)
+    b = torch.randint(0, 17, (E, N, K), generator=g, device=DEV, dtype=torch.uint8).view(torch.int8).sub_(8)
+    a_s = torch.exp2(torch.randint(-2, 3, (M,), generator=g, device=DEV).float())
+    b_s = torch.exp2(torch.randint(-2, 3, (E, N), generator=g, device=DEV).float())
+    expert, off = plan(g)
+    index = torch.randperm(M, generator=g, device=DEV).int() if gather else None
+    got = binding().int8gemm_run_grouped(a, a_s, b, b_s, off, index=index)
+    rows = torch.arange(M, device=DEV) if index is None else index.long()
+    x = (a.double() * a_s.double()[:, None])[rows]
+    for e in expert.unique().tolist():
+        at = expert == e
+        for n in range(0, N, N // 4):
+            to = slice(n, n + N // 4)
+            want = x[at] @ (b[e, to].double() * b_s[e, to].double()[:, None]).t()
             assert torch.equal(got[at, to].double(), want), (e, n)
