@@ -73,6 +73,7 @@ _BINDING_NAMES = (
     "QUANT_FP8",
     "QUANT_FP8_POW2",
     "QUANT_MXFP8",
+    "GRAD_ANY_SCALE",
     "library_path",
 )
 

@@ -161,13 +161,15 @@ int run_fp8(const mxg::F8Args& a, const float* bias, int act, int out_type, hipS
 }
 
 int run_fp8_grad(const mxg::F8GradArgs& a, int c_type, hipStream_t st) {
+  const bool any_scale = c_type >= 0 && (c_type & MXG_GRAD_ANY_SCALE) != 0;
+  if (any_scale) c_type -= MXG_GRAD_ANY_SCALE;
   if (!a.dY || !a.A || !a.SA || !a.dW || !type_ok(c_type) || !type_ok(a.out_type)) return MXG_EINVAL;
   if (mxg::fp8_weight_grad_bytes(a.M, a.N, a.K, a.E) > 0 && !a.workspace) return MXG_EINVAL;
   if (!aligned16(a.dY) || !aligned16(a.A) || !aligned16(a.dW) || !aligned16(a.workspace)) return MXG_EALIGN;
   if (!aligned4(a.SA) || !aligned4(a.offsets) || !aligned4(a.index)) return MXG_EALIGN;
   const int s = check_device();
   if (s != MXG_OK) return s;
-  return to_status(mxg::launch_fp8_weight_grad(a, c_type, st));
+  return to_status(mxg::launch_fp8_weight_grad(a, c_type, any_scale, st));
 }
 
 bool norm_dims_ok(int64_t rows, int64_t K) {

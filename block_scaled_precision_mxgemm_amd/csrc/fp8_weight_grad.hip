@@ -9,6 +9,16 @@
 // fp16 is taken as the sum of two bf16 values (TERMS = 2), its nearest one and that of
 // the rest (11 bits are 8 and 3), in fp32 as that of three (24 bits).
 //
+// ANY: scales of any kind, in fp32.  A tile of 128 columns of codes has one scale a row, so
+// that it goes with dY instead: fl32(dY s) as three bf16 values, against the codes as they
+// are: the MFMAs of dY in fp32 on tiles of 128 x 128, whatever dY's type.  In us, by powers
+// of two / others rounded / others in fp32 (dY in bf16; fp16; fp32):
+//   8192 x 4096 x 4096             227 / 250 / 1209   455 / 552 / 1188   719 / 802 / 1170
+//   2047 x 4100 x 2064            67.2 / 70.9 / 266   118 / 140 / 258    183 / 203 / 269
+//   512 x 4096 x 4096            29.7 / 31.1 / 87.3  43.4 / 46.4 / 84.7  57.7 / 63.3 / 87.2
+//   4096 x 4 of 16 of 4096 x 2048  322 / 347 / 1333                      828 / 897 / 1347
+// (of normal data the rounding is 2^-9.2 of the result, root mean square).
+//
 // Both operands are contracted over their rows, so that a lane's 8 elements of
 // an MFMA operand are a column of LDS: ds_read_b64_tr_b16 reads 4 rows of 16
 // columns and hands each lane a column.  Which of the 32 rows of a step an
@@ -80,9 +90,11 @@ struct GradCfg {
   static_assert(CX * NT * 16 == MS * BK && CY * NT * 8 == MS * BN && FN >= 2, "pieces split evenly");
 };
 
-template <int IN, class T, bool GATHER>
+template <int IN, class T, bool GATHER, bool ANY>
 struct Grad {
   static constexpr int FK = T::FK, FN = T::FN, TERMS = T::TERMS, COLS = FN * TERMS;
+  static_assert(!ANY || (T::BK == 128 && TERMS == 3), "a scale a row, products of it in fp32");
+  static constexpr int ROWS = T::CX + (ANY ? T::CY : 0);  // rows of A that a thread looks up for a slice
   static constexpr int kMS = T::MS;
   static constexpr int VY = IN == kOutF32 ? 2 : 1;  // registers of 16 bytes of a piece of dY
 
@@ -92,6 +104,7 @@ struct Grad {
     float s[T::CX];
     int bad;  // bit u: the row of x[u] is outside A
     v4i y[T::CY][VY];
+    float sy[T::CY];  // ANY: the scales of these rows
   };
   struct Tile {
     int e, k0, n0;
@@ -123,11 +136,27 @@ struct Grad {
     return w;
   }
 
-  static __device__ __forceinline__ void load_index(const F8GradArgs& a, const Tile& t, int m, int (&at)[T::CX]) {
+  static __device__ __forceinline__ void load_index(const F8GradArgs& a, const Tile& t, int m, int (&at)[ROWS]) {
     if constexpr (GATHER) {
 #pragma unroll
       for (int u = 0; u < T::CX; u++)
         at[u] = a.index[min(m + (int)threadIdx.x / (T::BK / 16) + u * ROWS_X, t.m1 - 1)];
+      if constexpr (ANY) {
+#pragma unroll
+        for (int u = 0; u < T::CY; u++)
+          at[T::CX + u] = a.index[min(m + (int)threadIdx.x / (T::BN / 8) + u * ROWS_Y, t.m1 - 1)];
+      }
+    }
+  }
+  // ANY: the scales of dY's rows in the tile's block of columns (rows past m1 take the last one's)
+  static __device__ __forceinline__ void load_scales(const F8GradArgs& a, const Tile& t, int m, const int (&at)[ROWS],
+                                                     Held& h) {
+#pragma unroll
+    for (int u = 0; u < T::CY; u++) {
+      int64_t row = min(m + opaque(threadIdx.x) / (T::BN / 8) + u * ROWS_Y, t.m1 - 1);
+      if constexpr (GATHER) row = row_of_index(a, at[T::CX + u]);
+      const float s = a.SA[max(row, (int64_t)0) * a.KB + (t.k0 >> 7)];
+      h.sy[u] = row < 0 ? __builtin_nanf("") : s;
     }
   }
 
@@ -137,7 +166,7 @@ struct Grad {
   // Else rows past m1 are fetched as the last one, and dY element by element.
   template <bool FULL>
   static __device__ __forceinline__ void load_slice(const F8GradArgs& a, const Tile& t, int m, const Place& w,
-                                                    const int (&at)[T::CX], Held& h) {
+                                                    const int (&at)[ROWS], Held& h) {
     using E = typename RowElem<IN>::type;
     const int most = t.m1 - 1 - m;
     h.bad = 0;
@@ -148,7 +177,7 @@ struct Grad {
         if (row < 0) h.bad |= 1 << u;
         row = max(row, (int64_t)0);
         h.x[u] = *reinterpret_cast<const v4i*>(a.A + row * a.K + w.x);
-        h.s[u] = a.SA[row * a.KB + w.s];
+        if constexpr (!ANY) h.s[u] = a.SA[row * a.KB + w.s];
       } else {
         uint32_t x = w.x, s = w.s;
         const uint8_t* from_x = a.A + (int64_t)m * a.K;
@@ -163,9 +192,10 @@ struct Grad {
           s += (uint32_t)(u * ROWS_X) * (uint32_t)a.KB - back * (uint32_t)a.KB;
         }
         h.x[u] = *reinterpret_cast<const v4i*>(from_x + x);
-        h.s[u] = from_s[s];
+        if constexpr (!ANY) h.s[u] = from_s[s];
       }
     }
+    if constexpr (ANY) load_scales(a, t, m, at, h);
     if constexpr (FULL) {
 #pragma unroll
       for (int u = 0; u < T::CY; u++) {
@@ -200,7 +230,7 @@ struct Grad {
     }
   }
   static __device__ __forceinline__ void load(const F8GradArgs& a, const Tile& t, int m, const Place& w,
-                                              const int (&at)[T::CX], Held& h) {
+                                              const int (&at)[ROWS], Held& h) {
     // a row more than the slice's: the last pieces of a row end up to BN - 1 columns behind it
     if (m + kMS <= t.m1 && ((a.M - m - (kMS - 1)) * a.N - t.n0 >= T::BN))
       load_slice<true>(a, t, m, w, at, h);
@@ -218,7 +248,8 @@ struct Grad {
     float s[T::CX];
 #pragma unroll
     for (int u = 0; u < T::CX; u++) {
-      s[u] = GATHER && (h.bad >> u & 1) ? __builtin_nanf("") : h.s[u];
+      // (ANY: a row outside A is NaN by dY's scale)
+      s[u] = ANY ? 1.0f : GATHER && (h.bad >> u & 1) ? __builtin_nanf("") : h.s[u];
       const uint32_t bits = __float_as_uint(s[u]);
       simple = simple && (bits & 0x7fffffu) == 0u && bits - 0x0d800000u <= 0x64000000u;
     }
@@ -256,6 +287,10 @@ struct Grad {
           for (int j = 0; j < 8; j++) f[j] = __int_as_float(h.y[u][j >> 2][j & 3]);
         } else {
           unpack16<IN>(h.y[u][0], f);
+        }
+        if constexpr (ANY) {
+#pragma unroll
+          for (int j = 0; j < 8; j++) f[j] *= h.sy[u];
         }
 #pragma unroll
         for (int j = 0; j < 4; j++) {
@@ -354,7 +389,7 @@ struct Grad {
     Tile t;
     find(blockIdx.x, t);
     Held h[2];
-    int at[T::CX];
+    int at[ROWS];
     Place w;
     // the lane's place in a fragment's rows; column f is at that ^ (f << 5)
     const int row = 4 * g + (i16 >> 2);
@@ -515,7 +550,12 @@ struct Grad {
 template <int IN, class T, bool GATHER>
 __global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2))) void fp8_weight_grad_kernel(
     F8GradArgs a, int tiles_k, int tiles_n, int splits) {
-  Grad<IN, T, GATHER>::run(a, tiles_k, tiles_n, splits);
+  Grad<IN, T, GATHER, false>::run(a, tiles_k, tiles_n, splits);
+}
+template <int IN, class T, bool GATHER>
+__global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2))) void fp8_weight_grad_any_kernel(
+    F8GradArgs a, int tiles_k, int tiles_n, int splits) {
+  Grad<IN, T, GATHER, true>::run(a, tiles_k, tiles_n, splits);
 }
 
 // dW = sum over the splits: each of 4 waves adds every fourth one for 256 elements, 8
@@ -539,33 +579,48 @@ __global__ __launch_bounds__(256) void fp8_weight_grad_sum_kernel(const float* p
   store_columns<false>(Epi{(uint8_t*)dW + i * epi_elem_bytes(type), nullptr, type, kActNone}, 4, 0, 0, s);
 }
 
-template <int IN, class T>
+template <int IN, class T, bool ANY>
 hipError_t launch_tiles(const F8GradArgs& a, int splits, hipStream_t stream) {
   const int tiles_n = (a.N + T::BN - 1) / T::BN, tiles_k = (a.K + T::BK - 1) / T::BK;
   const int64_t tiles = (int64_t)tiles_n * tiles_k * a.E * splits;
   if (tiles * T::NT > 0xffffffffll) return hipErrorInvalidConfiguration;  // threads of a launch
   const dim3 grid((unsigned)tiles), block(T::NT);
-  if (a.index != nullptr)
-    hipLaunchKernelGGL((fp8_weight_grad_kernel<IN, T, true>), grid, block, 0, stream, a, tiles_k, tiles_n, splits);
-  else
-    hipLaunchKernelGGL((fp8_weight_grad_kernel<IN, T, false>), grid, block, 0, stream, a, tiles_k, tiles_n, splits);
+  const bool gather = a.index != nullptr;
+  if constexpr (ANY) {
+    const auto kernel = gather ? fp8_weight_grad_any_kernel<IN, T, true> : fp8_weight_grad_any_kernel<IN, T, false>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, tiles_k, tiles_n, splits);
+  } else {
+    const auto kernel = gather ? fp8_weight_grad_kernel<IN, T, true> : fp8_weight_grad_kernel<IN, T, false>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, tiles_k, tiles_n, splits);
+  }
+  return hipGetLastError();
+}
+
+hipError_t add_parts(const F8GradArgs& a, int splits, hipStream_t stream) {
+  if (splits == 1) return hipSuccess;
+  const int64_t n = (int64_t)a.E * a.N * a.K;
+  hipLaunchKernelGGL(fp8_weight_grad_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
+                     (const float*)a.workspace, splits, n, a.dW, a.out_type);
   return hipGetLastError();
 }
 
 template <int IN>
-hipError_t launch_in(const F8GradArgs& a, hipStream_t stream) {
+hipError_t launch_in(const F8GradArgs& a, bool any_scale, hipStream_t stream) {
+  if (any_scale) {
+    // tiles of 128 x 128, in as many parts as the three terms of fp32 take (a workspace of theirs)
+    const GradChoice c = grad_choice(a.M, a.N, a.K, a.E, 3);
+    const int splits = c.large ? 1 : c.splits;
+    const hipError_t e = launch_tiles<IN, GradCfg<128, 128, 2, 2, 3, 32>, true>(a, splits, stream);
+    return e != hipSuccess ? e : add_parts(a, splits, stream);
+  }
   constexpr int TERMS = IN == kOutBF16 ? 1 : IN == kOutF16 ? 2 : 3;
   // (two workgroups a CU where dY is more than one term)
   using Large = typename std::conditional<TERMS == 1, GradCfg<256, 256, 4, 2, 1, 64>, GradCfg<256, 128, 4, 1, TERMS, 32>>::type;
   using Small = GradCfg<128, 128, 2, 2, TERMS, TERMS == 1 ? 64 : 32>;
   const GradChoice c = grad_choice(a.M, a.N, a.K, a.E, TERMS);
-  if (c.large) return launch_tiles<IN, Large>(a, 1, stream);
-  hipError_t e = launch_tiles<IN, Small>(a, c.splits, stream);
-  if (e != hipSuccess || c.splits == 1) return e;
-  const int64_t n = (int64_t)a.E * a.N * a.K;
-  hipLaunchKernelGGL(fp8_weight_grad_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
-                     (const float*)a.workspace, c.splits, n, a.dW, a.out_type);
-  return hipGetLastError();
+  if (c.large) return launch_tiles<IN, Large, false>(a, 1, stream);
+  const hipError_t e = launch_tiles<IN, Small, false>(a, c.splits, stream);
+  return e != hipSuccess ? e : add_parts(a, c.splits, stream);
 }
 
 }  // namespace
@@ -580,12 +635,12 @@ int64_t fp8_weight_grad_bytes(int64_t M, int64_t N, int64_t K, int64_t E) {
   return most;
 }
 
-hipError_t launch_fp8_weight_grad(const F8GradArgs& args, int y_type, hipStream_t stream) {
+hipError_t launch_fp8_weight_grad(const F8GradArgs& args, int y_type, bool any_scale, hipStream_t stream) {
   F8GradArgs a = args;
   set_division(a);
-  if (y_type == kOutF32) return launch_in<kOutF32>(a, stream);
-  if (y_type == kOutBF16) return launch_in<kOutBF16>(a, stream);
-  return launch_in<kOutF16>(a, stream);
+  if (y_type == kOutF32) return launch_in<kOutF32>(a, any_scale, stream);
+  if (y_type == kOutBF16) return launch_in<kOutBF16>(a, any_scale, stream);
+  return launch_in<kOutF16>(a, any_scale, stream);
 }
 
 }  // namespace mxg

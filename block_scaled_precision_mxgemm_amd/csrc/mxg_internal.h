@@ -96,7 +96,7 @@ struct F8GradArgs {
   void* workspace;
 };
 int64_t fp8_weight_grad_bytes(int64_t M, int64_t N, int64_t K, int64_t E);
-hipError_t launch_fp8_weight_grad(const F8GradArgs& a, int y_type, hipStream_t stream);
+hipError_t launch_fp8_weight_grad(const F8GradArgs& a, int y_type, bool any_scale, hipStream_t stream);
 
 constexpr int kQuantNone = 0;
 constexpr int kQuantInt8 = 1;

@@ -585,6 +585,13 @@ int fp8gemm_run_grouped(const uint8_t *A, const float *scaleA, int64_t rowsA,
  * fp8gemm_quantize and rmsnorm_quantize give with pow2).  Sums in fp32 on the
  * bf16 MFMA, rounded once to out_type; dC in fp16 or fp32 goes in as the sum of two
  * or of three bf16 values.
+ * For scales that are no powers of two the rounding of x moves dW by at most 2^-8 *
+ * sum |dC * x| (2^-9.2 of dW, root mean square, on normal data); an infinite scaleA, which
+ * no quantizer gives, makes what it enters infinite or NaN.
+ * With MXG_GRAD_ANY_SCALE or'ed to c_type scales of any kind are taken in fp32: dW[n][k] =
+ * sum_m fl32(dC[m][n] * scaleA[m][k / 128]) * A[m][k], the first factor as the sum of
+ * three bf16 values, which takes 1.1 (few rows, dC in fp32) to 5.3 (bf16, large sizes)
+ * times as long.
  * The gradient is that of the dequantized activations.
  *
  *   dC         device, M x N elements of c_type, 16-byte aligned
@@ -596,6 +603,7 @@ int fp8gemm_run_grouped(const uint8_t *A, const float *scaleA, int64_t rowsA,
  * Returns MXG_OK or an error status.  Deterministic.  The workspace's size is -1
  * for arguments that the call refuses.
  */
+#define MXG_GRAD_ANY_SCALE 16  /* or'ed to c_type */
 int64_t fp8gemm_weight_grad_workspace(int64_t M, int64_t N, int64_t K, int64_t E);
 int fp8gemm_weight_grad(const void *dC, int c_type, int64_t M, int64_t N,
                         const uint8_t *A, const float *scaleA, int64_t K,
