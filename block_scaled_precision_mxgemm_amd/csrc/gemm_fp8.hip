@@ -550,9 +550,13 @@ struct F8Ring {
     }
   }
 
-  // Where 16-bit rows do not start with a line, the caches join the stores of the largest
-  // tile to lines: 8000 x 2000 x 528 23.8 us, 28.4 past them (128 x 128 26.7 and 24.4).
-  static __device__ __forceinline__ bool joined(const F8Args& a) { return T::BN == 256 && (a.N & 63) != 0; }
+  // Where 16-bit rows do not start with half a line, the caches join the stores of the largest
+  // tile to lines, in us joined / past them: 8000 x 2000 x 528 23.8 / 28.4 (128 x 128 26.7 /
+  // 24.4), 8000 x 9992 x 528 106 / 116, 16384 x 4024 x 1040 119 / 127, 8192 x 9968 x 2064 216
+  // / 231; even from results of 400 MB on (16384 x 20008 x 1040 645 / 646, x 20016 620 / 595).
+  // Rows that start with half a line are joined by memory: 8000 x 9952 x 528 94.1 / 85.5,
+  // 16384 x 20000 x 528 389 / 319, 8192 x 14368 x 2064 327 / 313.
+  static __device__ __forceinline__ bool joined(const F8Args& a) { return T::BN == 256 && (a.N & 31) != 0; }
 
   // The same for 16-bit results: bias, activation and rounding first, so that 32 rows x
   // 64 columns go through the 4 KiB at once and come back 8 columns a lane (half the
