@@ -16,3 +16,19 @@ def test_few_rows_over_many_experts(rows, N, K, E):
 def test_few_rows_and_columns(M, N, K):
     """Where 16 x 32 leaves CUs without a tile, 16 x 16 is the faster one."""
     assert large.load_choice()(M, N, K) == "16x16"
+
+
+def test_gradient_cases_take_every_form_in_three_terms():
+    """dY in fp32, which is three terms: large tiles, small ones, and rows in parts."""
+    import ctypes
+    import os
+
+    import test_gpu_fp8_grad as grad
+
+    lib = ctypes.CDLL(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libfp8_choice.so"))
+    lib.fp8_grad_choice.argtypes = [ctypes.c_int64] * 4 + [ctypes.c_int]
+    taken = {lib.fp8_grad_choice(M, N, K, 1, 3) for M, N, K in grad.SIZES}
+    assert {0, 1} <= taken and len(taken) >= 4
+    rows = len(grad.COUNTS)
+    assert lib.fp8_grad_choice(sum(grad.COUNTS), 2020, 992, rows, 3) == 0
+    assert lib.fp8_grad_choice(sum(grad.COUNTS), 300, 400, rows, 3) >= 1
