@@ -25,7 +25,7 @@ namespace mxg {
 //   777 x 4100 x 2064               88.0   65.4   60.7   35.3   19.0*   20.2    24.4    38.5
 //   512 x 14336 x 4096               298    215    192    115   66.5    54.2*   54.3    67.7
 //   2048 x 4096 x 4096                                    117   49.3    40.2    42.0*   60.9
-//   8192 x 14336 x 4096                                  1609    758     601     584     466*
+//   8192 x 14336 x 4096                                  1609    758     601     584     443*
 //   16 x 4 of 64 of 2048 x 4096     90.2   73.5*  97.2   81.0   95.8     107     110     128
 //   256 x 4 of 64 of 2048 x 4096     195    140    152    115*   138     150     158     152
 //   1024 x 8 of 64 of 2048 x 4096                  616    343    280     231     201     167*

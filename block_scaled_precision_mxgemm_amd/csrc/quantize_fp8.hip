@@ -130,7 +130,7 @@ hipError_t quantize_in(const void* X, int64_t E, int64_t rows, int64_t K, int bl
   while (((int64_t)1 << s) < KB) s++;
   div.mul = (uint32_t)(((uint64_t)1 << (31 + s)) / (uint32_t)KB + 1);
   div.shift = 31 + s;
-  // fewer than 2^30 blocks and a grid of fewer than 2^32 threads in a launch
+  // at most 2^26 blocks in a launch: their numbers are 32-bit, its threads fewer than 2^32
   constexpr int per = 256 / (kBlock / RowElem<IN>::VEC) * kUnroll;
   const int64_t all = E * rows, most = ((int64_t)1 << 26) / KB;
   for (int64_t r = 0; r < all; r += most) {
